@@ -1,6 +1,7 @@
 """Gated delta rule (GDN-2 / Gated DeltaNet / DeltaNet) on AMD MI355X (gfx950).
 
-The computation lives in libgdn.so (C ABI, include/gdn.h), built from the HIP
+The computation lives in libgdn.so (C ABI, include/gdn.h and, for the
+softmax-attention layers of hybrids, include/gdn_attn.h), built from the HIP
 sources under csrc/.  This package holds the thin ctypes binding only.
 """
 from .gdn import (  # noqa: F401
@@ -11,4 +12,9 @@ from .gdn import (  # noqa: F401
     gdn_backward_varlen, gdn_backward_varlen_saved, gdn_backward_workspace_size, gdn_chunk_fwd,
     gdn_chunk_fwd_gated, gdn_chunk_fwd_save, gdn_chunk_fwd_varlen, gdn_chunk_fwd_varlen_save, gdn_decode_step, gdn_gates, gdn_output_gate, gdn_short_conv, lib,
     status_string,
+)
+from .attn import (  # noqa: F401
+    GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED, GdnAttnDecodeDesc, GdnAttnPrefillDesc, GdnKvAppendDesc, GdnQkDesc,
+    attn_abi_version, gdn_attn_decode, gdn_attn_decode_workspace_size, gdn_attn_prefill,
+    gdn_kv_append, gdn_qk_norm_rope,
 )

@@ -23,7 +23,8 @@ LIB_CHECK = os.path.join(PKG, "libgdn_check.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["gdn_api.cpp", "decode.hip", "chunk_fwd.hip", "chunk_fwd_sb.hip", "layer_ops.hip",
-           "backward.hip", "noalloc.hip"]
+           "backward.hip", "noalloc.hip", "attn_api.cpp", "attn_rope.hip", "attn_prefill.hip",
+           "attn_decode.hip"]
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -1,0 +1,86 @@
+// attn_device.hpp -- device helpers of the attention kernels: packed-sequence
+// lookup, 8-element chunks kept as loaded, reductions over lanes.
+#pragma once
+
+#include "attn_index.hpp"
+#include "attn_kernels.hpp"
+#include "gdn_device.hpp"
+
+#include <type_traits>
+
+namespace gdn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Item idx of packed offsets (find_packed_by): the wave probes 64 sequences at
+// a time and every lane gets the answer.
+__device__ __forceinline__ PackedItem find_packed(const int64_t* __restrict__ cu, int64_t N,
+                                                  int64_t total, int unit, int extra,
+                                                  int64_t idx) {
+  const int lane = threadIdx.x & 63;
+  return find_packed_by(cu, N, total, unit, extra, idx, [&](int64_t lo, int64_t step, int64_t hi) {
+    const int64_t i = lo + lane * step;
+    return (uint64_t)__ballot(i < hi && packed_at_or_before(cu, i, total, unit, extra, idx));
+  });
+}
+
+// 8 consecutive elements kept as loaded, so that many rows are in flight at
+// the cost of 4 (bf16) or 8 (fp32) registers each.
+template <typename T> struct Chunk8;
+template <> struct Chunk8<bf16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const bf16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void unpack(float* out) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      out[2 * i] = __uint_as_float(w[i] << 16);
+      out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Chunk8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void unpack(float* out) const {
+    out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
+    out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ void store8(bf16* p, const float* v) {
+  typedef __bf16 bf16x8s __attribute__((ext_vector_type(8)));
+  bf16x8s h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = (bf16)v[i];
+  *reinterpret_cast<bf16x8s*>(p) = h;
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// Sum over the L consecutive lanes (4 or 8, aligned) that hold one row.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float s) {
+  static_assert(L == 4 || L == 8, "lanes of a row");
+  auto dpp = [](float v, auto ctrl) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+        0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  s += dpp(s, std::integral_constant<int, 0xB1>{});   // quad_perm [1,0,3,2]
+  s += dpp(s, std::integral_constant<int, 0x4E>{});   // quad_perm [2,3,0,1]
+  if constexpr (L == 8) s += dpp(s, std::integral_constant<int, 0x141>{});  // row_half_mirror
+  return s;
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor(x, off));
+  return x;
+}
+
+}  // namespace gdn

@@ -1,0 +1,97 @@
+// attn_index.hpp -- which rows, pages and tokens a workgroup of the attention
+// kernels touches, from offsets, lengths and page tables that live on the
+// device and may hold anything.  Plain C++, so that the bounds can be checked
+// on the host too.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __HIP__
+#include <hip/hip_runtime.h>
+#define GDN_HD __host__ __device__ __forceinline__
+#else
+#define GDN_HD inline
+#endif
+
+namespace gdn {
+
+GDN_HD int64_t clamp_i64(int64_t x, int64_t lo, int64_t hi) {
+  return x < lo ? lo : (x > hi ? hi : x);
+}
+
+// Packed offsets: sequence n owns the work items from floor(cu[n] / unit) +
+// extra n onwards, so a sequence of L tokens has at least floor(L / unit) +
+// extra of them, and all sequences together at most total / unit + extra N.
+// The item `idx` is number `item` of sequence n, whose tokens are [start, end)
+// (within [0, total]).  For malformed offsets n is some sequence, and item may
+// be negative or end before start.
+struct PackedItem {
+  int64_t n, item, start, end;
+};
+// mask(lo, step, hi): bit i is set where lo + i step < hi and that sequence's
+// first item is at or before idx (i < 64).
+template <typename Mask>
+GDN_HD PackedItem find_packed_by(const int64_t* cu, int64_t N, int64_t total, int unit, int extra,
+                                 int64_t idx, Mask mask) {
+  int64_t lo = 0, hi = N;
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 63) >> 6;
+    const uint64_t m = mask(lo, step, hi);
+    lo += m ? (63 - __builtin_clzll(m)) * step : 0;
+    hi = lo + step < hi ? lo + step : hi;
+  }
+  PackedItem r;
+  r.n = lo;
+  r.start = clamp_i64(cu[lo], 0, total);
+  r.end = clamp_i64(cu[lo + 1], 0, total);
+  r.item = idx - (r.start / unit + extra * lo);
+  return r;
+}
+GDN_HD bool packed_at_or_before(const int64_t* cu, int64_t n, int64_t total, int unit, int extra,
+                                int64_t idx) {
+  return clamp_i64(cu[n], 0, total) / unit + extra * n <= idx;
+}
+
+// New rows [kept, stop) of the j-th page that L new tokens (rows a .. a + L of
+// the input) touch behind seq_len held ones; none when kept >= stop.
+struct AppendPage {
+  int64_t pi;     // page of the sequence: index into its row of the table
+  int64_t tok0;   // input row of the page's row 0 (meaningful from `kept` on)
+  int kept, stop;
+};
+GDN_HD AppendPage append_page(int64_t seq_len, int64_t max_pages, int P, int64_t j, int64_t a,
+                              int64_t L) {
+  AppendPage r{0, 0, 0, 0};
+  if (j < 0 || L <= 0) return r;
+  const int64_t cap = max_pages * P;
+  const int64_t s = clamp_i64(seq_len, 0, cap);
+  r.pi = s / P + j;
+  int64_t end = s + L < cap ? s + L : cap;
+  if (end > (r.pi + 1) * P) end = (r.pi + 1) * P;
+  const int64_t first = s > r.pi * P ? s : r.pi * P;
+  if (first >= end) return r;
+  r.tok0 = a + (r.pi * P - s);
+  r.kept = (int)(first - r.pi * P);
+  r.stop = (int)(end - r.pi * P);
+  return r;
+}
+
+// Tokens [lo, len) that a decode step sees, and split `split`'s [begin, end)
+// of them, where splits start at multiples of `step`.
+struct DecodeSpan {
+  int64_t len, lo, begin, end;
+  bool only;      // one split sees everything
+};
+GDN_HD DecodeSpan decode_span(int64_t seq_len, int64_t max_pages, int P, int64_t window,
+                              int64_t split, int64_t span, int step) {
+  DecodeSpan r;
+  r.len = clamp_i64(seq_len, 0, max_pages * P);
+  r.lo = window && r.len > window ? r.len - window : 0;
+  const int64_t first = r.lo / step * step;
+  r.begin = first + split * span;
+  r.end = r.begin + span < r.len ? r.begin + span : r.len;
+  r.only = first + span >= r.len;
+  return r;
+}
+
+}  // namespace gdn

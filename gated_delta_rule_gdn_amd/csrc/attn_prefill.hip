@@ -1,0 +1,363 @@
+// attn_prefill.hip -- causal softmax attention over packed prompts with
+// grouped heads on gfx950, full or in a sliding window:
+//
+//   o_t = sum_s p_ts v_s / sum_s p_ts,   p_ts = exp(scale * q_t . k_s - m_t)
+//
+// in one pass over the keys with a running maximum m and sum for each query.
+//
+// Both kernels put the queries on the columns of the products,
+//   S^T [tokens x queries] = K Q^T,    O^T [d x queries] += V^T P^T,
+// so that a lane holds scores of one query only: the maximum and the sum are
+// reduced in registers and across 2 (or 4) lanes, and the weights are, as they
+// lie in the score accumulators, the k-values this lane supplies to the second
+// product.  No weight crosses lanes or LDS.
+#include "attn_device.hpp"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kNone = -1e30f;           // running maximum (log2 units) before any token
+
+// One workgroup's query tile: queries [q0, q0 + BM) of the sequence that is
+// rows [a, a + L) of the packed tensors.
+struct Tile {
+  int64_t a, L, q0;
+  int hq;
+  bool valid;
+};
+
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const PrefillArgs& p, int64_t blk, int64_t blocks) {
+  Tile t;
+  t.hq = (int)(blk % p.Hq);
+  const int64_t slots = blocks / p.Hq;
+  const int64_t slot = slots - 1 - blk / p.Hq;      // late (long) tiles first
+  if (!p.cu_seqlens) {
+    const int64_t qt = slot / p.N, n = slot - qt * p.N;
+    t.a = n * p.Tseq;
+    t.L = p.Tseq;
+    t.q0 = qt * BM;
+  } else {
+    const PackedItem it = find_packed(p.cu_seqlens, p.N, p.total_T, BM, 1, slot);
+    t.a = it.start;
+    t.L = it.end - it.start;
+    t.q0 = it.item * BM;
+  }
+  t.valid = t.q0 >= 0 && t.q0 < t.L;
+  return t;
+}
+
+// ---------------------------------------------------------------------------
+// fp32: v_mfma_f32_16x16x4_f32, 16 queries to a wave, 64 to a workgroup, key
+// tiles of 32 tokens in LDS.
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ __launch_bounds__(kThreads) void prefill_f32_kernel(PrefillArgs p, int64_t blocks) {
+  constexpr int BM = 64, BN = 32, LD = D + 4, KB = D / 32, MT = D / 16;
+  __shared__ __align__(16) float s_k[BN * LD], s_v[BN * LD];
+  lds_nan_fill(s_k, sizeof s_k);
+  lds_nan_fill(s_v, sizeof s_v);
+  const Tile tl = find_tile<BM>(p, blockIdx.x, blocks);
+  if (!tl.valid) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, j = lane & 15;
+  const int hk = tl.hq / (p.Hq / p.Hk);
+  const int64_t q0 = tl.q0 + 16 * wave;     // the wave's first query
+  const int64_t tq = q0 + j;                // this lane's query
+  const float* kb_ = static_cast<const float*>(p.k) + tl.a * p.ld_k + hk * D;
+  const float* vb_ = static_cast<const float*>(p.v) + tl.a * p.ld_v + hk * D;
+
+  Frag8<float> q[KB];
+  {
+    const float flip = p.scale < 0.f ? -1.f : 1.f;
+    const int64_t row = tq < tl.L ? tq : tl.L - 1;
+    const float* qp = static_cast<const float*>(p.q) + (tl.a + row) * p.ld_q + tl.hq * D + 8 * g;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      load_f32<8, float>(qp + 32 * kb, q[kb].v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[kb].v[i] *= flip;
+    }
+  }
+  const float c_scale = fabsf(p.scale) * kLog2e;
+  f32x4 o[MT];
+#pragma unroll
+  for (int c = 0; c < MT; ++c) o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = kNone, l = 0.f;
+
+  int64_t lo = p.window ? tl.q0 - p.window + 1 : 0;   // first key that the tile sees
+  lo = lo < 0 ? 0 : lo / BN * BN;
+  const int64_t stop = tl.q0 + BM < tl.L ? tl.q0 + BM : tl.L;
+  for (int64_t k0 = lo; k0 < stop; k0 += BN) {
+    __syncthreads();
+    // rows past the sequence are zero: they may belong to another one
+    for (int e = tid; e < BN * D / 4; e += kThreads) {
+      const int row = e / (D / 4), c = 4 * (e % (D / 4));
+      float4 ku = make_float4(0.f, 0.f, 0.f, 0.f), vu = ku;
+      if (k0 + row < tl.L) {
+        ku = *reinterpret_cast<const float4*>(kb_ + (k0 + row) * p.ld_k + c);
+        vu = *reinterpret_cast<const float4*>(vb_ + (k0 + row) * p.ld_v + c);
+      }
+      lds_check(s_k + row * LD + c, 16);
+      *reinterpret_cast<float4*>(s_k + row * LD + c) = ku;
+      *reinterpret_cast<float4*>(s_v + row * LD + c) = vu;
+    }
+    __syncthreads();
+    if (k0 > q0 + 15 || (p.window && k0 + BN - 1 <= q0 - p.window)) continue;   // nothing seen
+    float x[2][4];
+    float mx = -__builtin_huge_valf();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        Frag8<float> a;
+        load_f32<8, float>(s_k + (16 * t + j) * LD + 32 * kb + 8 * g, a.v);
+        mma32(acc, a, q[kb]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t u = k0 + 16 * t + 4 * g + r;
+        const bool seen = u <= tq && (!p.window || u > tq - p.window);
+        x[t][r] = seen ? acc[r] * c_scale : -__builtin_huge_valf();
+        mx = fmaxf(mx, x[t][r]);
+      }
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float m_new = fmaxf(m, mx);
+    const float alpha = exp2_fast(m - m_new);
+    m = m_new;
+    l *= alpha;
+#pragma unroll
+    for (int c = 0; c < MT; ++c)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[c][r] *= alpha;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float e = exp2_fast(x[t][r] - m);
+        l += e;
+        const float* vr = s_v + (16 * t + 4 * g + r) * LD + j;
+#pragma unroll
+        for (int c = 0; c < MT; ++c)
+          o[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(vr[16 * c], e, o[c], 0, 0, 0);
+      }
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (tq >= tl.L) return;
+  const float inv = 1.f / l;                // a query sees itself: l > 0
+  float* op = static_cast<float*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * g;
+#pragma unroll
+  for (int c = 0; c < MT; ++c)
+    store4<float>(op + 16 * c, o[c][0] * inv, o[c][1] * inv, o[c][2] * inv, o[c][3] * inv);
+}
+
+// ---------------------------------------------------------------------------
+// bf16: v_mfma_f32_32x32x16_bf16, 32 queries to a wave, 128 to a workgroup,
+// key tiles of 64 tokens in LDS.
+//
+// Lane 32 h + i holds, of a 32 x 32 product, column i and rows
+// 8 a + 4 h + b (a, b = 0..3), and supplies 8 k-values.  The score tile's rows
+// of a 16-token block in a lane are tokens 4 h + b and 8 + 4 h + b, so V^T is
+// read with the same 8 tokens: two transposing LDS reads of 4 tokens each.
+//
+// LDS rows are D elements; the 16-byte chunks of a row are permuted so that
+// the lanes that read together fall on different banks (k_chunk: 16 rows at
+// one chunk; v_chunk: 4 rows at 4 neighbouring chunks).
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ int k_chunk(int row, int c) {
+  return D == 128 ? c ^ (row & 15) : c ^ ((row >> 1) & 7);
+}
+template <int D>
+__device__ __forceinline__ int v_chunk(int row, int c) {
+  return D == 128 ? c ^ ((row & 3) << 2) : c ^ (((row >> 1) & 1) << 2);
+}
+
+__device__ __forceinline__ bf16x4 read_tr16(const bf16* p) {
+  lds_check(p, 8);
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) v4s*)(p)));
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p, int64_t blocks) {
+  constexpr int BM = 128, BN = 64, KB = D / 16, MT = D / 32;
+  constexpr int CH = D / 8;                           // 16-byte chunks of a row
+  constexpr int NL = BN * CH / kThreads;              // chunks a thread stages
+  __shared__ __align__(16) bf16 s_k[BN * D], s_v[BN * D];
+  lds_nan_fill(s_k, sizeof s_k);
+  lds_nan_fill(s_v, sizeof s_v);
+  const Tile tl = find_tile<BM>(p, blockIdx.x, blocks);
+  if (!tl.valid) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, i32 = lane & 31;
+  const int hk = tl.hq / (p.Hq / p.Hk);
+  const int L = (int)tl.L;
+  const int q0 = (int)tl.q0 + 32 * wave;    // the wave's first query
+  const int tq = q0 + i32;                  // this lane's query
+  const bf16* kb_ = static_cast<const bf16*>(p.k) + tl.a * p.ld_k + hk * D;
+  const bf16* vb_ = static_cast<const bf16*>(p.v) + tl.a * p.ld_v + hk * D;
+
+  bf16x8 q[KB];
+  {
+    const int row = tq < L ? tq : L - 1;
+    const bf16* qp = static_cast<const bf16*>(p.q) + (tl.a + row) * p.ld_q + tl.hq * D + 8 * h;
+    const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;   // the scale below is positive
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      uint4 u = *reinterpret_cast<const uint4*>(qp + 16 * kb);
+      u.x ^= flip; u.y ^= flip; u.z ^= flip; u.w ^= flip;
+      q[kb] = __builtin_bit_cast(bf16x8, u);
+    }
+  }
+  const float c_scale = fabsf(p.scale) * kLog2e;
+  f32x16 o[MT];
+#pragma unroll
+  for (int c = 0; c < MT; ++c)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[c][r] = 0.f;
+  float m = kNone, l = 0.f;
+
+  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
+  int lo = window ? (int)tl.q0 - window + 1 : 0;      // first key that the tile sees
+  lo = lo < 0 ? 0 : lo / BN * BN;
+  const int stop = (int)tl.q0 + BM < L ? (int)tl.q0 + BM : L;
+
+  uint4 kr[NL], vr[NL];
+  auto load_tile = [&](int k0) {            // rows past the sequence are zero
+#pragma unroll
+    for (int e = 0; e < NL; ++e) {
+      const int ci = e * kThreads + tid, row = ci / CH, c = ci % CH;
+      kr[e] = vr[e] = make_uint4(0, 0, 0, 0);
+      if (k0 + row < L) {
+        kr[e] = *reinterpret_cast<const uint4*>(kb_ + (int64_t)(k0 + row) * p.ld_k + 8 * c);
+        vr[e] = *reinterpret_cast<const uint4*>(vb_ + (int64_t)(k0 + row) * p.ld_v + 8 * c);
+      }
+    }
+  };
+  load_tile(lo);
+  for (int k0 = lo; k0 < stop; k0 += BN) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < NL; ++e) {
+      const int ci = e * kThreads + tid, row = ci / CH, c = ci % CH;
+      bf16* dk = s_k + row * D + 8 * k_chunk<D>(row, c);
+      bf16* dv = s_v + row * D + 8 * v_chunk<D>(row, c);
+      lds_check(dk, 16);
+      lds_check(dv, 16);
+      *reinterpret_cast<uint4*>(dk) = kr[e];
+      *reinterpret_cast<uint4*>(dv) = vr[e];
+    }
+    __syncthreads();
+    if (k0 + BN < stop) load_tile(k0 + BN);
+    if (k0 > q0 + 31 || (window && k0 + BN - 1 <= q0 - window)) continue;   // nothing seen
+
+    f32x16 s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[t][r] = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const int row = 32 * t + i32;
+        const bf16* src = s_k + row * D + 8 * k_chunk<D>(row, 2 * kb + h);
+        lds_check(src, 16);
+        s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(src), q[kb],
+                                                       s[t], 0, 0, 0);
+      }
+    }
+    if (k0 + BN - 1 > q0 || (window && k0 <= q0 + 31 - window)) {   // some pairs are not seen
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int u = k0 + 32 * t + 8 * (r / 4) + 4 * h + r % 4;
+          const bool seen = u <= tq && (!window || u > tq - window);
+          if (!seen) s[t][r] = -__builtin_huge_valf();
+        }
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[t][r]);
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float m_new = fmaxf(m, mx * c_scale);
+    const float alpha = exp2_fast(m - m_new);
+    m = m_new;
+    l *= alpha;
+#pragma unroll
+    for (int c = 0; c < MT; ++c)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[c][r] *= alpha;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {           // 16-token blocks
+      bf16x8 w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e = exp2_fast(__builtin_fmaf(s[b / 2][8 * (b % 2) + i], c_scale, -m));
+        l += e;
+        w[i] = (bf16)e;
+      }
+#pragma unroll
+      for (int c = 0; c < MT; ++c) {
+        bf16x8 a;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int li = lane & 15;
+          const int row = 16 * b + 8 * half + 4 * h + (li >> 2);
+          const int col = 32 * c + 16 * ((lane >> 4) & 1) + 4 * (li & 3);
+          const bf16x4 u = read_tr16(s_v + row * D + 8 * v_chunk<D>(row, col / 8) + col % 8);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[4 * half + i] = u[i];
+        }
+        o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w, o[c], 0, 0, 0);
+      }
+    }
+  }
+  l += __shfl_xor(l, 32);
+  if (tq >= L) return;
+  const float inv = 1.f / l;                // a query sees itself: l > 0
+  bf16* op = static_cast<bf16*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * h;
+#pragma unroll
+  for (int c = 0; c < MT; ++c)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+      store4<bf16>(op + 32 * c + 2 * r, o[c][r] * inv, o[c][r + 1] * inv, o[c][r + 2] * inv,
+                   o[c][r + 3] * inv);
+}
+
+}  // namespace
+
+int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType io) {
+  const int64_t bm = io == DType::F32 ? 64 : 128;
+  return (packed ? total_T / bm + N : N * ((Tseq + bm - 1) / bm)) * Hq;
+}
+
+hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t stream) {
+  const int64_t blocks =
+      prefill_blocks(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, a.Hq, a.io);
+  const dim3 grid((unsigned)blocks);
+  if (a.io == DType::F32) {
+    if (a.d == 128) prefill_f32_kernel<128><<<grid, kThreads, 0, stream>>>(a, blocks);
+    else prefill_f32_kernel<64><<<grid, kThreads, 0, stream>>>(a, blocks);
+  } else {
+    if (a.d == 128) prefill_bf16_kernel<128><<<grid, kThreads, 0, stream>>>(a, blocks);
+    else prefill_bf16_kernel<64><<<grid, kThreads, 0, stream>>>(a, blocks);
+  }
+  return hipGetLastError();
+}
+
+#ifdef GDN_CHECK
+unsigned check_violations_attn_prefill() { return take_check_violations(); }
+#endif
+
+}  // namespace gdn

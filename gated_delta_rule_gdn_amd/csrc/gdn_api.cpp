@@ -12,9 +12,17 @@
 #include <cstdint>
 #include <cstdio>
 
+#include "api_common.hpp"
 #include "gdn_kernels.hpp"
 
 namespace {
+
+using gdn::Span;
+using gdn::aligned16;
+using gdn::dtype_bytes;
+using gdn::overlaps;
+using gdn::span;
+using gdn::to_dtype;
 
 // Status of a call whose launches returned e.  The debug build (-DGDN_CHECK)
 // also waits for the work to finish and reads the kernels' LDS-check
@@ -32,28 +40,6 @@ gdn_status launched(hipError_t e) {
 #endif
   return GDN_OK;
 }
-
-struct Span {
-  uintptr_t lo, hi;  // [lo, hi)
-  bool valid() const { return hi > lo; }
-};
-
-Span span(const void* p, int64_t elems, int64_t elem_bytes) {
-  Span s{0, 0};
-  if (p && elems > 0) {
-    s.lo = reinterpret_cast<uintptr_t>(p);
-    s.hi = s.lo + static_cast<uintptr_t>(elems * elem_bytes);
-  }
-  return s;
-}
-
-bool overlaps(const Span& a, const Span& b) {
-  return a.valid() && b.valid() && a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t dtype_bytes(int32_t d) { return d == GDN_F32 ? 4 : 2; }
 
 // Common shape/type checks shared by both entry points.
 gdn_status check_common(int32_t Hk, int32_t Hv, int32_t dk, int32_t dv, int32_t io,
@@ -74,8 +60,6 @@ gdn_status check_common(int32_t Hk, int32_t Hv, int32_t dk, int32_t dv, int32_t 
   if (!(gate == io || gate == GDN_F32)) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
-
-gdn::DType to_dtype(int32_t d) { return d == GDN_F32 ? gdn::DType::F32 : gdn::DType::BF16; }
 
 // Checks pointer presence, alignment and overlap.  `rows` is the number of
 // (token, head)-independent rows of the leading dims: B*T for the forward,
