@@ -6,12 +6,12 @@ goes to that device's current stream, or to the one given.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
+from torch._C import _cuda_getCurrentRawStream
 
-from .gdn import _DT, _ptr, GDN_OK, GdnError, lib
+from .gdn import _DT, GDN_OK, GdnError, lib
 
 GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
 ATTN_ABI_VERSION = 1
@@ -66,92 +66,94 @@ def attn_abi_version() -> int:
     return lib.gdn_attn_abi_version()
 
 
-def _dev(t, name) -> int:
+# A decode step's calls are so short that the host's share decides how fast they
+# follow each other, so each tensor is checked in one expression, and what is
+# wrong with it is found out only where that fails.
+
+def _refuse(t, name, dev, shape, dtype):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    return t.get_device()
-
-
-def _heads(t, name, dev, rows, H, d, dtype) -> int:
-    """A [rows, H, d] device tensor whose rows are dense (a column block of a
-    wider buffer is fine).  Returns its row stride in elements."""
-    _same(t, name, dev, dtype)
-    if t.shape != (rows, H, d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, H, d)}")
-    s = t.stride()
-    if s[2] != 1 or (H > 1 and s[1] != d):
-        if rows * H:
-            raise ValueError(f"{name} must have dense rows of {H} x {d} elements")
-    return s[0] if rows > 1 else H * d
-
-
-def _same(t, name, dev, dtype):
-    if not t.is_cuda or t.get_device() != dev:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the same device as the other tensors")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-
-
-def _dense(t, name, dev, shape, dtype):
-    _same(t, name, dev, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
+
+
+def _dense(t, name, dev, shape, dtype) -> int:
+    """The address of a contiguous tensor of this shape and type (None: 0)."""
+    if t is None:
+        return 0
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, dev, shape, dtype)
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _maybe(t, name, dev, shape, dtype):
-    if t is not None:
-        _dense(t, name, dev, shape, dtype)
+def _heads(t, name, dev, shape, dtype):
+    """The address and row stride (elements) of a [rows, H, d] tensor whose
+    rows are dense; a column block of a wider buffer is fine."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _refuse(t, name, dev, shape, dtype)
+    rows, H, d = shape
+    ld, sh, sd = t.stride()
+    if (sd != 1 or (sh != d and H > 1)) and rows * H:
+        raise ValueError(f"{name} must have dense rows of {H} x {d} elements")
+    return t.data_ptr(), ld if rows > 1 else H * d
 
 
-class _On:
-    """The device and stream of a call.  Outputs and workspaces that the call
-    allocates belong to that stream."""
-
-    def __init__(self, dev, stream):
-        self.dev = dev
-        self.given = stream
-        if stream is None:
-            self.raw = torch.cuda.current_stream(dev).cuda_stream
-        elif isinstance(stream, torch.cuda.Stream):
-            if stream.device.index != dev:
-                raise ValueError("stream is on another device than the tensors")
-            self.raw = stream.cuda_stream
-        else:
-            self.raw = int(stream)
-
-    def empty(self, shape, dtype):
-        device = torch.device("cuda", self.dev)
-        if self.given is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        s = self.given if isinstance(self.given, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(self.raw, device=device)
-        with torch.cuda.stream(s):
-            return torch.empty(shape, dtype=dtype, device=device)
-
-    def call(self, fn, name, *args):
-        guard = contextlib.nullcontext() if torch.cuda.current_device() == self.dev else \
-            torch.cuda.device(self.dev)
-        with guard:
-            st = fn(*args, self.raw)
-        if st != GDN_OK:
-            raise GdnError(st, name)
-
-
-def _io(t, name):
-    if t.dtype not in _DT:
+def _first(t, name):
+    """Device, dtype and shape of the [rows, H, d] tensor that sets those of a call."""
+    dev, io = t.get_device(), t.dtype
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if io not in _DT:
         raise ValueError(f"{name} must be float32 or bfloat16")
-    return t.dtype
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions (rows, heads, head size)")
+    return dev, io, t.shape
+
+
+def _raw_stream(stream, dev) -> int:
+    if stream is None:
+        return _cuda_getCurrentRawStream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise ValueError("stream is on another device than the tensors")
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _empty(shape, dtype, dev, stream):
+    """An output or workspace that belongs to the stream of the call."""
+    device = torch.device("cuda", dev)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call(fn, name, dev, *args):
+    if torch.cuda.current_device() == dev:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != GDN_OK:
+        raise GdnError(st, name)
 
 
 def _rope(inv_freq, dev):
+    """rope_dim and the address of the frequencies."""
     if inv_freq is None:
-        return 0
+        return 0, 0
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a 1-d tensor of rope_dim / 2 frequencies")
-    _dense(inv_freq, "inv_freq", dev, inv_freq.shape, torch.float32)
-    return 2 * inv_freq.shape[0]
+    p = _dense(inv_freq, "inv_freq", dev, inv_freq.shape, torch.float32)
+    return 2 * inv_freq.shape[0], p
 
 
 def gdn_qk_norm_rope(q_raw, k_raw=None, positions=None, inv_freq=None, q_weight=None,
@@ -169,72 +171,65 @@ def gdn_qk_norm_rope(q_raw, k_raw=None, positions=None, inv_freq=None, q_weight=
     one = q_raw if q_raw is not None else k_raw
     if one is None:
         raise ValueError("q_raw or k_raw must be given")
-    dev, io = _dev(one, "q_raw"), _io(one, "q_raw")
-    if one.dim() != 3:
-        raise ValueError("q_raw and k_raw must be [rows, H, d]")
-    rows, d = one.shape[0], one.shape[2]
-    on = _On(dev, stream)
-    Hq = Hk = ld_q = ld_k = 0
+    dev, io, (rows, _, d) = _first(one, "q_raw" if one is q_raw else "k_raw")
+    Hq = Hk = ld_q = ld_k = q_in = k_in = 0
     if q_raw is not None:
-        Hq = q_raw.shape[1]
-        ld_q = _heads(q_raw, "q_raw", dev, rows, Hq, d, io)
+        shape = q_raw.shape
+        Hq = shape[1]
+        q_in, ld_q = _heads(q_raw, "q_raw", dev, shape, io)
         if q is None:
-            q = on.empty((rows, Hq, d), io)
-        _dense(q, "q", dev, (rows, Hq, d), io)
+            q = _empty(shape, io, dev, stream)
     elif q is not None:
         raise ValueError("q without q_raw")
     if k_raw is not None:
-        if k_raw.dim() != 3:
-            raise ValueError("q_raw and k_raw must be [rows, H, d]")
-        Hk = k_raw.shape[1]
-        ld_k = _heads(k_raw, "k_raw", dev, rows, Hk, d, io)
+        Hk = k_raw.shape[1] if k_raw.dim() == 3 else 0
+        k_in, ld_k = _heads(k_raw, "k_raw", dev, (rows, Hk, d), io)
         if k is None:
-            k = on.empty((rows, Hk, d), io)
-        _dense(k, "k", dev, (rows, Hk, d), io)
+            k = _empty((rows, Hk, d), io, dev, stream)
     elif k is not None:
         raise ValueError("k without k_raw")
-    _maybe(q_weight, "q_weight", dev, (d,), torch.float32)
-    _maybe(k_weight, "k_weight", dev, (d,), torch.float32)
     if inv_freq is not None and positions is None:
         raise ValueError("rotation needs positions")
-    rope = _rope(inv_freq, dev)
-    _maybe(positions, "positions", dev, (rows,), torch.int64)
+    rope, freqs = _rope(inv_freq, dev)
+    pos = _dense(positions, "positions", dev, (rows,), torch.int64)
     desc = GdnQkDesc(rows, ld_q, ld_k, Hq, Hk, d, rope,
                      GDN_ROPE_INTERLEAVED if interleaved else GDN_ROPE_HALF, _DT[io], rope_scale,
                      eps)
-    on.call(lib.gdn_qk_norm_rope, "gdn_qk_norm_rope", ctypes.byref(desc), _ptr(q_raw),
-            _ptr(k_raw), _ptr(q_weight), _ptr(k_weight), _ptr(positions) if rope else None,
-            _ptr(inv_freq) if rope else None, _ptr(q), _ptr(k))
+    _call(lib.gdn_qk_norm_rope, "gdn_qk_norm_rope", dev, ctypes.byref(desc), q_in, k_in,
+          _dense(q_weight, "q_weight", dev, (d,), torch.float32),
+          _dense(k_weight, "k_weight", dev, (d,), torch.float32), pos if rope else 0,
+          freqs if rope else 0, _dense(q, "q", dev, (rows, Hq, d), io),
+          _dense(k, "k", dev, (rows, Hk, d), io), _raw_stream(stream, dev))
     return q, k
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, dev):
-    """(num_pages, H_k, page_size, d, N, max_pages) of a paged cache."""
+    """(shape of the cache, shape of the table, addresses) of a paged cache."""
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_pages, H_k, page_size, d]")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [N, max_pages]")
-    shape = k_cache.shape
-    _dense(k_cache, "k_cache", dev, shape, torch.float8_e4m3fn)
-    _dense(v_cache, "v_cache", dev, shape, torch.float8_e4m3fn)
-    _dense(k_scale, "k_scale", dev, shape[:2], torch.float32)
-    _dense(v_scale, "v_scale", dev, shape[:2], torch.float32)
-    _dense(page_table, "page_table", dev, page_table.shape, torch.int32)
-    _dense(seq_lens, "seq_lens", dev, page_table.shape[:1], torch.int64)
-    return (*shape, *page_table.shape)
+    shape, table = k_cache.shape, page_table.shape
+    scales = shape[:2]
+    return shape, table, (
+        _dense(k_cache, "k_cache", dev, shape, torch.float8_e4m3fn),
+        _dense(v_cache, "v_cache", dev, shape, torch.float8_e4m3fn),
+        _dense(k_scale, "k_scale", dev, scales, torch.float32),
+        _dense(v_scale, "v_scale", dev, scales, torch.float32),
+        _dense(page_table, "page_table", dev, table, torch.int32),
+        _dense(seq_lens, "seq_lens", dev, table[:1], torch.int64))
 
 
 def _packed(cu_seqlens, N, dev):
-    """Number of sequences of a packed or equal-length batch."""
+    """Number of sequences of a packed or equal-length batch, and the offsets' address."""
     if cu_seqlens is None:
-        return 1 if N is None else N
+        return 1 if N is None else N, 0
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be a 1-d tensor of N + 1 offsets")
     n = cu_seqlens.shape[0] - 1
     if N is not None and N != n:
         raise ValueError(f"cu_seqlens has {n + 1} offsets, expected N + 1 = {N + 1}")
-    _dense(cu_seqlens, "cu_seqlens", dev, (n + 1,), torch.int64)
-    return n
+    return n, _dense(cu_seqlens, "cu_seqlens", dev, (n + 1,), torch.int64)
 
 
 def gdn_kv_append(k_raw, v_raw, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
@@ -249,23 +244,19 @@ def gdn_kv_append(k_raw, v_raw, k_cache, v_cache, k_scale, v_scale, page_table, 
     tokens held before the call (not changed); cu_seqlens int64 [N + 1] or
     None for total_T / N new tokens each.
     """
-    dev, io = _dev(k_raw, "k_raw"), _io(k_raw, "k_raw")
-    pages, Hk, P, d, N, width = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
-                                       dev)
-    T = k_raw.shape[0]
-    ld_k = _heads(k_raw, "k_raw", dev, T, Hk, d, io)
-    ld_v = _heads(v_raw, "v_raw", dev, T, Hk, d, io)
-    _packed(cu_seqlens, N, dev)
-    _maybe(k_weight, "k_weight", dev, (d,), torch.float32)
-    rope = _rope(inv_freq, dev)
+    dev, io, (T, _, _) = _first(k_raw, "k_raw")
+    (pages, Hk, P, d), (N, width), (kc, vc, ks, vs, table, lens) = _cache(
+        k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, dev)
+    k_in, ld_k = _heads(k_raw, "k_raw", dev, (T, Hk, d), io)
+    v_in, ld_v = _heads(v_raw, "v_raw", dev, (T, Hk, d), io)
+    cu = _packed(cu_seqlens, N, dev)[1]
+    rope, freqs = _rope(inv_freq, dev)
     desc = GdnKvAppendDesc(N, T, ld_k, ld_v, pages, width, Hk, d, P, rope,
                            GDN_ROPE_INTERLEAVED if interleaved else GDN_ROPE_HALF, _DT[io],
                            rope_scale, eps)
-    _On(dev, stream).call(
-        lib.gdn_kv_append, "gdn_kv_append", ctypes.byref(desc), _ptr(cu_seqlens), _ptr(seq_lens),
-        _ptr(page_table), _ptr(k_raw), _ptr(v_raw), _ptr(k_weight),
-        _ptr(inv_freq) if rope else None, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-        _ptr(v_scale))
+    _call(lib.gdn_kv_append, "gdn_kv_append", dev, ctypes.byref(desc), cu, lens, table, k_in, v_in,
+          _dense(k_weight, "k_weight", dev, (d,), torch.float32), freqs if rope else 0, kc, vc, ks,
+          vs, _raw_stream(stream, dev))
 
 
 def gdn_attn_prefill(q, k, v, cu_seqlens=None, N=None, window: int = 0, scale=None, o=None,
@@ -277,37 +268,31 @@ def gdn_attn_prefill(q, k, v, cu_seqlens=None, N=None, window: int = 0, scale=No
     defaults to 1); window 0 (all) or the number of tokens seen; scale
     defaults to 1 / sqrt(d).  o [total_T, H_q, d] is allocated when not given.
     """
-    dev, io = _dev(q, "q"), _io(q, "q")
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q and k must be [total_T, H, d]")
-    T, Hq, d = q.shape
+    dev, io, (T, Hq, d) = _first(q, "q")
+    if k.dim() != 3:
+        raise ValueError("k must be [total_T, H_k, d]")
     Hk = k.shape[1]
-    ld_q = _heads(q, "q", dev, T, Hq, d, io)
-    ld_k = _heads(k, "k", dev, T, Hk, d, io)
-    ld_v = _heads(v, "v", dev, T, Hk, d, io)
-    N = _packed(cu_seqlens, N, dev)
-    on = _On(dev, stream)
+    q_in, ld_q = _heads(q, "q", dev, (T, Hq, d), io)
+    k_in, ld_k = _heads(k, "k", dev, (T, Hk, d), io)
+    v_in, ld_v = _heads(v, "v", dev, (T, Hk, d), io)
+    N, cu = _packed(cu_seqlens, N, dev)
     if o is None:
-        o = on.empty((T, Hq, d), io)
-    _dense(o, "o", dev, (T, Hq, d), io)
+        o = _empty((T, Hq, d), io, dev, stream)
     desc = GdnAttnPrefillDesc(N, T, ld_q, ld_k, ld_v, window, Hq, Hk, d, _DT[io],
                               d ** -0.5 if scale is None else scale)
-    on.call(lib.gdn_attn_prefill, "gdn_attn_prefill", ctypes.byref(desc), _ptr(cu_seqlens),
-            _ptr(q), _ptr(k), _ptr(v), _ptr(o))
+    _call(lib.gdn_attn_prefill, "gdn_attn_prefill", dev, ctypes.byref(desc), cu, q_in, k_in, v_in,
+          _dense(o, "o", dev, (T, Hq, d), io), _raw_stream(stream, dev))
     return o
-
-
-def _decode_desc(q, k_cache, page_table, window, scale):
-    N, Hq, d = q.shape
-    pages, Hk, P = k_cache.shape[:3]
-    return GdnAttnDecodeDesc(N, pages, page_table.shape[1], window, Hq, Hk, d, P, _DT[_io(q, "q")],
-                             d ** -0.5 if scale is None else scale)
 
 
 def gdn_attn_decode_workspace_size(q, k_cache, page_table, window: int = 0) -> int:
     """Workspace bytes gdn_attn_decode needs for these shapes (0: none)."""
-    return int(lib.gdn_attn_decode_workspace_size(
-        ctypes.byref(_decode_desc(q, k_cache, page_table, window, None))))
+    N, Hq, d = q.shape
+    pages, Hk, P = k_cache.shape[:3]
+    if q.dtype not in _DT:
+        raise ValueError("q must be float32 or bfloat16")
+    desc = GdnAttnDecodeDesc(N, pages, page_table.shape[1], window, Hq, Hk, d, P, _DT[q.dtype], 1.0)
+    return int(lib.gdn_attn_decode_workspace_size(ctypes.byref(desc)))
 
 
 def gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, window: int = 0,
@@ -321,26 +306,24 @@ def gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
     of at least gdn_attn_decode_workspace_size(...) bytes; it and o are
     allocated when not given.
     """
-    dev, io = _dev(q, "q"), _io(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [N, H_q, d]")
-    _, Hk, _, d, N, _ = _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, dev)
-    Hq = q.shape[1]
-    _dense(q, "q", dev, (N, Hq, d), io)
-    on = _On(dev, stream)
+    dev, io, shape = _first(q, "q")
+    (pages, Hk, P, d), (N, width), cache = _cache(k_cache, v_cache, k_scale, v_scale, page_table,
+                                                  seq_lens, dev)
+    Hq = shape[1]
+    q_in = _dense(q, "q", dev, (N, Hq, d), io)
     if o is None:
-        o = on.empty((N, Hq, d), io)
-    _dense(o, "o", dev, (N, Hq, d), io)
-    desc = _decode_desc(q, k_cache, page_table, window, scale)
-    need = lib.gdn_attn_decode_workspace_size(ctypes.byref(desc))
-    nbytes = 0
+        o = _empty(shape, io, dev, stream)
+    desc = GdnAttnDecodeDesc(N, pages, width, window, Hq, Hk, d, P, _DT[io],
+                             d ** -0.5 if scale is None else scale)
+    ref = ctypes.byref(desc)
+    need = lib.gdn_attn_decode_workspace_size(ref)
+    ws = nbytes = 0
     if need:
         if workspace is None:
-            workspace = on.empty((need,), torch.uint8)
-        if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+            workspace = _empty((need,), torch.uint8, dev, stream)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the device of the others")
-        nbytes = workspace.numel() * workspace.element_size()
-    on.call(lib.gdn_attn_decode, "gdn_attn_decode", ctypes.byref(desc), _ptr(q), _ptr(k_cache),
-            _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(seq_lens), _ptr(o),
-            _ptr(workspace) if need else None, nbytes)
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(lib.gdn_attn_decode, "gdn_attn_decode", dev, ref, q_in, *cache,
+          _dense(o, "o", dev, shape, io), ws, nbytes, _raw_stream(stream, dev))
     return o

@@ -553,7 +553,7 @@ def test_binding_refusals():
         gdn.gdn_attn_prefill(x, x, x.float())
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         gdn.gdn_attn_prefill(x.half(), x.half(), x.half())
-    with pytest.raises(ValueError, match="same device"):
+    with pytest.raises(ValueError, match="device tensor"):
         gdn.gdn_attn_prefill(x, x.cpu(), x)
     with pytest.raises(ValueError, match="shape"):
         gdn.gdn_attn_prefill(x, x, x[:3])
