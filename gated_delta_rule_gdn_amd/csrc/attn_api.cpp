@@ -50,7 +50,7 @@ gdn_status check_head(int32_t d, int32_t io) {
 gdn_status check_rows(int64_t rows, int64_t ld, int32_t H, int32_t d) {
   const int64_t cols = (int64_t)H * d;
   if (cols > (int64_t(1) << 22)) return GDN_ERR_UNSUPPORTED;
-  if (ld < cols || ld % 8 != 0 || ld >= (int64_t(1) << 31)) return GDN_ERR_INVALID_ARG;
+  if (ld < cols || ld % 8 != 0 || ld > (int64_t(1) << 24)) return GDN_ERR_INVALID_ARG;
   if ((double)rows * (double)ld > kMaxElems) return GDN_ERR_INVALID_ARG;
   return GDN_OK;
 }

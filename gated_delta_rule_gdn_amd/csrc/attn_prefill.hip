@@ -186,12 +186,51 @@ __device__ __forceinline__ bf16x4 read_tr16(const bf16* p) {
       (__attribute__((address_space(3))) v4s*)(p)));
 }
 
+// 16 bytes for each lane from base + voff + soff straight into LDS at
+// lds + 16 * lane (lds is the same for the wave).  The load is counted by
+// vmcnt like any other; the compiler does not know of it, so wait_tiles()
+// stands before the barrier behind which the bytes are read.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void load_lds16(uint32_t lds, i32x4 base, uint32_t voff, uint32_t soff) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      ::"s"(lds), "v"(voff), "s"(base), "s"(soff) : "memory");
+#endif
+}
+// This wave's loads have landed and its LDS reads are done; then all waves'.
+__device__ __forceinline__ void wait_tiles() {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#endif
+}
+__device__ __forceinline__ i32x4 buffer_at(const void* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  i32x4 r;
+  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+  r[1] = __builtin_amdgcn_readfirstlane((int)((u >> 32) & 0xffff));
+  r[2] = -1;                              // offsets are kept in range by the caller
+  r[3] = 0x00027000;
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+
+// The loop over key tiles is pipelined by hand: while the weights of tile i
+// are formed (VALU), the scores of tile i + 1 are on the matrix cores, and
+// while the maximum of tile i + 1 is formed, tile i's product with V is.  K
+// runs one tile ahead of V; both are double-buffered in LDS and loaded one
+// iteration before they are read, with one barrier to an iteration.
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p, int64_t blocks) {
   constexpr int BM = 128, BN = 64, KB = D / 16, MT = D / 32;
   constexpr int CH = D / 8;                           // 16-byte chunks of a row
-  constexpr int NL = BN * CH / kThreads;              // chunks a thread stages
-  __shared__ __align__(16) bf16 s_k[BN * D], s_v[BN * D];
+  constexpr int NL = BN * CH / kThreads;              // chunks a thread loads of a tile
+  constexpr int RL = kThreads / CH;                   // rows of one such load
+  __shared__ __align__(16) bf16 s_k[2][BN * D], s_v[2][BN * D];
   lds_nan_fill(s_k, sizeof s_k);
   lds_nan_fill(s_v, sizeof s_v);
   const Tile tl = find_tile<BM>(p, blockIdx.x, blocks);
@@ -200,8 +239,9 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, i32 = lane & 31;
   const int hk = tl.hq / (p.Hq / p.Hk);
-  const int L = (int)tl.L;
-  const int q0 = (int)tl.q0 + 32 * wave;    // the wave's first query
+  const int L = __builtin_amdgcn_readfirstlane((int)tl.L);
+  const int qt0 = __builtin_amdgcn_readfirstlane((int)tl.q0);
+  const int q0 = qt0 + 32 * wave;           // the wave's first query
   const int tq = q0 + i32;                  // this lane's query
   const bf16* kb_ = static_cast<const bf16*>(p.k) + tl.a * p.ld_k + hk * D;
   const bf16* vb_ = static_cast<const bf16*>(p.v) + tl.a * p.ld_v + hk * D;
@@ -227,53 +267,73 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p
   float m = kNone, l = 0.f;
 
   const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
-  int lo = window ? (int)tl.q0 - window + 1 : 0;      // first key that the tile sees
+  int lo = window ? qt0 - window + 1 : 0;             // first key that the tile sees
   lo = lo < 0 ? 0 : lo / BN * BN;
-  const int stop = (int)tl.q0 + BM < L ? (int)tl.q0 + BM : L;
+  const int stop = qt0 + BM < L ? qt0 + BM : L;
+  const int mine = q0 + 32 < stop ? q0 + 32 : stop;   // this wave needs keys before it
 
-  uint4 kr[NL], vr[NL];
-  auto load_tile = [&](int k0) {            // rows past the sequence are zero
+  // loads of one tile: row r0 + e RL, permuted so that LDS position pc of row r
+  // gets chunk k_chunk(r, pc); rows past the sequence repeat its last one
+  // (their scores are masked), so nothing of another sequence is read
+  const int r0 = tid / CH, pc = tid % CH;
+  const uint32_t ck = 16 * k_chunk<D>(r0, pc), cv = 16 * v_chunk<D>(r0, pc);
+  const uint32_t lk2 = (uint32_t)p.ld_k * 2, lv2 = (uint32_t)p.ld_v * 2;
+  const uint32_t wave_lds = (uint32_t)wave * 1024;
+  auto load_tile = [&](const bf16* base, int64_t ld, uint32_t ld2, uint32_t chunk, const bf16* dst,
+                       int k0) {
+    const i32x4 rs = buffer_at(base + k0 * ld);
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(dst)) + wave_lds;
+    if (k0 + BN <= L) {
+      const uint32_t voff = (uint32_t)r0 * ld2 + chunk;
 #pragma unroll
-    for (int e = 0; e < NL; ++e) {
-      const int ci = e * kThreads + tid, row = ci / CH, c = ci % CH;
-      kr[e] = vr[e] = make_uint4(0, 0, 0, 0);
-      if (k0 + row < L) {
-        kr[e] = *reinterpret_cast<const uint4*>(kb_ + (int64_t)(k0 + row) * p.ld_k + 8 * c);
-        vr[e] = *reinterpret_cast<const uint4*>(vb_ + (int64_t)(k0 + row) * p.ld_v + 8 * c);
+      for (int e = 0; e < NL; ++e) load_lds16(at + e * 4096, rs, voff, (uint32_t)(e * RL) * ld2);
+    } else {
+#pragma unroll
+      for (int e = 0; e < NL; ++e) {
+        const int row = r0 + e * RL < L - k0 ? r0 + e * RL : L - 1 - k0;
+        load_lds16(at + e * 4096, rs, (uint32_t)row * ld2 + chunk, 0);
       }
     }
   };
-  load_tile(lo);
-  for (int k0 = lo; k0 < stop; k0 += BN) {
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < NL; ++e) {
-      const int ci = e * kThreads + tid, row = ci / CH, c = ci % CH;
-      bf16* dk = s_k + row * D + 8 * k_chunk<D>(row, c);
-      bf16* dv = s_v + row * D + 8 * v_chunk<D>(row, c);
-      lds_check(dk, 16);
-      lds_check(dv, 16);
-      *reinterpret_cast<uint4*>(dk) = kr[e];
-      *reinterpret_cast<uint4*>(dv) = vr[e];
-    }
-    __syncthreads();
-    if (k0 + BN < stop) load_tile(k0 + BN);
-    if (k0 > q0 + 31 || (window && k0 + BN - 1 <= q0 - window)) continue;   // nothing seen
 
-    f32x16 s[2];
+  auto scores = [&](const bf16* kt, f32x16* s) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[t][r] = 0.f;
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
         const int row = 32 * t + i32;
-        const bf16* src = s_k + row * D + 8 * k_chunk<D>(row, 2 * kb + h);
+        const bf16* src = kt + row * D + 8 * k_chunk<D>(row, 2 * kb + h);
         lds_check(src, 16);
         s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(src), q[kb],
                                                        s[t], 0, 0, 0);
       }
-    }
+  };
+  auto top = [&](const f32x16* s) {
+    float mx = s[0][0];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[t][r]);
+    return fmaxf(mx, __shfl_xor(mx, 32)) * c_scale;
+  };
+
+  f32x16 s[2];
+  load_tile(kb_, p.ld_k, lk2, ck, s_k[0], lo);
+  wait_tiles();
+  if (lo + BN < stop) load_tile(kb_, p.ld_k, lk2, ck, s_k[1], lo + BN);
+  load_tile(vb_, p.ld_v, lv2, cv, s_v[0], lo);
+  scores(s_k[0], s);
+  float mx = top(s);
+  int buf = 0;
+  for (int k0 = lo; k0 < stop; k0 += BN, buf ^= 1) {
+    wait_tiles();
+    if (k0 + 2 * BN < stop) load_tile(kb_, p.ld_k, lk2, ck, s_k[buf], k0 + 2 * BN);
+    if (k0 + BN < stop) load_tile(vb_, p.ld_v, lv2, cv, s_v[buf ^ 1], k0 + BN);
+    if (k0 >= mine) continue;               // nothing left for this wave to see
     if (k0 + BN - 1 > q0 || (window && k0 <= q0 + 31 - window)) {   // some pairs are not seen
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -283,30 +343,34 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p
           const bool seen = u <= tq && (!window || u > tq - window);
           if (!seen) s[t][r] = -__builtin_huge_valf();
         }
+      mx = top(s);
     }
-    float mx = s[0][0];
+    // The sums are kept relative to m, which need not be the maximum: it is
+    // moved only when a score passes it by 2^8, so weights stay below 2^8 and
+    // the output is rarely rescaled.
+    if (__any(mx > m + 8.f)) {
+      const float m_new = fmaxf(m, mx);
+      const float alpha = exp2_fast(m - m_new);
+      m = m_new;
+      l *= alpha;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int c = 0; c < MT; ++c)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[t][r]);
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float m_new = fmaxf(m, mx * c_scale);
-    const float alpha = exp2_fast(m - m_new);
-    m = m_new;
-    l *= alpha;
+        for (int r = 0; r < 16; ++r) o[c][r] *= alpha;
+    }
+    f32x16 sn[2];
+    scores(s_k[buf ^ 1], sn);               // of the next tile (unused after the last)
+    bf16x8 w[4];
 #pragma unroll
-    for (int c = 0; c < MT; ++c)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[c][r] *= alpha;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {           // 16-token blocks
-      bf16x8 w;
+    for (int b = 0; b < 4; ++b)             // 16-token blocks
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float e = exp2_fast(__builtin_fmaf(s[b / 2][8 * (b % 2) + i], c_scale, -m));
         l += e;
-        w[i] = (bf16)e;
+        w[b][i] = (bf16)e;
       }
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int c = 0; c < MT; ++c) {
         bf16x8 a;
@@ -315,13 +379,15 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p
           const int li = lane & 15;
           const int row = 16 * b + 8 * half + 4 * h + (li >> 2);
           const int col = 32 * c + 16 * ((lane >> 4) & 1) + 4 * (li & 3);
-          const bf16x4 u = read_tr16(s_v + row * D + 8 * v_chunk<D>(row, col / 8) + col % 8);
+          const bf16x4 u = read_tr16(s_v[buf] + row * D + 8 * v_chunk<D>(row, col / 8) + col % 8);
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[4 * half + i] = u[i];
         }
-        o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w, o[c], 0, 0, 0);
+        o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w[b], o[c], 0, 0, 0);
       }
-    }
+    mx = top(sn);
+    s[0] = sn[0];
+    s[1] = sn[1];
   }
   l += __shfl_xor(l, 32);
   if (tq >= L) return;

@@ -16,7 +16,7 @@
  * nothing allocated, no mutable state), with these additions:
  *  - Row strides: an input of shape [rows, H, d] has its H d elements of a row
  *    together and `ld` elements from one row to the next, so it may be a
- *    column block of a projection output.  ld % 8 == 0, H d <= ld < 2^31.
+ *    column block of a projection output.  ld % 8 == 0, H d <= ld <= 2^24.
  *    Pointers are 16-byte aligned unless stated otherwise.
  *  - Query head h reads key/value head h / (H_q / H_k).
  *  - Paged cache: k_cache, v_cache [num_pages, H_k, page_size, d] are codes of
