@@ -24,6 +24,55 @@ __device__ __forceinline__ PackedItem find_packed(const int64_t* __restrict__ cu
   });
 }
 
+// Sum over the wave: within the rows of 16 lanes by DPP moves, then four lanes.
+__device__ __forceinline__ int wave_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, false);   // quad_perm [1,0,3,2]
+  v += __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xf, 0xf, false);   // quad_perm [2,3,0,1]
+  v += __builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, false);  // row_half_mirror
+  v += __builtin_amdgcn_update_dpp(0, v, 0x140, 0xf, 0xf, false);  // row_mirror
+  return __builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16) +
+         __builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48);
+}
+
+// rank_tile_by over at most 1024 sequences: each lane keeps the tiles of up to
+// 16 of them, sequence 64 i + lane in c[i].
+__device__ __forceinline__ PackedItem rank_tile(const int64_t* __restrict__ cu, int N,
+                                                int64_t total, int unit, int64_t rank) {
+  constexpr int kMost = 16;
+  const int lane = threadIdx.x & 63;
+  int c[kMost];
+  const int used = (N + 63) >> 6;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int n = 64 * i + lane;
+    c[i] = i < used && n < N ? (int)packed_tiles(cu, n, total, unit) : 0;
+  }
+  auto count = [&](auto f) {                // fits in 32 bits: the host bounds the tiles
+    int v = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i)
+      if (i < used) v += (int)f((int64_t)c[i]);
+    return (int64_t)wave_sum(v);
+  };
+  auto pick = [&](auto f, int64_t k) {
+    int64_t found = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (i >= used) continue;
+      uint64_t m = __ballot(f((int64_t)c[i]));
+      const int here = __popcll(m);
+      if (k >= 0 && k < here) {
+        for (; k > 0; --k) m &= m - 1;
+        found = 64 * i + (__ffsll((unsigned long long)m) - 1);
+        k = -1;
+      }
+      if (k >= 0) k -= here;
+    }
+    return found;
+  };
+  return rank_tile_by(cu, total, unit, rank, count, pick);
+}
+
 // 8 consecutive elements kept as loaded, so that many rows are in flight at
 // the cost of 4 (bf16) or 8 (fp32) registers each.
 template <typename T> struct Chunk8;

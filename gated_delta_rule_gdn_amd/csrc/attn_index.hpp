@@ -52,6 +52,33 @@ GDN_HD bool packed_at_or_before(const int64_t* cu, int64_t n, int64_t total, int
   return clamp_i64(cu[n], 0, total) / unit + extra * n <= idx;
 }
 
+// Tiles of `unit` tokens of packed sequences in falling order of their number
+// within the sequence (equal numbers by sequence): which tile is `rank`-th.
+// None (end <= start) where there are fewer.  count(f) is the sum of f(n) over
+// the N sequences, pick(f, k) the k-th sequence (from 0) with f(n) true.
+GDN_HD int64_t packed_tiles(const int64_t* cu, int64_t n, int64_t total, int unit) {
+  const int64_t L = clamp_i64(cu[n + 1], 0, total) - clamp_i64(cu[n], 0, total);
+  return L > 0 ? (L + unit - 1) / unit : 0;
+}
+template <typename Count, typename Pick>
+GDN_HD PackedItem rank_tile_by(const int64_t* cu, int64_t total, int unit, int64_t rank,
+                               Count count, Pick pick) {
+  // largest j with sum_n max(0, tiles_n - j) > rank
+  int64_t lo = 0, hi = (total + unit - 1) / unit;
+  PackedItem r{0, 0, 0, 0};
+  if (count([&](int64_t c) { return c; }) <= rank) return r;
+  while (hi - lo > 1) {
+    const int64_t j = lo + (hi - lo) / 2;
+    if (count([&](int64_t c) { return c > j ? c - j : 0; }) > rank) lo = j; else hi = j;
+  }
+  const int64_t above = count([&](int64_t c) { return c > lo + 1 ? c - lo - 1 : 0; });
+  r.n = pick([&](int64_t c) { return c > lo; }, rank - above);
+  r.item = lo;
+  r.start = clamp_i64(cu[r.n], 0, total);
+  r.end = clamp_i64(cu[r.n + 1], 0, total);
+  return r;
+}
+
 // New rows [kept, stop) of the j-th page that L new tokens (rows a .. a + L of
 // the input) touch behind seq_len held ones; none when kept >= stop.
 struct AppendPage {

@@ -20,30 +20,91 @@ constexpr int kThreads = 256;
 constexpr float kNone = -1e30f;           // running maximum (log2 units) before any token
 
 // One workgroup's query tile: queries [q0, q0 + BM) of the sequence that is
-// rows [a, a + L) of the packed tensors.
+// rows [a, a + L) of the packed tensors, and a query head.
 struct Tile {
   int64_t a, L, q0;
   int hq;
   bool valid;
 };
 
+// Workgroup blk runs on XCD blk % 8, and each XCD has an L2 of its own, so the
+// workgroups that follow each other on an XCD should read the same keys and
+// values; and a query tile costs as many key tiles as lie before it, so the
+// late tiles should start first.  The query heads of a key head always follow
+// each other.  (All counts fit in 32 bits: the host bounds the grid.)
+//
+// Equal lengths, key heads of all sequences a multiple of 8: an XCD keeps its
+// share of them, in groups of 4 query heads or more, and goes through each
+// group's tiles from the last to the first.  64 workgroups
+// of an XCD then walk the keys of 4 heads together (B 8, T 4096, 16 heads:
+// 95 % of the L2 reads hit against 48 % with heads dealt round the XCDs).
+// Otherwise tiles are dealt round the XCDs, the last tiles of all sequences
+// first.
+//
+// Packed lengths: the same order over tiles by their number in the sequence,
+// found by counting: with c_n tiles in sequence n, sum_n max(0, c_n - j) tiles
+// have number j or more.
+constexpr uint32_t kXcds = 8;
+constexpr int64_t kNear = 4096;           // a window that makes all tiles cost about the same
+constexpr int64_t kMaxRanked = 1024;      // sequences that are ranked; more keep their order
+
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const PrefillArgs& p, int64_t blk, int64_t blocks) {
+__device__ __forceinline__ Tile find_tile(const PrefillArgs& p, uint32_t blocks) {
   Tile t;
-  t.hq = (int)(blk % p.Hq);
-  const int64_t slots = blocks / p.Hq;
-  const int64_t slot = slots - 1 - blk / p.Hq;      // late (long) tiles first
+  const uint32_t blk = blockIdx.x;
+  const uint32_t G = (uint32_t)(p.Hq / p.Hk), Hk = (uint32_t)p.Hk, N = (uint32_t)p.N;
+  const uint32_t per = blocks / kXcds;                    // full rounds over the XCDs
+  const uint32_t xcd = blk % kXcds, i = blk / kXcds;
+  t.valid = true;
   if (!p.cu_seqlens) {
-    const int64_t qt = slot / p.N, n = slot - qt * p.N;
+    const uint32_t tiles = ((uint32_t)p.Tseq + BM - 1) / BM, pairs = N * Hk;
+    const uint32_t mine = pairs / kXcds;                  // pairs of an XCD
+    uint32_t pair, tile, head;
+    if (pairs % kXcds == 0) {
+      const uint32_t gp = G >= 4 ? 1 : 4 / G;             // pairs of a group
+      const uint32_t grp = i / (gp * tiles * G), w = i - grp * (gp * tiles * G);
+      const uint32_t here = mine - grp * gp < gp ? mine - grp * gp : gp;
+      const uint32_t level = w / (here * G), x = w - level * (here * G);
+      tile = tiles - 1 - level;
+      pair = xcd + kXcds * (grp * gp + x / G);
+      head = x % G;
+    } else {
+      // unit = (tile from the last, pair); the last partial round is dealt plainly
+      uint32_t unit;
+      const uint32_t rounds = per / G;
+      if (i < rounds * G) { unit = i / G * kXcds + xcd; head = i % G; }
+      else { const uint32_t r = blk - rounds * G * kXcds; unit = rounds * kXcds + r / G; head = r % G; }
+      tile = tiles - 1 - unit / pairs;
+      pair = unit % pairs;
+    }
+    const uint32_t n = pair / Hk, hk = pair - n * Hk;
     t.a = n * p.Tseq;
     t.L = p.Tseq;
-    t.q0 = qt * BM;
-  } else {
-    const PackedItem it = find_packed(p.cu_seqlens, p.N, p.total_T, BM, 1, slot);
-    t.a = it.start;
-    t.L = it.end - it.start;
-    t.q0 = it.item * BM;
+    t.q0 = (int64_t)tile * BM;
+    t.hq = (int)(hk * G + head);
+    return t;
   }
+  const bool near = p.window > 0 && p.window <= kNear;
+  uint32_t unit, head;
+  const uint32_t rounds = per / G;
+  if (i < rounds * G) {
+    unit = i / G * kXcds + xcd;
+    head = i % G;
+  } else {
+    const uint32_t r = blk - rounds * G * kXcds;
+    unit = rounds * kXcds + r / G;
+    head = r % G;
+  }
+  const uint32_t rank = unit / Hk;
+  t.hq = (int)((unit - rank * Hk) * G + head);
+  PackedItem it;
+  if (near || p.N > kMaxRanked)
+    it = find_packed(p.cu_seqlens, p.N, p.total_T, BM, 1, (int64_t)rank);
+  else
+    it = rank_tile(p.cu_seqlens, (int)p.N, p.total_T, BM, (int64_t)rank);
+  t.a = it.start;
+  t.L = it.end - it.start;
+  t.q0 = it.item * BM;
   t.valid = t.q0 >= 0 && t.q0 < t.L;
   return t;
 }
@@ -53,12 +114,12 @@ __device__ __forceinline__ Tile find_tile(const PrefillArgs& p, int64_t blk, int
 // tiles of 32 tokens in LDS.
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ __launch_bounds__(kThreads) void prefill_f32_kernel(PrefillArgs p, int64_t blocks) {
+__global__ __launch_bounds__(kThreads) void prefill_f32_kernel(PrefillArgs p, uint32_t blocks) {
   constexpr int BM = 64, BN = 32, LD = D + 4, KB = D / 32, MT = D / 16;
   __shared__ __align__(16) float s_k[BN * LD], s_v[BN * LD];
   lds_nan_fill(s_k, sizeof s_k);
   lds_nan_fill(s_v, sizeof s_v);
-  const Tile tl = find_tile<BM>(p, blockIdx.x, blocks);
+  const Tile tl = find_tile<BM>(p, blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -219,13 +280,19 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
 
+// Maximum over the two lanes 32 apart.
+__device__ __forceinline__ float over_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // The loop over key tiles is pipelined by hand: while the weights of tile i
 // are formed (VALU), the scores of tile i + 1 are on the matrix cores, and
 // while the maximum of tile i + 1 is formed, tile i's product with V is.  K
 // runs one tile ahead of V; both are double-buffered in LDS and loaded one
 // iteration before they are read, with one barrier to an iteration.
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p, int64_t blocks) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel(PrefillArgs p, uint32_t blocks) {
   constexpr int BM = 128, BN = 64, KB = D / 16, MT = D / 32;
   constexpr int CH = D / 8;                           // 16-byte chunks of a row
   constexpr int NL = BN * CH / kThreads;              // chunks a thread loads of a tile
@@ -233,7 +300,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p
   __shared__ __align__(16) bf16 s_k[2][BN * D], s_v[2][BN * D];
   lds_nan_fill(s_k, sizeof s_k);
   lds_nan_fill(s_v, sizeof s_v);
-  const Tile tl = find_tile<BM>(p, blockIdx.x, blocks);
+  const Tile tl = find_tile<BM>(p, blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -245,26 +312,6 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p
   const int tq = q0 + i32;                  // this lane's query
   const bf16* kb_ = static_cast<const bf16*>(p.k) + tl.a * p.ld_k + hk * D;
   const bf16* vb_ = static_cast<const bf16*>(p.v) + tl.a * p.ld_v + hk * D;
-
-  bf16x8 q[KB];
-  {
-    const int row = tq < L ? tq : L - 1;
-    const bf16* qp = static_cast<const bf16*>(p.q) + (tl.a + row) * p.ld_q + tl.hq * D + 8 * h;
-    const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;   // the scale below is positive
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      uint4 u = *reinterpret_cast<const uint4*>(qp + 16 * kb);
-      u.x ^= flip; u.y ^= flip; u.z ^= flip; u.w ^= flip;
-      q[kb] = __builtin_bit_cast(bf16x8, u);
-    }
-  }
-  const float c_scale = fabsf(p.scale) * kLog2e;
-  f32x16 o[MT];
-#pragma unroll
-  for (int c = 0; c < MT; ++c)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) o[c][r] = 0.f;
-  float m = kNone, l = 0.f;
 
   const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
   int lo = window ? qt0 - window + 1 : 0;             // first key that the tile sees
@@ -296,6 +343,50 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p
     }
   };
 
+  // The queries come in whole rows too, by way of the second key buffer (waves
+  // 0 and 1) and the second value buffer: loads of a fragment's rows straight
+  // into registers touch 64 rows each.
+  load_tile(kb_, p.ld_k, lk2, ck, s_k[0], lo);
+  bf16* sq = wave < 2 ? s_k[1] + wave * (32 * D) : s_v[1] + (wave - 2) * (32 * D);
+  {
+    constexpr int RQ = 64 / CH;             // rows of a wave's load
+    const i32x4 rs = buffer_at(static_cast<const bf16*>(p.q) + (tl.a + q0) * p.ld_q + tl.hq * D);
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(sq));
+#pragma unroll
+    for (int e = 0; e < 32 / RQ; ++e) {
+      const int row = e * RQ + lane / CH;
+      const int from = q0 + row < L ? row : L - 1 - q0;   // past the sequence: its last row
+      if (q0 < L)                           // (a wave without a query loads none)
+        load_lds16(at + e * 1024, rs, (uint32_t)from * (uint32_t)(p.ld_q * 2) +
+                                                    16 * k_chunk<D>(row, lane % CH), 0);
+    }
+  }
+  load_tile(vb_, p.ld_v, lv2, cv, s_v[0], lo);
+  wait_tiles();
+  bf16x8 q[KB];
+  {
+    const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;   // the scale below is positive
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const bf16* src = sq + i32 * D + 8 * k_chunk<D>(i32, 2 * kb + h);
+      lds_check(src, 16);
+      uint4 u = *reinterpret_cast<const uint4*>(src);
+      u.x ^= flip; u.y ^= flip; u.z ^= flip; u.w ^= flip;
+      q[kb] = __builtin_bit_cast(bf16x8, u);
+    }
+  }
+  wait_tiles();                             // every wave has its queries
+  if (lo + BN < stop) load_tile(kb_, p.ld_k, lk2, ck, s_k[1], lo + BN);
+
+  const float c_scale = fabsf(p.scale) * kLog2e;
+  f32x16 o[MT];
+#pragma unroll
+  for (int c = 0; c < MT; ++c)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[c][r] = 0.f;
+  float m = kNone, l = 0.f;
+
+
   auto scores = [&](const bf16* kt, f32x16* s) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -318,33 +409,39 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[t][r]);
-    return fmaxf(mx, __shfl_xor(mx, 32)) * c_scale;
+    return over_halves(mx) * c_scale;
   };
 
   f32x16 s[2];
-  load_tile(kb_, p.ld_k, lk2, ck, s_k[0], lo);
-  wait_tiles();
-  if (lo + BN < stop) load_tile(kb_, p.ld_k, lk2, ck, s_k[1], lo + BN);
-  load_tile(vb_, p.ld_v, lv2, cv, s_v[0], lo);
   scores(s_k[0], s);
   float mx = top(s);
-  int buf = 0;
-  for (int k0 = lo; k0 < stop; k0 += BN, buf ^= 1) {
+  // One iteration: tile k0's scores are in s, V's buffer is `buf`; leaves the
+  // next tile's scores in sn and their maximum in mx.
+  auto step = [&](int k0, int buf, f32x16* s, f32x16* sn) {
     wait_tiles();
     if (k0 + 2 * BN < stop) load_tile(kb_, p.ld_k, lk2, ck, s_k[buf], k0 + 2 * BN);
     if (k0 + BN < stop) load_tile(vb_, p.ld_v, lv2, cv, s_v[buf ^ 1], k0 + BN);
-    if (k0 >= mine) continue;               // nothing left for this wave to see
-    if (k0 + BN - 1 > q0 || (window && k0 <= q0 + 31 - window)) {   // some pairs are not seen
+    if (k0 >= mine) return;                 // nothing left for this wave to see
+    // element (t, r) is token k0 + 4 h + at: not seen where at > tq - k0 - 4 h,
+    // or at <= that less the window
+    const bool front = k0 + BN - 1 > q0, back = window && k0 <= q0 + 31 - window;
+    if (front) {
+      const int last = tq - k0 - 4 * h;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int u = k0 + 32 * t + 8 * (r / 4) + 4 * h + r % 4;
-          const bool seen = u <= tq && (!window || u > tq - window);
-          if (!seen) s[t][r] = -__builtin_huge_valf();
-        }
-      mx = top(s);
+        for (int r = 0; r < 16; ++r)
+          if (32 * t + 8 * (r / 4) + r % 4 > last) s[t][r] = -__builtin_huge_valf();
     }
+    if (back) {
+      const int before = tq - window - k0 - 4 * h;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (32 * t + 8 * (r / 4) + r % 4 <= before) s[t][r] = -__builtin_huge_valf();
+    }
+    if (front || back) mx = top(s);
     // The sums are kept relative to m, which need not be the maximum: it is
     // moved only when a score passes it by 2^8, so weights stay below 2^8 and
     // the output is rarely rescaled.
@@ -358,47 +455,90 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_bf16_kernel(PrefillArgs p
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[c][r] *= alpha;
     }
-    f32x16 sn[2];
-    scores(s_k[buf ^ 1], sn);               // of the next tile (unused after the last)
-    bf16x8 w[4];
+    // One product to a line of this schedule, with LDS reads some products
+    // ahead of their use and a share of the vector work behind each; the
+    // compiler keeps the lines in order.
+    constexpr int NQ = 2 * KB, NP = 4 * MT;   // products of scores and of the output
+    constexpr int AK = 2, AV = 2;             // reads ahead (2 to 6 measure alike; 3 spill at D 64)
+    constexpr int EW = 32 / NQ;               // weights to a score product
+    bf16x8 kf[NQ], vf[NP], w[4];
+    auto read_k = [&](int i) {
+      const int row = 32 * (i % 2) + i32;
+      const bf16* src = s_k[buf ^ 1] + row * D + 8 * k_chunk<D>(row, 2 * (i / 2) + h);
+      lds_check(src, 16);
+      kf[i] = *reinterpret_cast<const bf16x8*>(src);
+    };
+    auto read_v = [&](int j) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b)             // 16-token blocks
+      for (int half = 0; half < 2; ++half) {
+        const int li = lane & 15;
+        const int row = 16 * (j / MT) + 8 * half + 4 * h + (li >> 2);
+        const int col = 32 * (j % MT) + 16 * ((lane >> 4) & 1) + 4 * (li & 3);
+        const bf16x4 u = read_tr16(s_v[buf] + row * D + 8 * v_chunk<D>(row, col / 8) + col % 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = exp2_fast(__builtin_fmaf(s[b / 2][8 * (b % 2) + i], c_scale, -m));
-        l += e;
-        w[b][i] = (bf16)e;
+        for (int i = 0; i < 4; ++i) vf[j][4 * half + i] = u[i];
       }
+    };
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int c = 0; c < MT; ++c) {
-        bf16x8 a;
+      for (int r = 0; r < 16; ++r) sn[t][r] = 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int li = lane & 15;
-          const int row = 16 * b + 8 * half + 4 * h + (li >> 2);
-          const int col = 32 * c + 16 * ((lane >> 4) & 1) + 4 * (li & 3);
-          const bf16x4 u = read_tr16(s_v[buf] + row * D + 8 * v_chunk<D>(row, col / 8) + col % 8);
+    for (int i = 0; i < AK; ++i) read_k(i);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[4 * half + i] = u[i];
-        }
-        o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w[b], o[c], 0, 0, 0);
+    for (int i = 0; i < NQ; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + AK < NQ) read_k(i + AK);
+      if (i >= NQ - AV) read_v(i - (NQ - AV));
+      sn[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], q[i / 2], sn[i % 2], 0, 0, 0);
+#pragma unroll
+      for (int e = EW * i; e < EW * i + EW; ++e) {
+        const float x = exp2_fast(__builtin_fmaf(s[e / 16][e % 16], c_scale, -m));
+        l += x;
+        w[e / 8][e % 8] = (bf16)x;
       }
-    mx = top(sn);
-    s[0] = sn[0];
-    s[1] = sn[1];
+    }
+    float top_n = -__builtin_huge_valf();
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (j + AV < NP) read_v(j + AV);
+      o[j % MT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[j], w[j / MT], o[j % MT], 0, 0, 0);
+      constexpr int EM = 32 / NP;
+#pragma unroll
+      for (int e = EM * j; e < EM * j + EM; ++e) top_n = fmaxf(top_n, sn[e / 16][e % 16]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    mx = over_halves(top_n) * c_scale;
+  };
+  f32x16 s1[2];
+  for (int k0 = lo; k0 < stop; k0 += 2 * BN) {
+    step(k0, 0, s, s1);
+    if (k0 + BN < stop) step(k0 + BN, 1, s1, s);
   }
   l += __shfl_xor(l, 32);
-  if (tq >= L) return;
   const float inv = 1.f / l;                // a query sees itself: l > 0
-  bf16* op = static_cast<bf16*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * h;
+  // rows leave through LDS (this wave's quarter of the key tiles, which no wave
+  // reads any more), so that a store covers whole rows
+  wait_tiles();
+  static_assert(BM == 2 * BN, "the waves' rows fill the key tiles");
+  bf16* so = &s_k[0][0] + wave * 32 * D;
 #pragma unroll
   for (int c = 0; c < MT; ++c)
 #pragma unroll
-    for (int r = 0; r < 16; r += 4)
-      store4<bf16>(op + 32 * c + 2 * r, o[c][r] * inv, o[c][r + 1] * inv, o[c][r + 2] * inv,
-                   o[c][r + 3] * inv);
+    for (int r = 0; r < 16; r += 4) {
+      bf16* dst = so + i32 * D + 8 * ((4 * c + r / 4) ^ (i32 & (CH - 1))) + 4 * h;
+      lds_check(dst, 8);
+      store4<bf16>(dst, o[c][r] * inv, o[c][r + 1] * inv, o[c][r + 2] * inv, o[c][r + 3] * inv);
+    }
+  bf16* op = static_cast<bf16*>(p.o) + ((tl.a + q0) * p.Hq + tl.hq) * (int64_t)D;
+#pragma unroll
+  for (int e = 0; e < 32 * CH / 64; ++e) {
+    const int row = (e * 64 + lane) / CH, c = (e * 64 + lane) % CH;
+    if (q0 + row < L)
+      *reinterpret_cast<uint4*>(op + row * (int64_t)p.Hq * D + 8 * c) =
+          *reinterpret_cast<const uint4*>(so + row * D + 8 * (c ^ (row & (CH - 1))));
+  }
 }
 
 }  // namespace
@@ -413,11 +553,11 @@ hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t stream) {
       prefill_blocks(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, a.Hq, a.io);
   const dim3 grid((unsigned)blocks);
   if (a.io == DType::F32) {
-    if (a.d == 128) prefill_f32_kernel<128><<<grid, kThreads, 0, stream>>>(a, blocks);
-    else prefill_f32_kernel<64><<<grid, kThreads, 0, stream>>>(a, blocks);
+    if (a.d == 128) prefill_f32_kernel<128><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
+    else prefill_f32_kernel<64><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
   } else {
-    if (a.d == 128) prefill_bf16_kernel<128><<<grid, kThreads, 0, stream>>>(a, blocks);
-    else prefill_bf16_kernel<64><<<grid, kThreads, 0, stream>>>(a, blocks);
+    if (a.d == 128) prefill_bf16_kernel<128><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
+    else prefill_bf16_kernel<64><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
   }
   return hipGetLastError();
 }

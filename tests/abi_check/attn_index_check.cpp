@@ -113,6 +113,36 @@ void tiles(std::mt19937& r, bool good) {   // a prefill's query tiles
     for (int64_t t = 0; t < total; ++t) need(seen[t] == 1, "each query computed once");
 }
 
+void ranked_tiles(std::mt19937& r, bool good) {   // the same tiles, the late ones first
+  const int64_t N = 1 + r() % (r() % 4 ? 9 : 200);
+  int64_t total;
+  const auto cu = offsets(r, N, total, good);
+  const int BM = r() % 2 ? 64 : 128;
+  std::vector<int64_t> c(N);
+  for (int64_t n = 0; n < N; ++n) c[n] = packed_tiles(cu.data(), n, total, BM);
+  auto count = [&](auto f) { int64_t v = 0; for (int64_t x : c) v += f(x); return v; };
+  auto pick = [&](auto f, int64_t k) {
+    int64_t n = 0;
+    for (; n < N; ++n) if (f(c[n]) && k-- == 0) break;
+    return n < N ? n : 0;
+  };
+  std::vector<int> seen(total, 0);
+  int64_t before = INT64_MAX;
+  for (int64_t x = 0; x < total / BM + N; ++x, ++items) {
+    const PackedItem it = rank_tile_by(cu.data(), total, BM, x, count, pick);
+    const int64_t L = it.end - it.start, q0 = it.item * BM;
+    if (q0 < 0 || q0 >= L) continue;
+    need(it.item <= before, "falling order");
+    before = it.item;
+    for (int64_t q = q0; q < q0 + BM && q < L; ++q) {
+      need(it.start + q >= 0 && it.start + q < total, "query row");
+      ++seen[it.start + q];
+    }
+  }
+  if (good)
+    for (int64_t t = 0; t < total; ++t) need(seen[t] == 1, "each query computed once");
+}
+
 void decode(std::mt19937& r) {
   const int P = 16 << (r() % 4), step = 32;
   const int64_t width = 1 + r() % 50, cap = width * P, span = 128 * (1 + r() % 5);
@@ -149,6 +179,8 @@ int main() {
     append_equal(r);
     tiles(r, true);
     tiles(r, false);
+    ranked_tiles(r, true);
+    ranked_tiles(r, false);
     decode(r);
   }
   std::printf("ok %ld\n", items);
