@@ -116,12 +116,15 @@ gdn_status check_decode_desc(const gdn_attn_decode_desc* d) {
   if (st != GDN_OK) return st;
   if ((int64_t)d->H_q * d->d > (int64_t(1) << 22)) return GDN_ERR_UNSUPPORTED;
   if ((double)d->N * d->H_q * d->d > kMaxElems) return GDN_ERR_INVALID_ARG;
-  if ((double)d->N * d->H_q * 256.0 > kMaxThreads) return GDN_ERR_UNSUPPORTED;
+  // segments are counted in 32 bits, and so are their rounds of 128 tokens
+  if ((double)d->N * d->H_q * 256.0 > kMaxThreads ||
+      (double)d->N * d->H_q * ((double)d->max_pages * d->page_size / 128.0 + 1.0) > 2.0e9)
+    return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 
-gdn::AttnDecodeSplit decode_split(const gdn_attn_decode_desc* d) {
-  return gdn::attn_decode_split(d->N, d->max_pages * d->page_size, d->window, d->H_q, d->H_k, d->d);
+gdn::AttnDecodePlan decode_plan(const gdn_attn_decode_desc* d) {
+  return gdn::attn_decode_plan(d->N, d->max_pages * d->page_size, d->window, d->H_q, d->H_k, d->d);
 }
 
 }  // namespace
@@ -273,7 +276,7 @@ gdn_status gdn_attn_prefill(const gdn_attn_prefill_desc* d, const int64_t* cu_se
 
 size_t gdn_attn_decode_workspace_size(const gdn_attn_decode_desc* d) {
   if (check_decode_desc(d) != GDN_OK || d->N == 0) return 0;
-  return (size_t)decode_split(d).ws_floats * 4;
+  return (size_t)decode_plan(d).ws_floats * 4;
 }
 
 gdn_status gdn_attn_decode(const gdn_attn_decode_desc* d, const void* q, const void* k_cache,
@@ -283,14 +286,11 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_desc* d, const void* q, const v
   gdn_status st = check_decode_desc(d);
   if (st != GDN_OK) return st;
   if (d->N == 0) return GDN_OK;
-  const gdn::AttnDecodeSplit sp = decode_split(d);
-  if ((double)d->N * d->H_k * ((d->H_q / d->H_k + 15) / 16) * (double)sp.splits * 256.0 >
-      kMaxThreads)
-    return GDN_ERR_UNSUPPORTED;
+  const gdn::AttnDecodePlan plan = decode_plan(d);
   if (!q || !o || !aligned16(q) || !aligned16(o)) return GDN_ERR_INVALID_ARG;
   st = check_cache_ptrs(CachePtrs{k_cache, v_cache, k_scale, v_scale, page_table, seq_lens});
   if (st != GDN_OK) return st;
-  const int64_t need = sp.ws_floats * 4;
+  const int64_t need = plan.ws_floats * 4;
   if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < (size_t)need))
     return GDN_ERR_INVALID_ARG;
 

@@ -7,10 +7,18 @@
 // them).  Every code is read once; a token's 2 d bytes take 4 d flops for
 // each of the group's query heads, so the kernel is bound by HBM.
 //
-// A workgroup has one sequence, one key head, up to 16 query heads of its
-// group and one span of tokens.  Its 4 waves take steps of 32 tokens in turn,
-// each with a running maximum and sum of its own, and join through LDS at the
-// end.  Products run on v_mfma_f32_16x16x32_bf16 with the queries as columns:
+// The work is cut into rounds of 128 tokens of one segment: a sequence, a key
+// head and up to 16 query heads of its group.  The rounds of all segments, in
+// order, are dealt to the workgroups in equal shares, so lengths need not be
+// alike and one long cache fills the chip; a share begins and ends anywhere.
+// What a workgroup has of a segment is written straight to the output if that
+// is all of it, else as a partial result, and a second kernel joins those.
+// (Where no cache can be longer than kDirect tokens each workgroup has one
+// whole segment, and nothing is joined.)
+//
+// The 4 waves of a workgroup take 32 tokens of a round each, with a running
+// maximum and sum of their own, and join through LDS when the segment ends.
+// Products run on v_mfma_f32_16x16x32_bf16 with the queries as columns:
 //
 //   S^T [16 tokens x 16 queries] = K Q^T     twice, tokens 0-15 and 16-31
 //   O^T [d x 16 queries]        += V^T P^T   over the 32 tokens
@@ -31,6 +39,13 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kStep = 32;                 // tokens of a wave's step
 constexpr int kRound = kWaves * kStep;    // tokens of a workgroup's step
+#ifndef KB_BLOCKS
+#define KB_BLOCKS 512
+#define KB_LEAST 4
+#endif
+constexpr int64_t kBlocks = KB_BLOCKS;           // workgroups that fill the chip: 2 to a CU
+constexpr int kLeast = KB_LEAST;                 // rounds that are worth a workgroup
+constexpr int64_t kDirect = 4 * kRound;   // tokens of a cache that one workgroup takes whole
 constexpr float kNone = -1e30f;           // running maximum (log2 units) before any token
 
 // Two e4m3 codes (low or high half of a dword) as bf16.
@@ -69,17 +84,38 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// Codes of one step in this lane.
+// Codes of one step in this lane, and the tiles' scales.
 template <int D>
 struct StepCodes {
-  uint32_t k[2][D / 16];      // tile, D/4 bytes of token j of the tile
+  uint32_t k[2][D / 16];      // tile, bytes [16 g, +16) of each 64 of token j
   uint32_t v[8][D / 64];      // token 4 g + i (tile i / 4), D/16 columns
-  float ks[2], vs[2];         // the tiles' scales; ks < 0: no page
+  float ks[2], vs[2];
+  bool there[2];
 };
 
+// A segment's round: tokens [token, token + 128) of those in [lo, len).
+struct Round {
+  int n, hk, qg;      // the segment
+  int r, rounds;      // number within the segment, and how many it has
+  int64_t token, lo, len;
+};
+
+// Partial results in the workspace: two for each workgroup, of gn <= 16 rows of
+// D + 4 floats (sums, maximum, sum of weights): [0] of a segment that began in
+// an earlier workgroup, [1] of one that goes on in the next.  Then for each
+// workgroup the segment of [1] (-1: none) and the last workgroup that has a
+// part of it.
+template <int D>
+__device__ __forceinline__ float* part_at(float* ws, int rows, int64_t block, int which, int row) {
+  return ws + ((block * 2 + which) * rows + row) * (D + 4);
+}
+__device__ __forceinline__ int2* chain_at(float* ws, int rows, int D, int64_t blocks, int64_t block) {
+  return reinterpret_cast<int2*>(ws + blocks * 2 * rows * (D + 4)) + block;
+}
+
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void attn_decode_kernel(AttnDecodeArgs p, int qgroups,
-                                                               int splits, int64_t span) {
+__global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs p, int qgroups,
+                                                                  bool direct) {
   constexpr int NT = std::is_same<T, float>::value ? 3 : 1;   // bf16 terms of q and of a weight
   constexpr int KB = D / 32;              // k-blocks of the score product
   constexpr int MT = D / 16;              // 16-column tiles of the output
@@ -90,36 +126,97 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(AttnDecodeArgs p,
   lds_nan_fill(s_l, sizeof s_l);
 
   const int G = p.Hq / p.Hk;
-  const int split = blockIdx.x % splits;
-  const int64_t rest = blockIdx.x / splits;
-  const int qg = (int)(rest % qgroups);
-  const int64_t nh = rest / qgroups;
-  const int64_t n = nh / p.Hk;
-  const int hk = (int)(nh - n * p.Hk);
-  const int g0 = 16 * qg;                 // first query head of the group here
-  const int gn = G - g0 < 16 ? G - g0 : 16;
-
+  const int prows = G < 16 ? G : 16;      // rows of a partial result
   const PagedCache& kv = p.cache;
   const int P = kv.page_size;
-  const DecodeSpan sp = decode_span(kv.seq_lens[n], kv.max_pages, P, p.window, split, span, kStep);
-  const int64_t len = sp.len, lo = sp.lo, begin = sp.begin, end = sp.end;
-  const bool only = sp.only;
-  if (begin >= end && !(only && split == 0)) return;
-
+  const int N = (int)p.N;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, j = lane & 15;
+  const uint32_t per_seq = (uint32_t)(p.Hk * qgroups);
 
-  // queries: lane holds query j's channels [g D/4, +D/4), as B operands
+  // this workgroup's share, and the segment it begins in
+  auto rounds_of = [&](int64_t seq_len) {
+    return decode_rounds(seq_len, kv.max_pages, P, p.window, kRound, kStep);
+  };
+  auto begin_round = [&](int n, uint32_t seg_in_seq, int r, int64_t seq_len) {
+    const DecodeSpan sp = decode_span(seq_len, kv.max_pages, P, p.window, kStep);
+    Round u;
+    u.n = n;
+    u.hk = (int)(seg_in_seq / (uint32_t)qgroups);
+    u.qg = (int)(seg_in_seq - (uint32_t)u.hk * qgroups);
+    u.rounds = sp.rounds(kRound);
+    u.r = r;
+    u.lo = sp.lo;
+    u.len = sp.len;
+    u.token = sp.first + (int64_t)r * kRound;
+    return u;
+  };
+  Round cur;
+  int count;                              // rounds of this workgroup
+  int share = 0, at = 0;                  // rounds of a workgroup; first round here, of all
+  if (direct) {
+    const int n = (int)(blockIdx.x / per_seq);
+    cur = begin_round(n, blockIdx.x - (uint32_t)n * per_seq, 0, kv.seq_lens[n]);
+    count = cur.rounds;
+  } else {
+    int total = 0;
+    for (int n0 = 0; n0 < N; n0 += 64)
+      total += n0 + lane < N ? rounds_of(kv.seq_lens[n0 + lane]) : 0;
+    total = wave_sum(total) * (int)per_seq;
+    share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    if (share < kLeast) share = kLeast;
+    at = (int)blockIdx.x * share;
+    count = total - at < share ? total - at : share;
+    if (count <= 0) {
+      if (tid == 0) *chain_at(p.ws, prows, D, gridDim.x, blockIdx.x) = make_int2(-1, 0);
+      return;
+    }
+    int before = 0;                       // rounds of the sequences before n
+    for (int n0 = 0;; n0 += 64) {
+      const int mine = (n0 + lane < N ? rounds_of(kv.seq_lens[n0 + lane]) : 0) * (int)per_seq;
+      const int all = wave_sum(mine);
+      if (before + all <= at && n0 + 64 < N) { before += all; continue; }
+      int upto = mine;                    // inclusive scan over the lanes
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(upto, off);
+        if (lane >= off) upto += v;
+      }
+      const uint64_t past = __ballot(before + upto > at);   // some lane: at < total
+      const int i = past ? __ffsll((unsigned long long)past) - 1 : 0;
+      const int n = n0 + i;
+      before += __builtin_amdgcn_readlane(upto, i) - __builtin_amdgcn_readlane(mine, i);
+      const int64_t seq_len = kv.seq_lens[n];
+      const int rn = rounds_of(seq_len);
+      const int seg = (at - before) / rn;
+      cur = begin_round(n, (uint32_t)seg, at - before - seg * rn, seq_len);
+      break;
+    }
+  }
+  auto advance = [&](const Round& u) {
+    Round v = u;
+    v.r++;
+    v.token += kRound;
+    if (v.r < v.rounds) return v;
+    uint32_t seg = (uint32_t)(u.hk * qgroups + u.qg) + 1;
+    int n = u.n;
+    if (seg == per_seq) { seg = 0; n = n + 1 < N ? n + 1 : n; }
+    return begin_round(n, seg, 0, kv.seq_lens[n]);
+  };
+
+  // queries: lane holds query j's channels [16 g, +16) of each 64, as B operands
   bf16x8 q[NT][KB];
-  {
+  auto load_queries = [&](const Round& u) {
+    const int gn = G - 16 * u.qg < 16 ? G - 16 * u.qg : 16;
     const T* qp = static_cast<const T*>(p.q) +
-                  ((n * p.Hq) + hk * G + g0 + (j < gn ? j : 0)) * (int64_t)D + g * (D / 4);
+                  ((int64_t)u.n * p.Hq + u.hk * G + 16 * u.qg + (j < gn ? j : 0)) * (int64_t)D +
+                  16 * g;
     const float flip = p.scale < 0.f ? -1.f : 1.f;            // the scale below is positive
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       float x[8];
-      load_f32<8, T>(qp + 8 * kb, x);
+      load_f32<8, T>(qp + 64 * (kb / 2) + 8 * (kb % 2), x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         bf16 t[NT];
@@ -128,47 +225,62 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(AttnDecodeArgs p,
         for (int c = 0; c < NT; ++c) q[c][kb][i] = t[c];
       }
     }
-  }
+  };
   const float c_scale = fabsf(p.scale) * kLog2e;
 
   f32x4 o[MT];
+  float m, l;
+  auto reset = [&]() {
 #pragma unroll
-  for (int c = 0; c < MT; ++c) o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = kNone, l = 0.f;
+    for (int c = 0; c < MT; ++c) o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    m = kNone;
+    l = 0.f;
+  };
 
-  const int32_t* __restrict__ table = kv.table + n * kv.max_pages;
-  auto load_step = [&](int64_t t0, StepCodes<D>& s) {
+  // The loop runs two loads ahead: the table entries of round i + 2 and the
+  // codes of round i + 1 are on their way while round i is computed.
+  const int shift = __builtin_ctz(P);     // P is a power of two
+  const float* __restrict__ kscale = kv.k_scale;
+  const float* __restrict__ vscale = kv.v_scale;
+  const uint32_t k_lane = (uint32_t)(j * D + 16 * g);
+  const uint32_t v_lane = (uint32_t)(4 * g * D + j * (D / 16));
+  auto entries = [&](const Round& u, int* e) {
+    const int32_t* __restrict__ table = kv.table + u.n * kv.max_pages;
+    const int64_t t0 = u.token + wave * kStep;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) e[t] = t0 + 16 * t < u.len ? table[(t0 + 16 * t) >> shift] : -1;
+  };
+  auto load_step = [&](const Round& u, const int* e, StepCodes<D>& s) {
+    const int64_t t0 = u.token + wave * kStep;
+    if (t0 >= u.len) return;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t tok = t0 + 16 * t;
-      const int64_t pi = tok / P;
-      int64_t page = tok < len ? table[pi] : -1;
-      const bool there = page >= 0 && page < kv.num_pages;
-      if (!there) page = 0;
-      const int64_t at = page * p.Hk + hk;
-      const int64_t row = at * P + (tok - pi * P);            // first row of the tile
-      s.ks[t] = there ? kv.k_scale[at] : -1.f;
-      s.vs[t] = there ? kv.v_scale[at] : 0.f;
-      const uint8_t* kp = kv.k + (row + j) * D + g * (D / 4);
-      const uint8_t* vp = kv.v + (row + 4 * g) * D + j * (D / 16);
+      const int page = __builtin_amdgcn_readfirstlane(e[t]);
+      s.there[t] = page >= 0 && page < kv.num_pages;
+      const int64_t at = s.there[t] ? (int64_t)page * p.Hk + u.hk : u.hk;   // else any page
+      const int64_t row = (at << shift) + ((t0 + 16 * t) & (P - 1));
+      s.ks[t] = kscale[at];
+      s.vs[t] = s.there[t] ? vscale[at] : 0.f;   // (0 weight times a stray NaN)
+      const uint8_t* kp = kv.k + row * D;
+      const uint8_t* vp = kv.v + row * D;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
-        const uint4 u = reinterpret_cast<const uint4*>(kp)[i];
-        s.k[t][4 * i] = u.x; s.k[t][4 * i + 1] = u.y;
-        s.k[t][4 * i + 2] = u.z; s.k[t][4 * i + 3] = u.w;
+        const uint4 w = *reinterpret_cast<const uint4*>(kp + k_lane + 64 * i);
+        s.k[t][4 * i] = w.x; s.k[t][4 * i + 1] = w.y;
+        s.k[t][4 * i + 2] = w.z; s.k[t][4 * i + 3] = w.w;
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
-          s.v[4 * t + r][i] = reinterpret_cast<const uint32_t*>(vp + r * D)[i];
+          s.v[4 * t + r][i] = reinterpret_cast<const uint32_t*>(vp + v_lane + r * D)[i];
     }
   };
 
-  for (int64_t t0 = begin + wave * kStep; t0 < end; t0 += kRound) {
-    StepCodes<D> s;
-    load_step(t0, s);
-    const bool edge = t0 < lo || t0 + kStep > len || s.ks[0] < 0.f || s.ks[1] < 0.f;
+  auto compute = [&](const Round& u, StepCodes<D>& s) {
+    const int64_t t0 = u.token + wave * kStep, lo = u.lo, len = u.len;
+    if (t0 >= len) return;                  // (the wave has no token of this round)
+    const bool edge = t0 < lo || t0 + kStep > len || !s.there[0] || !s.there[1];
 
     // scores of query j: x[4 t + r] is token t0 + 16 t + 4 g + r, in log2 units
     float x[8];
@@ -188,7 +300,7 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(AttnDecodeArgs p,
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t tok = t0 + 16 * (i / 4) + 4 * g + i % 4;
-        const bool seen = tok >= lo && tok < len && s.ks[i / 4] >= 0.f;
+        const bool seen = tok >= lo && tok < len && s.there[i / 4];
         if (!seen) {
           x[i] = -__builtin_huge_valf();
 #pragma unroll
@@ -198,16 +310,19 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(AttnDecodeArgs p,
     }
     float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
                      fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float m_new = fmaxf(m, mx);
-    const float alpha = exp2_fast(m - m_new);
-    m = m_new;
-    l *= alpha;
+    mx = over_halves(over_rows(mx));
+    // The sums are kept relative to m, which need not be the maximum: it is
+    // moved only when a score passes it by 2^8.
+    if (__any(mx > m + 8.f)) {
+      const float m_new = fmaxf(m, mx);
+      const float alpha = exp2_fast(m - m_new);
+      m = m_new;
+      l *= alpha;
 #pragma unroll
-    for (int c = 0; c < MT; ++c)
+      for (int c = 0; c < MT; ++c)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[c][r] *= alpha;
+        for (int r = 0; r < 4; ++r) o[c][r] *= alpha;
+    }
 
     bf16x8 w[NT];
 #pragma unroll
@@ -234,68 +349,119 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(AttnDecodeArgs p,
         for (int c = NT - 1; c >= 0; --c) o[4 * cc + i] = mfma(va, w[c], o[4 * cc + i]);
       }
     }
-  }
+  };
 
-  // join the waves: o[c][r] is column (4 g + r) D/16 + c of query j
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+  // Joins the waves and writes this workgroup's part of a segment that `u` ends
+  // here.  o[c][r] is column (4 g + r) D/16 + c of query j.
+  auto flush = [&](const Round& u, bool from_start) {
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    __syncthreads();                        // the last flush has been read
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int c = 0; c < MT; c += 4) {
-      float* dst = &s_o[wave][j][(4 * g + r) * MT + c];
-      lds_check(dst, 16);
-      *reinterpret_cast<float4*>(dst) = make_float4(o[c][r], o[c + 1][r], o[c + 2][r], o[c + 3][r]);
+      for (int c = 0; c < MT; c += 4) {
+        float* dst = &s_o[wave][j][(4 * g + r) * MT + c];
+        lds_check(dst, 16);
+        *reinterpret_cast<float4*>(dst) =
+            make_float4(o[c][r], o[c + 1][r], o[c + 2][r], o[c + 3][r]);
+      }
+    if (g == 0) { s_m[wave][j] = m; s_l[wave][j] = l; }
+    __syncthreads();
+    const bool to_end = u.r == u.rounds - 1;
+    const int gn = G - 16 * u.qg < 16 ? G - 16 * u.qg : 16;
+    constexpr int LPQ = D / 4;              // threads of a query, 4 columns each
+    for (int qi = tid / LPQ; qi < gn; qi += kThreads / LPQ) {
+      const int col = 4 * (tid % LPQ);
+      float mm = kNone, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, s_m[w][qi]);
+      float r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = exp2_fast(s_m[w][qi] - mm);
+        ll += f * s_l[w][qi];
+        const float4 x = *reinterpret_cast<const float4*>(&s_o[w][qi][col]);
+        r[0] += f * x.x; r[1] += f * x.y; r[2] += f * x.z; r[3] += f * x.w;
+      }
+      if (from_start && to_end) {
+        const int64_t row = (int64_t)u.n * p.Hq + u.hk * G + 16 * u.qg + qi;
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;          // no token seen: o = 0
+        store4<T>(static_cast<T*>(p.o) + row * D + col, r[0] * inv, r[1] * inv, r[2] * inv,
+                  r[3] * inv);
+      } else {
+        float* part = part_at<D>(p.ws, prows, blockIdx.x, from_start ? 1 : 0, qi);
+        *reinterpret_cast<float4*>(part + col) = make_float4(r[0], r[1], r[2], r[3]);
+        if (col == 0) { part[D] = mm; part[D + 1] = ll; }
+      }
     }
-  if (g == 0) { s_m[wave][j] = m; s_l[wave][j] = l; }
-  __syncthreads();
-  constexpr int LPQ = D / 4;              // threads of a query, 4 columns each
-  for (int qi = tid / LPQ; qi < gn; qi += kThreads / LPQ) {
-    const int col = 4 * (tid % LPQ);
-    float mm = kNone, ll = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, s_m[w][qi]);
-    float r[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = exp2_fast(s_m[w][qi] - mm);
-      ll += f * s_l[w][qi];
-      const float4 u = *reinterpret_cast<const float4*>(&s_o[w][qi][col]);
-      r[0] += f * u.x; r[1] += f * u.y; r[2] += f * u.z; r[3] += f * u.w;
+  };
+
+  int e[2];
+  StepCodes<D> sa, sb;
+  entries(cur, e);
+  load_queries(cur);
+  reset();
+  load_step(cur, e, sa);
+  Round next = cur;
+  if (count > 1) { next = advance(cur); entries(next, e); }
+  bool from_start = cur.r == 0;
+  bool chained = false;                     // the last segment goes on in the next workgroup
+  auto step = [&](int i, StepCodes<D>& s, StepCodes<D>& sn) {
+    Round after = next;
+    if (i + 1 < count) {
+      load_step(next, e, sn);
+      if (i + 2 < count) { after = advance(next); entries(after, e); }
     }
-    const int64_t row = n * p.Hq + hk * G + g0 + qi;
-    if (only) {
-      const float inv = ll > 0.f ? 1.f / ll : 0.f;            // no token seen: o = 0
-      store4<T>(static_cast<T*>(p.o) + row * D + col, r[0] * inv, r[1] * inv, r[2] * inv, r[3] * inv);
-    } else {
-      float* part = p.ws + (row * splits + split) * (D + 4);
-      *reinterpret_cast<float4*>(part + col) = make_float4(r[0], r[1], r[2], r[3]);
-      if (col == 0) { part[D] = mm; part[D + 1] = ll; }
+    compute(cur, s);
+    const bool ends = cur.r == cur.rounds - 1;
+    if (ends || i + 1 == count) {
+      flush(cur, from_start);
+      chained = !ends && from_start;
+      if (i + 1 < count) {
+        load_queries(next);
+        reset();
+        from_start = true;
+      }
     }
+    if (i + 1 < count) cur = next;
+    next = after;
+  };
+  for (int i = 0; i < count; i += 2) {
+    step(i, sa, sb);
+    if (i + 1 < count) step(i + 1, sb, sa);
+  }
+  if (!direct && tid == 0) {
+    // the rounds of the segment from here on end with round at + count - 1 + left
+    const int left = cur.rounds - 1 - cur.r;
+    const int seg = cur.n * (int)per_seq + cur.hk * qgroups + cur.qg;
+    *chain_at(p.ws, prows, D, gridDim.x, blockIdx.x) =
+        chained ? make_int2(seg, (at + count - 1 + left) / share) : make_int2(-1, 0);
   }
 }
 
-// Joins the partial results of a sequence's splits: one workgroup for each
-// query row, its threads over (split mod groups, 4 columns).
+// Joins the parts of the segments that lie in several workgroups: a workgroup
+// of the first kernel that begins one, and a query of its group (grid y); the
+// threads go over parts (mod the groups) and 4 columns.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, int splits,
-                                                             int64_t span) {
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, int qgroups,
+                                                             int rows) {
   constexpr int LPQ = D / 4, GR = kThreads / LPQ;
   __shared__ float s_o[GR][D];
   __shared__ float s_l[GR], s_m[GR];
-  const int64_t row = blockIdx.x;
-  const int64_t n = row / p.Hq;
-  const PagedCache& kv = p.cache;
-  const DecodeSpan sp =
-      decode_span(kv.seq_lens[n], kv.max_pages, kv.page_size, p.window, 0, span, kStep);
-  if (sp.only) return;                    // written whole by its one split
-  const int ns = (int)((sp.len - sp.begin + span - 1) / span);
+  const int2 chain = *chain_at(p.ws, rows, D, gridDim.x, blockIdx.x);
+  if (chain.x < 0) return;
+  const int G = p.Hq / p.Hk, qi = blockIdx.y;
+  const int per_seq = p.Hk * qgroups;
+  const int n = chain.x / per_seq, hk = (chain.x - n * per_seq) / qgroups, qg = chain.x % qgroups;
+  if (16 * qg + qi >= G) return;
+  const int parts = chain.y - (int)blockIdx.x + 1;
   const int gr = threadIdx.x / LPQ, col = 4 * (threadIdx.x % LPQ);
-  const float* part = p.ws + row * splits * (D + 4);
   float mm = kNone, ll = 0.f, r[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = gr; s < ns; s += GR) {
-    const float ms = part[s * (D + 4) + D], ls = part[s * (D + 4) + D + 1];
-    const float4 u = *reinterpret_cast<const float4*>(part + s * (D + 4) + col);
+  for (int i = gr; i < parts; i += GR) {
+    const float* part = part_at<D>(p.ws, rows, blockIdx.x + i, i == 0 ? 1 : 0, qi);
+    const float ms = part[D], ls = part[D + 1];
+    const float4 u = *reinterpret_cast<const float4*>(part + col);
     const float m2 = fmaxf(mm, ms);
     const float f0 = exp2_fast(mm - m2), f1 = exp2_fast(ms - m2);
     mm = m2;
@@ -317,46 +483,39 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, i
     r[0] += f * u.x; r[1] += f * u.y; r[2] += f * u.z; r[3] += f * u.w;
   }
   const float inv = ll > 0.f ? 1.f / ll : 0.f;
+  const int64_t row = (int64_t)n * p.Hq + hk * G + 16 * qg + qi;
   store4<T>(static_cast<T*>(p.o) + row * D + col, r[0] * inv, r[1] * inv, r[2] * inv, r[3] * inv);
 }
 
 template <typename T, int D>
 hipError_t launch_t(const AttnDecodeArgs& a, hipStream_t stream) {
-  const AttnDecodeSplit sp = attn_decode_split(a.N, a.cache.max_pages * a.cache.page_size, a.window,
+  const AttnDecodePlan plan = attn_decode_plan(a.N, a.cache.max_pages * a.cache.page_size, a.window,
                                                a.Hq, a.Hk, D);
-  const int qgroups = (a.Hq / a.Hk + 15) / 16;
-  const int64_t blocks = a.N * a.Hk * qgroups * sp.splits;
-  attn_decode_kernel<T, D><<<dim3((unsigned)blocks), kThreads, 0, stream>>>(
-      a, qgroups, (int)sp.splits, sp.span);
+  const int G = a.Hq / a.Hk, qgroups = (G + 15) / 16, rows = G < 16 ? G : 16;
+  attn_decode_kernel<T, D><<<dim3((unsigned)plan.blocks), kThreads, 0, stream>>>(
+      a, qgroups, plan.ws_floats == 0);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || sp.splits == 1) return e;
-  attn_join_kernel<T, D><<<dim3((unsigned)(a.N * a.Hq)), kThreads, 0, stream>>>(
-      a, (int)sp.splits, sp.span);
+  if (e != hipSuccess || plan.ws_floats == 0) return e;
+  attn_join_kernel<T, D><<<dim3((unsigned)plan.blocks, (unsigned)rows), kThreads, 0, stream>>>(
+      a, qgroups, rows);
   return hipGetLastError();
 }
 
 }  // namespace
 
 // The tokens that a sequence can hold are known on the host (the width of the
-// page table), its length is not.  Spans are as long as leaves kTarget
-// workgroups if all sequences are full, and at least kLeast tokens: a span's
-// partial result costs 2 (D + 4) 4 bytes for each query head against
-// 2 D bytes for each token.
-AttnDecodeSplit attn_decode_split(int64_t N, int64_t max_tokens, int64_t window, int Hq, int Hk,
-                                  int d) {
-  constexpr int64_t kTarget = 2048, kLeast = 512;
+// page table), its length is not.
+AttnDecodePlan attn_decode_plan(int64_t N, int64_t max_tokens, int64_t window, int Hq, int Hk,
+                                int d) {
   if (window > 0 && window + kStep < max_tokens) max_tokens = window + kStep;
-  const int64_t groups = N * Hk * ((Hq / Hk + 15) / 16);
-  int64_t want = groups > 0 ? kTarget / groups : 1;
-  if (want < 1) want = 1;
-  int64_t span = (max_tokens + want - 1) / want;
-  if (span < kLeast) span = kLeast;
-  span = (span + kRound - 1) / kRound * kRound;
-  AttnDecodeSplit s;
-  s.splits = (max_tokens + span - 1) / span;
-  s.span = span;
-  s.ws_floats = s.splits > 1 ? N * Hq * s.splits * (d + 4) : 0;
-  return s;
+  const int64_t G = Hq / Hk, segments = N * Hk * ((G + 15) / 16);
+  const int64_t rounds = segments * ((max_tokens + kRound - 1) / kRound);
+  AttnDecodePlan p{segments, rounds, 0};
+  if (max_tokens <= kDirect) return p;
+  const int64_t want = (rounds + kLeast - 1) / kLeast;
+  p.blocks = want < kBlocks ? want : kBlocks;
+  p.ws_floats = p.blocks * (2 * (G < 16 ? G : 16) * (d + 4) + 2);
+  return p;
 }
 
 hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t stream) {

@@ -103,22 +103,27 @@ GDN_HD AppendPage append_page(int64_t seq_len, int64_t max_pages, int P, int64_t
   return r;
 }
 
-// Tokens [lo, len) that a decode step sees, and split `split`'s [begin, end)
-// of them, where splits start at multiples of `step`.
+// Tokens [lo, len) that a decode step sees.  They are taken in rounds of
+// `round` tokens from `first` on, a multiple of `step`; a sequence without
+// tokens has one (empty) round.
 struct DecodeSpan {
-  int64_t len, lo, begin, end;
-  bool only;      // one split sees everything
+  int64_t len, lo, first;
+  GDN_HD int rounds(int round) const {
+    const int64_t r = (len - first + round - 1) / round;
+    return r > 0 ? (int)r : 1;
+  }
 };
 GDN_HD DecodeSpan decode_span(int64_t seq_len, int64_t max_pages, int P, int64_t window,
-                              int64_t split, int64_t span, int step) {
+                              int step) {
   DecodeSpan r;
   r.len = clamp_i64(seq_len, 0, max_pages * P);
   r.lo = window && r.len > window ? r.len - window : 0;
-  const int64_t first = r.lo / step * step;
-  r.begin = first + split * span;
-  r.end = r.begin + span < r.len ? r.begin + span : r.len;
-  r.only = first + span >= r.len;
+  r.first = r.lo / step * step;
   return r;
+}
+GDN_HD int decode_rounds(int64_t seq_len, int64_t max_pages, int P, int64_t window, int round,
+                         int step) {
+  return decode_span(seq_len, max_pages, P, window, step).rounds(round);
 }
 
 }  // namespace gdn

@@ -69,16 +69,16 @@ struct AttnDecodeArgs {
   const void* q;
   PagedCache cache;                   // read only
   void* o;
-  float* ws;                          // attn_decode_split(...) partials
+  float* ws;                          // attn_decode_plan(...).ws_floats
 };
 
-// How a decode call divides the caches: `splits` workgroups for each sequence,
-// key head and 16 query heads of its group, `span` tokens each.
-struct AttnDecodeSplit {
-  int64_t splits, span, ws_floats;
+// How a decode call divides the caches: its workgroups, the most rounds of
+// work there can be (fits in 32 bits, checked by the caller) and the workspace.
+struct AttnDecodePlan {
+  int64_t blocks, rounds, ws_floats;
 };
-AttnDecodeSplit attn_decode_split(int64_t N, int64_t max_tokens, int64_t window, int Hq, int Hk,
-                                  int d);
+AttnDecodePlan attn_decode_plan(int64_t N, int64_t max_tokens, int64_t window, int Hq, int Hk,
+                                int d);
 
 // Workgroups of a launch (checked against the grid limit by the caller).
 int64_t qk_norm_rope_blocks(int64_t rows, int Hq, int Hk, int d);

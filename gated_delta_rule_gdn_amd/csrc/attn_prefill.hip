@@ -280,12 +280,6 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
 
-// Maximum over the two lanes 32 apart.
-__device__ __forceinline__ float over_halves(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-
 // The loop over key tiles is pipelined by hand: while the weights of tile i
 // are formed (VALU), the scores of tile i + 1 are on the matrix cores, and
 // while the maximum of tile i + 1 is formed, tile i's product with V is.  K

@@ -144,30 +144,27 @@ void ranked_tiles(std::mt19937& r, bool good) {   // the same tiles, the late on
 }
 
 void decode(std::mt19937& r) {
-  const int P = 16 << (r() % 4), step = 32;
-  const int64_t width = 1 + r() % 50, cap = width * P, span = 128 * (1 + r() % 5);
+  const int P = 16 << (r() % 4), step = 32, round = 128;
+  const int64_t width = 1 + r() % 50, cap = width * P;
   const int64_t window = r() % 2 ? 0 : 1 + r() % (2 * cap);
   int64_t len = (int64_t)(r() % (2 * cap + 40)) - 20;
   if (r() % 20 == 0) len = r() % 2 ? INT64_MAX : INT64_MIN;
-  const int64_t most = window > 0 && window + step < cap ? window + step : cap;
-  const int64_t splits = (most + span - 1) / span;
   const int64_t L = clamp_i64(len, 0, cap), lo = window && L > window ? L - window : 0;
+  const DecodeSpan d = decode_span(len, width, P, window, step);
+  need(d.len == L && d.lo == lo && d.first <= lo && d.first % step == 0 && d.first > lo - step, "range");
+  const int rounds = decode_rounds(len, width, P, window, round, step);
+  const int64_t most = window > 0 && window + step < cap ? window + step : cap;
+  need(rounds >= 1 && rounds <= (most + round - 1) / round, "rounds within what the host expects");
   std::vector<int> seen(cap, 0);
-  int64_t active = 0;
-  for (int64_t s = 0; s < splits; ++s, ++items) {
-    const DecodeSpan d = decode_span(len, width, P, window, s, span, step);
-    need(d.len == L && d.lo == lo && d.lo >= 0 && d.len <= cap, "range");
-    if (d.begin < d.end) ++active;
-    for (int64_t t0 = d.begin; t0 < d.end; t0 += step) {
-      need(t0 % step == 0 && t0 >= 0 && t0 / P < width, "step within the page table");
-      for (int64_t t = t0; t < t0 + step && t < d.len; ++t)
-        if (t >= d.lo) { need(t < d.end, "token within the split"); ++seen[t]; }
-    }
-    need(d.only == (L - lo / step * step <= span), "one split");
-  }
+  for (int i = 0; i < rounds; ++i, ++items)
+    for (int64_t t0 = d.first + (int64_t)i * round; t0 < d.first + (int64_t)(i + 1) * round; t0 += step)
+      for (int64_t tile = t0; tile < t0 + step; tile += 16) {
+        if (tile >= d.len) continue;
+        need(tile >= 0 && tile / P < width && tile % P + 16 <= P, "tile within a page of the table");
+        for (int64_t t = tile; t < tile + 16; ++t)
+          if (t >= d.lo && t < d.len) ++seen[t];
+      }
   for (int64_t t = 0; t < cap; ++t) need(seen[t] == (t >= lo && t < L), "each token seen once");
-  const DecodeSpan d0 = decode_span(len, width, P, window, 0, span, step);
-  if (!d0.only) need((d0.len - d0.begin + span - 1) / span == active && active <= splits, "splits joined");
 }
 }  // namespace
 

@@ -17,9 +17,10 @@ int64_t kv_append_slots(int64_t N, int64_t total_T, int64_t Tseq, bool packed, i
 int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType) {
   return (packed ? total_T / 64 + N : N * ((Tseq + 63) / 64)) * Hq;
 }
-AttnDecodeSplit attn_decode_split(int64_t N, int64_t max_tokens, int64_t, int Hq, int, int d) {
-  const int64_t s = (max_tokens + 511) / 512;
-  return AttnDecodeSplit{s, 512, s > 1 ? N * Hq * s * (d + 4) : 0};
+AttnDecodePlan attn_decode_plan(int64_t N, int64_t max_tokens, int64_t, int Hq, int Hk, int d) {
+  const int64_t rounds = N * Hk * ((Hq / Hk + 15) / 16) * ((max_tokens + 127) / 128);
+  const int64_t b = rounds < 512 ? rounds : 512;
+  return AttnDecodePlan{b, rounds, max_tokens > 512 ? b * (2 * 16 * (d + 4) + 2) : 0};
 }
 hipError_t launch_qk_norm_rope(const QkNormRopeArgs&, hipStream_t) { ++g_launches; return hipSuccess; }
 hipError_t launch_kv_append(const KvAppendArgs&, hipStream_t) { ++g_launches; return hipSuccess; }
