@@ -39,12 +39,8 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kStep = 32;                 // tokens of a wave's step
 constexpr int kRound = kWaves * kStep;    // tokens of a workgroup's step
-#ifndef KB_BLOCKS
-#define KB_BLOCKS 512
-#define KB_LEAST 4
-#endif
-constexpr int64_t kBlocks = KB_BLOCKS;           // workgroups that fill the chip: 2 to a CU
-constexpr int kLeast = KB_LEAST;                 // rounds that are worth a workgroup
+constexpr int64_t kBlocks = 512;         // workgroups that fill the chip: 2 to a CU
+constexpr int kLeast = 4;                // rounds that are worth a workgroup
 constexpr int64_t kDirect = 4 * kRound;   // tokens of a cache that one workgroup takes whole
 constexpr float kNone = -1e30f;           // running maximum (log2 units) before any token
 
@@ -440,51 +436,116 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
   }
 }
 
-// Joins the parts of the segments that lie in several workgroups: a workgroup
-// of the first kernel that begins one, and a query of its group (grid y); the
-// threads go over parts (mod the groups) and 4 columns.
-template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, int qgroups,
-                                                             int rows) {
-  constexpr int LPQ = D / 4, GR = kThreads / LPQ;
-  __shared__ float s_o[GR][D];
-  __shared__ float s_l[GR], s_m[GR];
-  const int2 chain = *chain_at(p.ws, rows, D, gridDim.x, blockIdx.x);
-  if (chain.x < 0) return;
-  const int G = p.Hq / p.Hk, qi = blockIdx.y;
-  const int per_seq = p.Hk * qgroups;
-  const int n = chain.x / per_seq, hk = (chain.x - n * per_seq) / qgroups, qg = chain.x % qgroups;
-  if (16 * qg + qi >= G) return;
-  const int parts = chain.y - (int)blockIdx.x + 1;
-  const int gr = threadIdx.x / LPQ, col = 4 * (threadIdx.x % LPQ);
-  float mm = kNone, ll = 0.f, r[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = gr; i < parts; i += GR) {
-    const float* part = part_at<D>(p.ws, rows, blockIdx.x + i, i == 0 ? 1 : 0, qi);
-    const float ms = part[D], ls = part[D + 1];
-    const float4 u = *reinterpret_cast<const float4*>(part + col);
-    const float m2 = fmaxf(mm, ms);
-    const float f0 = exp2_fast(mm - m2), f1 = exp2_fast(ms - m2);
-    mm = m2;
-    ll = ll * f0 + ls * f1;
+// Joins the parts of the segments that lie in several workgroups.  Every
+// workgroup reads which of the first kernel's begin such a segment, and they
+// share the work.  Few segments (of many parts): a workgroup takes 32 columns
+// of one query, 8 lanes for each of 32 parts at a time.  Many (of few parts):
+// a wave takes a query, D/4 lanes for each part.  (128K tokens of one
+// sequence, 4 segments of 128 parts: 10.9 us with a workgroup to a query,
+// 6.0 us.)
+constexpr int kJoinBlocks = 1024;
+constexpr int kManyChains = 64;
+
+template <int D>
+struct JoinSum {
+  float m = kNone, l = 0.f, r[4] = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(float m1, float l1, float4 u) {
+    const float m2 = fmaxf(m, m1);
+    const float f0 = exp2_fast(m - m2), f1 = exp2_fast(m1 - m2);
+    m = m2;
+    l = l * f0 + l1 * f1;
     r[0] = r[0] * f0 + u.x * f1; r[1] = r[1] * f0 + u.y * f1;
     r[2] = r[2] * f0 + u.z * f1; r[3] = r[3] * f0 + u.w * f1;
   }
-  *reinterpret_cast<float4*>(&s_o[gr][col]) = make_float4(r[0], r[1], r[2], r[3]);
-  if (col == 0) { s_m[gr] = mm; s_l[gr] = ll; }
-  __syncthreads();
-  if (gr != 0) return;
-  for (int w = 0; w < GR; ++w) mm = fmaxf(mm, s_m[w]);
-  ll = 0.f;
-  r[0] = r[1] = r[2] = r[3] = 0.f;
-  for (int w = 0; w < GR; ++w) {
-    const float f = exp2_fast(s_m[w] - mm);
-    ll += f * s_l[w];
-    const float4 u = *reinterpret_cast<const float4*>(&s_o[w][col]);
-    r[0] += f * u.x; r[1] += f * u.y; r[2] += f * u.z; r[3] += f * u.w;
+  // parts first, first + by, ... of the chain that begins in `block`
+  __device__ __forceinline__ void gather(float* ws, int rows, int block, int parts, int qi, int col,
+                                         int first, int by) {
+#pragma unroll 4
+    for (int i = first; i < parts; i += by) {
+      const float* part = part_at<D>(ws, rows, block + i, i == 0 ? 1 : 0, qi);
+      add(part[D], part[D + 1], *reinterpret_cast<const float4*>(part + col));
+    }
   }
-  const float inv = ll > 0.f ? 1.f / ll : 0.f;
-  const int64_t row = (int64_t)n * p.Hq + hk * G + 16 * qg + qi;
-  store4<T>(static_cast<T*>(p.o) + row * D + col, r[0] * inv, r[1] * inv, r[2] * inv, r[3] * inv);
+};
+
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, int qgroups,
+                                                             int rows, int blocks) {
+  __shared__ int s_start[kBlocks], s_end[kBlocks], s_seg[kBlocks], s_count[kBlocks / 64];
+  __shared__ float s_o[32][36], s_m[32], s_l[32];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // the workgroups that begin a segment others go on with, in order
+  int2 chain[kBlocks / kThreads];
+#pragma unroll
+  for (int i = 0; i < kBlocks / kThreads; ++i) {
+    const int b = i * kThreads + tid;
+    chain[i] = b < blocks ? *chain_at(p.ws, rows, D, blocks, b) : make_int2(-1, 0);
+    const uint64_t m = __ballot(chain[i].x >= 0);
+    if (lane == 0) s_count[i * kWaves + wave] = __popcll(m);
+  }
+  __syncthreads();
+  int chains = 0;
+#pragma unroll
+  for (int i = 0; i < kBlocks / kThreads; ++i) {
+    const uint64_t m = __ballot(chain[i].x >= 0);
+    int before = 0;
+    for (int w = 0; w < i * kWaves + wave; ++w) before += s_count[w];
+    if (chain[i].x >= 0) {
+      const int k = before + __popcll(m & ((1ull << lane) - 1));
+      s_start[k] = i * kThreads + tid;
+      s_end[k] = chain[i].y;
+      s_seg[k] = chain[i].x;
+    }
+  }
+  for (int w = 0; w < kBlocks / 64; ++w) chains += s_count[w];
+  __syncthreads();
+
+  const int G = p.Hq / p.Hk, per_seq = p.Hk * qgroups;
+  auto out_row = [&](int seg, int qi) -> int64_t {   // -1: not a query of the group
+    const int n = seg / per_seq, hk = (seg - n * per_seq) / qgroups, qg = seg % qgroups;
+    return 16 * qg + qi < G ? (int64_t)n * p.Hq + hk * G + 16 * qg + qi : -1;
+  };
+  auto write = [&](int64_t row, int col, const JoinSum<D>& a) {
+    const float inv = a.l > 0.f ? 1.f / a.l : 0.f;
+    store4<T>(static_cast<T*>(p.o) + row * D + col, a.r[0] * inv, a.r[1] * inv, a.r[2] * inv,
+              a.r[3] * inv);
+  };
+  if (chains > kManyChains) {
+    constexpr int LPQ = D / 4;
+    const int col = 4 * (lane % LPQ);
+    for (int it = blockIdx.x * kWaves + wave; it < chains * rows; it += gridDim.x * kWaves) {
+      const int k = it / rows, qi = it - k * rows;
+      const int64_t row = out_row(s_seg[k], qi);
+      if (row < 0) continue;
+      JoinSum<D> a;
+      a.gather(p.ws, rows, s_start[k], s_end[k] - s_start[k] + 1, qi, col, lane / LPQ, 64 / LPQ);
+#pragma unroll
+      for (int off = 32; off >= LPQ; off >>= 1) {
+        const float4 u = make_float4(__shfl_xor(a.r[0], off), __shfl_xor(a.r[1], off),
+                                     __shfl_xor(a.r[2], off), __shfl_xor(a.r[3], off));
+        const float m1 = __shfl_xor(a.m, off), l1 = __shfl_xor(a.l, off);
+        a.add(m1, l1, u);
+      }
+      if (lane < LPQ) write(row, col, a);
+    }
+    return;
+  }
+  constexpr int CP = D / 32;                // column parts
+  const int gr = tid / 8, c4 = 4 * (tid % 8);
+  for (int it = blockIdx.x; it < chains * rows * CP; it += gridDim.x) {
+    const int k = it / (rows * CP), qi = it / CP % rows, col = 32 * (it % CP) + c4;
+    const int64_t row = out_row(s_seg[k], qi);
+    JoinSum<D> a;
+    if (row >= 0) a.gather(p.ws, rows, s_start[k], s_end[k] - s_start[k] + 1, qi, col, gr, 32);
+    *reinterpret_cast<float4*>(&s_o[gr][c4]) = make_float4(a.r[0], a.r[1], a.r[2], a.r[3]);
+    if (c4 == 0) { s_m[gr] = a.m; s_l[gr] = a.l; }
+    __syncthreads();
+    if (tid < 8 && row >= 0) {
+      for (int w = 1; w < 32; ++w) a.add(s_m[w], s_l[w], *reinterpret_cast<const float4*>(&s_o[w][c4]));
+      write(row, col, a);
+    }
+    __syncthreads();
+  }
 }
 
 template <typename T, int D>
@@ -496,8 +557,8 @@ hipError_t launch_t(const AttnDecodeArgs& a, hipStream_t stream) {
       a, qgroups, plan.ws_floats == 0);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.ws_floats == 0) return e;
-  attn_join_kernel<T, D><<<dim3((unsigned)plan.blocks, (unsigned)rows), kThreads, 0, stream>>>(
-      a, qgroups, rows);
+  attn_join_kernel<T, D><<<dim3(kJoinBlocks), kThreads, 0, stream>>>(a, qgroups, rows,
+                                                                     (int)plan.blocks);
   return hipGetLastError();
 }
 

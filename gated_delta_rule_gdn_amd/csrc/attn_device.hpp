@@ -12,16 +12,40 @@ namespace gdn {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// Item idx of packed offsets (find_packed_by): the wave probes 64 sequences at
-// a time and every lane gets the answer.
+__device__ __forceinline__ int64_t read_lane(int64_t x, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)x >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// Item idx of packed offsets (find_packed_by), and lens[n] where lens is given.
+// Up to 63 sequences are read by the lanes of a wave at once, lengths with
+// them, and the answer comes from the lanes: one memory latency.  More are
+// probed 64 at a time; every lane gets the answer.
 __device__ __forceinline__ PackedItem find_packed(const int64_t* __restrict__ cu, int64_t N,
-                                                  int64_t total, int unit, int extra,
-                                                  int64_t idx) {
+                                                  int64_t total, int unit, int extra, int64_t idx,
+                                                  const int64_t* __restrict__ lens = nullptr,
+                                                  int64_t* len = nullptr) {
   const int lane = threadIdx.x & 63;
-  return find_packed_by(cu, N, total, unit, extra, idx, [&](int64_t lo, int64_t step, int64_t hi) {
-    const int64_t i = lo + lane * step;
-    return (uint64_t)__ballot(i < hi && packed_at_or_before(cu, i, total, unit, extra, idx));
-  });
+  if (N < 64) {
+    const int64_t c = clamp_i64(cu[lane < N ? lane : N], 0, total);
+    const int64_t s = lens ? lens[lane < N ? lane : N - 1] : 0;
+    const uint64_t m = __ballot(lane < N && c / unit + extra * lane <= idx);
+    PackedItem r;
+    r.n = m ? 63 - __builtin_clzll(m) : 0;
+    r.start = read_lane(c, (int)r.n);
+    r.end = read_lane(c, (int)r.n + 1);
+    r.item = idx - (r.start / unit + extra * r.n);
+    if (lens) *len = read_lane(s, (int)r.n);
+    return r;
+  }
+  const PackedItem r =
+      find_packed_by(cu, N, total, unit, extra, idx, [&](int64_t lo, int64_t step, int64_t hi) {
+        const int64_t i = lo + lane * step;
+        return (uint64_t)__ballot(i < hi && packed_at_or_before(cu, i, total, unit, extra, idx));
+      });
+  if (lens) *len = lens[r.n];
+  return r;
 }
 
 // Sum over the wave: within the rows of 16 lanes by DPP moves, then four lanes.

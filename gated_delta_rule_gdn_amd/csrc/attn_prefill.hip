@@ -110,30 +110,55 @@ __device__ __forceinline__ Tile find_tile(const PrefillArgs& p, uint32_t blocks)
 }
 
 // ---------------------------------------------------------------------------
-// fp32: v_mfma_f32_16x16x4_f32, 16 queries to a wave, 64 to a workgroup, key
-// tiles of 32 tokens in LDS.
+// fp32: v_mfma_f32_16x16x4_f32.  A workgroup has 32 queries; waves 0 and 1 take
+// 16 each over the first 16 tokens of every key tile of 32, waves 2 and 3 the
+// same queries over the other 16, with a running maximum and sum of their own,
+// and the pairs join through LDS at the end.  Short prompts have few query
+// tiles, and this halves the time that one takes.  The next key tile is loaded
+// into registers while this one is computed.
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ __launch_bounds__(kThreads) void prefill_f32_kernel(PrefillArgs p, uint32_t blocks) {
-  constexpr int BM = 64, BN = 32, LD = D + 4, KB = D / 32, MT = D / 16;
+  constexpr int BM = 32, BN = 32, LD = D + 4, KB = D / 32, MT = D / 16;
+  constexpr int NL = BN * D / 4 / kThreads;           // 16-byte loads of a thread and tile
   __shared__ __align__(16) float s_k[BN * LD], s_v[BN * LD];
+  __shared__ float s_m[32], s_l[32];
   lds_nan_fill(s_k, sizeof s_k);
   lds_nan_fill(s_v, sizeof s_v);
   const Tile tl = find_tile<BM>(p, blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wq = wave & 1, wk = wave >> 1;
   const int g = lane >> 4, j = lane & 15;
   const int hk = tl.hq / (p.Hq / p.Hk);
-  const int64_t q0 = tl.q0 + 16 * wave;     // the wave's first query
-  const int64_t tq = q0 + j;                // this lane's query
+  const int L = (int)tl.L;
+  const int q0 = (int)tl.q0 + 16 * wq;      // the wave's first query
+  const int tq = q0 + j;                    // this lane's query
   const float* kb_ = static_cast<const float*>(p.k) + tl.a * p.ld_k + hk * D;
   const float* vb_ = static_cast<const float*>(p.v) + tl.a * p.ld_v + hk * D;
 
+  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
+  int lo = window ? (int)tl.q0 - window + 1 : 0;      // first key that the tile sees
+  lo = lo < 0 ? 0 : lo / BN * BN;
+  const int stop = (int)tl.q0 + BM < L ? (int)tl.q0 + BM : L;
+  float4 kr[NL], vr[NL];
+  auto load_tile = [&](int k0) {            // rows past the sequence are zero: they may
+#pragma unroll                              // belong to another one
+    for (int e = 0; e < NL; ++e) {
+      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+      kr[e] = vr[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + row < L) {
+        kr[e] = *reinterpret_cast<const float4*>(kb_ + (int64_t)(k0 + row) * p.ld_k + c);
+        vr[e] = *reinterpret_cast<const float4*>(vb_ + (int64_t)(k0 + row) * p.ld_v + c);
+      }
+    }
+  };
+  load_tile(lo);
   Frag8<float> q[KB];
   {
-    const float flip = p.scale < 0.f ? -1.f : 1.f;
-    const int64_t row = tq < tl.L ? tq : tl.L - 1;
+    const float flip = p.scale < 0.f ? -1.f : 1.f;    // the scale below is positive
+    const int row = tq < L ? tq : L - 1;
     const float* qp = static_cast<const float*>(p.q) + (tl.a + row) * p.ld_q + tl.hq * D + 8 * g;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
@@ -148,74 +173,84 @@ __global__ __launch_bounds__(kThreads) void prefill_f32_kernel(PrefillArgs p, ui
   for (int c = 0; c < MT; ++c) o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = kNone, l = 0.f;
 
-  int64_t lo = p.window ? tl.q0 - p.window + 1 : 0;   // first key that the tile sees
-  lo = lo < 0 ? 0 : lo / BN * BN;
-  const int64_t stop = tl.q0 + BM < tl.L ? tl.q0 + BM : tl.L;
-  for (int64_t k0 = lo; k0 < stop; k0 += BN) {
+  for (int k0 = lo; k0 < stop; k0 += BN) {
     __syncthreads();
-    // rows past the sequence are zero: they may belong to another one
-    for (int e = tid; e < BN * D / 4; e += kThreads) {
-      const int row = e / (D / 4), c = 4 * (e % (D / 4));
-      float4 ku = make_float4(0.f, 0.f, 0.f, 0.f), vu = ku;
-      if (k0 + row < tl.L) {
-        ku = *reinterpret_cast<const float4*>(kb_ + (k0 + row) * p.ld_k + c);
-        vu = *reinterpret_cast<const float4*>(vb_ + (k0 + row) * p.ld_v + c);
-      }
+#pragma unroll
+    for (int e = 0; e < NL; ++e) {
+      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
       lds_check(s_k + row * LD + c, 16);
-      *reinterpret_cast<float4*>(s_k + row * LD + c) = ku;
-      *reinterpret_cast<float4*>(s_v + row * LD + c) = vu;
+      *reinterpret_cast<float4*>(s_k + row * LD + c) = kr[e];
+      *reinterpret_cast<float4*>(s_v + row * LD + c) = vr[e];
     }
     __syncthreads();
-    if (k0 > q0 + 15 || (p.window && k0 + BN - 1 <= q0 - p.window)) continue;   // nothing seen
-    float x[2][4];
-    float mx = -__builtin_huge_valf();
+    if (k0 + BN < stop) load_tile(k0 + BN);
+    const int kw = k0 + 16 * wk;            // this wave's tokens
+    if (kw > q0 + 15 || (window && kw + 15 <= q0 - window)) continue;   // nothing seen
+    f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        Frag8<float> a;
-        load_f32<8, float>(s_k + (16 * t + j) * LD + 32 * kb + 8 * g, a.v);
-        mma32(acc, a, q[kb]);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t u = k0 + 16 * t + 4 * g + r;
-        const bool seen = u <= tq && (!p.window || u > tq - p.window);
-        x[t][r] = seen ? acc[r] * c_scale : -__builtin_huge_valf();
-        mx = fmaxf(mx, x[t][r]);
-      }
+    for (int kb = 0; kb < KB; ++kb) {       // two chains, so that products need not wait
+      Frag8<float> a;
+      load_f32<8, float>(s_k + (16 * wk + j) * LD + 32 * kb + 8 * g, a.v);
+      mma32(acc[kb & 1], a, q[kb]);
     }
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float m_new = fmaxf(m, mx);
-    const float alpha = exp2_fast(m - m_new);
-    m = m_new;
-    l *= alpha;
+    float x[4], mx = -__builtin_huge_valf();
 #pragma unroll
-    for (int c = 0; c < MT; ++c)
+    for (int r = 0; r < 4; ++r) {
+      const int u = kw + 4 * g + r;
+      const bool seen = u <= tq && (!window || u > tq - window);
+      x[r] = seen ? (acc[0][r] + acc[1][r]) * c_scale : -__builtin_huge_valf();
+      mx = fmaxf(mx, x[r]);
+    }
+    mx = over_halves(over_rows(mx));
+    // The sums are kept relative to m, which need not be the maximum: it is
+    // moved only when a score passes it by 2^8.
+    if (__any(mx > m + 8.f)) {
+      const float m_new = fmaxf(m, mx);
+      const float alpha = exp2_fast(m - m_new);
+      m = m_new;
+      l *= alpha;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[c][r] *= alpha;
+      for (int c = 0; c < MT; ++c)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+        for (int r = 0; r < 4; ++r) o[c][r] *= alpha;
+    }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float e = exp2_fast(x[t][r] - m);
-        l += e;
-        const float* vr = s_v + (16 * t + 4 * g + r) * LD + j;
+    for (int r = 0; r < 4; ++r) {
+      const float e = exp2_fast(x[r] - m);
+      l += e;
+      const float* vl = s_v + (16 * wk + 4 * g + r) * LD + j;
 #pragma unroll
-        for (int c = 0; c < MT; ++c)
-          o[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(vr[16 * c], e, o[c], 0, 0, 0);
-      }
+      for (int c = 0; c < MT; ++c)
+        o[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(vl[16 * c], e, o[c], 0, 0, 0);
+    }
   }
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
-  if (tq >= tl.L) return;
-  const float inv = 1.f / l;                // a query sees itself: l > 0
+
+  // waves 2 and 3 hand over through the key tile
+  static_assert(32 * LD <= BN * LD, "32 queries of sums");
+  __syncthreads();
+  if (wk == 1) {
+#pragma unroll
+    for (int c = 0; c < MT; ++c) {
+      float* dst = s_k + (16 * wq + j) * LD + 16 * c + 4 * g;
+      lds_check(dst, 16);
+      *reinterpret_cast<float4*>(dst) = make_float4(o[c][0], o[c][1], o[c][2], o[c][3]);
+    }
+    if (g == 0) { s_m[16 * wq + j] = m; s_l[16 * wq + j] = l; }
+  }
+  __syncthreads();
+  if (wk == 1 || tq >= L) return;
+  const float m1 = s_m[16 * wq + j], mm = fmaxf(m, m1);
+  const float f0 = exp2_fast(m - mm), f1 = exp2_fast(m1 - mm);
+  const float inv = 1.f / (l * f0 + s_l[16 * wq + j] * f1);   // a query sees itself: > 0
   float* op = static_cast<float*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * g;
 #pragma unroll
-  for (int c = 0; c < MT; ++c)
-    store4<float>(op + 16 * c, o[c][0] * inv, o[c][1] * inv, o[c][2] * inv, o[c][3] * inv);
+  for (int c = 0; c < MT; ++c) {
+    const float4 u = *reinterpret_cast<const float4*>(s_k + (16 * wq + j) * LD + 16 * c + 4 * g);
+    store4<float>(op + 16 * c, (o[c][0] * f0 + u.x * f1) * inv, (o[c][1] * f0 + u.y * f1) * inv,
+                  (o[c][2] * f0 + u.z * f1) * inv, (o[c][3] * f0 + u.w * f1) * inv);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -538,7 +573,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
 }  // namespace
 
 int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType io) {
-  const int64_t bm = io == DType::F32 ? 64 : 128;
+  const int64_t bm = io == DType::F32 ? 32 : 128;
   return (packed ? total_T / bm + N : N * ((Tseq + bm - 1) / bm)) * Hq;
 }
 

@@ -205,48 +205,58 @@ __global__ __launch_bounds__(P <= 32 ? 64 : 2 * P) void kv_append_kernel(KvAppen
   const int head = blockIdx.y;
   const bool is_k = blockIdx.z == 0;
 
-  // which sequence and page
-  int64_t n, j, a, L;
+  // which sequence and page; the table entry is needed only where the codes go
+  const PagedCache& kv = p.cache;
+  int64_t n, j, a, L, held;
   if (!p.cu_seqlens) {
-    const int64_t per = (p.Tseq + P - 2) / P + 1;
-    n = blockIdx.x / per;
-    j = blockIdx.x - n * per;
+    const uint32_t per = ((uint32_t)p.Tseq + P - 2) / P + 1;
+    const uint32_t n32 = blockIdx.x / per;
+    n = n32;
+    j = blockIdx.x - n32 * per;
     a = n * p.Tseq;
     L = p.Tseq;
+    held = kv.seq_lens[n];
   } else {
-    const PackedItem it = find_packed(p.cu_seqlens, p.N, p.total_T, P, 2, blockIdx.x);
+    const PackedItem it =
+        find_packed(p.cu_seqlens, p.N, p.total_T, P, 2, blockIdx.x, kv.seq_lens, &held);
     n = it.n;
     j = it.item;
     a = it.start;
     L = it.end - it.start;
   }
-  const PagedCache& kv = p.cache;
-  const AppendPage ap = append_page(kv.seq_lens[n], kv.max_pages, P, j, a, L);
+  const AppendPage ap = append_page(held, kv.max_pages, P, j, a, L);
   if (ap.kept >= ap.stop) return;
-  const int64_t page = kv.table[n * kv.max_pages + ap.pi];
-  if (page < 0 || page >= kv.num_pages) return;
   const int kept = ap.kept, stop = ap.stop;
+  const int64_t page = kv.table[n * kv.max_pages + ap.pi];
 
-  const int64_t at = page * p.Hk + head;
-  uint8_t* __restrict__ codes = (is_k ? kv.k : kv.v) + at * (int64_t)(P * D);
-  float* scale = (is_k ? kv.k_scale : kv.v_scale) + at;
-  const float old_scale = kept ? *scale : 0.f;
   const T* __restrict__ in = static_cast<const T*>(is_k ? p.k_raw : p.v_raw) + head * D;
   const int64_t ld = is_k ? p.ld_k : p.ld_v;
   const int l = threadIdx.x % LPR;
-  const int row0 = (threadIdx.x >> 6) * 32 + (threadIdx.x & 63) / LPR;
+  const int wrow = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * 32;   // the wave's rows
+  const int row0 = wrow + (threadIdx.x & 63) / LPR;
   RopeArgs rope = p.rope;
   if (!is_k) rope.dim = 0;
   const LaneMap m = lane_map(l, rope);
+  // passes with new rows: a single token's page has one
+  bool has[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i)
+    has[i] = wrow + i * RPW < stop && wrow + (i + 1) * RPW > kept;
 
   Chunk8<T> ca[PASSES], cb[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
+    if (!has[i]) continue;
     int row = row0 + i * RPW;
     row = row < kept ? kept : (row >= stop ? stop - 1 : row);   // loads stay on new rows
     ca[i].load(in + (ap.tok0 + row) * ld + m.c0);
     cb[i].load(in + (ap.tok0 + row) * ld + m.c1);
   }
+  if (page < 0 || page >= kv.num_pages) return;
+  const int64_t at = page * p.Hk + head;
+  uint8_t* __restrict__ codes = (is_k ? kv.k : kv.v) + at * (int64_t)(P * D);
+  float* scale = (is_k ? kv.k_scale : kv.v_scale) + at;
+  const float old_scale = kept ? *scale : 0.f;
   float w[16];
   const bool normed = is_k && p.k_weight;
   load_weights(is_k ? p.k_weight : nullptr, m, w);
@@ -257,6 +267,7 @@ __global__ __launch_bounds__(P <= 32 ? 64 : 2 * P) void kv_append_kernel(KvAppen
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
+    if (!has[i]) continue;
     const int row = row0 + i * RPW;
     ca[i].unpack(x[i]);
     cb[i].unpack(x[i] + 8);

@@ -98,7 +98,7 @@ void tiles(std::mt19937& r, bool good) {   // a prefill's query tiles
   const int64_t N = 1 + r() % (r() % 4 ? 9 : 200);
   int64_t total;
   const auto cu = offsets(r, N, total, good);
-  const int BM = r() % 2 ? 64 : 128;
+  const int BM = r() % 2 ? 32 : 128;
   std::vector<int> seen(total, 0);
   for (int64_t x = 0; x < total / BM + N; ++x, ++items) {
     const PackedItem it = find(cu, N, total, BM, 1, x);
@@ -117,7 +117,7 @@ void ranked_tiles(std::mt19937& r, bool good) {   // the same tiles, the late on
   const int64_t N = 1 + r() % (r() % 4 ? 9 : 200);
   int64_t total;
   const auto cu = offsets(r, N, total, good);
-  const int BM = r() % 2 ? 64 : 128;
+  const int BM = r() % 2 ? 32 : 128;
   std::vector<int64_t> c(N);
   for (int64_t n = 0; n < N; ++n) c[n] = packed_tiles(cu.data(), n, total, BM);
   auto count = [&](auto f) { int64_t v = 0; for (int64_t x : c) v += f(x); return v; };

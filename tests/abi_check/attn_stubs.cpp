@@ -15,7 +15,7 @@ int64_t kv_append_slots(int64_t N, int64_t total_T, int64_t Tseq, bool packed, i
   return packed ? total_T / P + 2 * N : N * ((Tseq + P - 2) / P + 1);
 }
 int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType) {
-  return (packed ? total_T / 64 + N : N * ((Tseq + 63) / 64)) * Hq;
+  return (packed ? total_T / 32 + N : N * ((Tseq + 31) / 32)) * Hq;
 }
 AttnDecodePlan attn_decode_plan(int64_t N, int64_t max_tokens, int64_t, int Hq, int Hk, int d) {
   const int64_t rounds = N * Hk * ((Hq / Hk + 15) / 16) * ((max_tokens + 127) / 128);
