@@ -37,31 +37,64 @@ __device__ __forceinline__ LaneMap lane_map(int l, const RopeArgs& r) {
   return m;
 }
 
-// cos and sin of pos * freq, times the factor.  The angle in turns is formed
-// and reduced in 64-bit floats (pos * freq alone would lose 2^-24 of a far
-// position's angle).  Results that are rounded to bf16 or e4m3 take the
-// hardware's sine, whose error (about 2^-20) is far below their half step of
-// 2^-9 or 2^-4; fp32 results take the exact routine.
-template <bool EXACT>
-__device__ __forceinline__ void turn(double pos, double freq_turns, float factor, float& c,
-                                     float& s) {
-  const double t = pos * freq_turns;
-  const float r = (float)(t - __builtin_rint(t));   // [-1/2, 1/2]
-  if constexpr (EXACT) {
-    sincospif(2.f * r, &s, &c);
-  } else {
-    s = __builtin_amdgcn_sinf(r);                   // of r turns
-    c = __builtin_amdgcn_cosf(r);
-  }
-  c *= factor;
-  s *= factor;
-}
-constexpr double kInv2Pi = 0.15915494309189533577;
-
-__device__ __forceinline__ void load_freqs(const RopeArgs& r, int l, const LaneMap& m,
-                                           double* out) {
+// cos and sin of pos * inv_freq[8 l ..], times the factor.  The angle is needed
+// in turns, reduced; pos * freq alone would lose 2^-24 of a far position's
+// angle.  Positions below 2^24 are exact in fp32, and the frequency in turns is
+// kept as two fp32 terms: the leading product's error comes back by an fma, its
+// whole turns leave exactly, and the rest is added (error 2^-25 turns).  Other
+// positions go through 64-bit floats, whose conversions are slow (an append of
+// 32768 tokens, 4 heads: 25.6 us with them for all, 24.0 us so).  Results that are rounded to
+// bf16 or e4m3 take the hardware's sine, whose error (about 2^-20) is far below
+// their half step of 2^-9 or 2^-4; fp32 results take the exact routine.
+struct Freqs {
+  float hi[8], lo[8];                       // inv_freq / 2 pi
+};
+__device__ __forceinline__ void load_freqs(const RopeArgs& r, int l, const LaneMap& m, Freqs& f) {
+#pragma clang fp contract(off)             // the products below are meant to be rounded
+  constexpr float kHi = 0.15915494f, kLo = (float)(0.15915494309189533577 - (double)kHi);
+  float x[8];
+  const float* src = r.inv_freq + (m.turns ? 8 * l : 0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = m.turns ? (double)r.inv_freq[8 * l + i] * kInv2Pi : 0.0;
+  for (int i = 0; i < 8; ++i) x[i] = src[i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    f.hi[i] = x[i] * kHi;
+    f.lo[i] = __builtin_fmaf(x[i], kLo, __builtin_fmaf(x[i], kHi, -f.hi[i]));
+  }
+}
+
+template <bool EXACT>
+__device__ __forceinline__ void turn(int64_t pos, const Freqs& f, const RopeArgs& rope, int l,
+                                     const LaneMap& m, float* c, float* s) {
+#pragma clang fp contract(off)
+  float r[8];                               // turns in [-1/2, 1/2]
+  if (pos < (1 << 24) && pos > -(1 << 24)) {
+    const float x = (float)(int)pos;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = x * f.hi[i];
+      const float e = __builtin_fmaf(x, f.hi[i], -p);
+      r[i] = (p - __builtin_rintf(p)) + __builtin_fmaf(x, f.lo[i], e);
+    }
+  } else {
+    const float* src = rope.inv_freq + (m.turns ? 8 * l : 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double t = (double)pos * ((double)src[i] * 0.15915494309189533577);
+      r[i] = (float)(t - __builtin_rint(t));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (EXACT) {
+      sincospif(2.f * r[i], &s[i], &c[i]);
+    } else {
+      s[i] = __builtin_amdgcn_sinf(r[i]);   // of r turns
+      c[i] = __builtin_amdgcn_cosf(r[i]);
+    }
+    c[i] *= rope.factor;
+    s[i] *= rope.factor;
+  }
 }
 
 // Norm (when normed) and rotation of one row's 16 channels in this lane.
@@ -132,12 +165,9 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs p
   float w[16], c[8], s[8];
   load_weights(weight, m, w);
   if (p.rope.dim) {
-    double f[8];
+    Freqs f;
     load_freqs(p.rope, l, m, f);
-    const double pos = (double)p.positions[r];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      turn<std::is_same<T, float>::value>(pos, f[i], p.rope.factor, c[i], s[i]);
+    turn<std::is_same<T, float>::value>(p.positions[r], f, p.rope, l, m, c, s);
   }
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
@@ -163,6 +193,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs p
 // slots floor(cu[n] / P) + 2 n onwards and slots past a sequence's last page
 // leave at once.
 // ---------------------------------------------------------------------------
+constexpr int append_rows_per_wave(int P) { return P < 16 ? P : 16; }
+
 __device__ __forceinline__ float pow2_scale(float amax) {
   // least 2^e with amax <= 448 2^e: amax = m 2^x, m in [1, 2), and 448 = 1.75 2^8
   const uint32_t u = __float_as_uint(amax);
@@ -171,20 +203,14 @@ __device__ __forceinline__ float pow2_scale(float amax) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ float finite_or_zero(float a) {   // |a| of a finite value, else 0
-  a = fabsf(a);
-  return a < __builtin_huge_valf() ? a : 0.f;
-}
-
-// Four e4m3 codes of x * inv, rounded to nearest even; infinities become the
-// largest code, NaN stays NaN.
-__device__ __forceinline__ uint32_t codes4(const float* x, float inv) {
+// Four e4m3 codes of x * inv, rounded to nearest even; NaN stays NaN.  Where
+// there may be infinities (clamp), they become the largest code.
+__device__ __forceinline__ uint32_t codes4(const float* x, float inv, bool clamp) {
   float y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float v = x[i] * inv;
-    const float t = __builtin_amdgcn_fmed3f(v, -448.f, 448.f);
-    y[i] = v != v ? v : t;
+    y[i] = x[i] * inv;
+    if (clamp && y[i] == y[i]) y[i] = __builtin_amdgcn_fmed3f(y[i], -448.f, 448.f);
   }
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
@@ -193,15 +219,113 @@ __device__ __forceinline__ uint32_t codes4(const float* x, float inv) {
 __device__ __forceinline__ uint32_t recode4(uint32_t c, float factor) {
   float x[4] = {__builtin_amdgcn_cvt_f32_fp8(c, 0), __builtin_amdgcn_cvt_f32_fp8(c, 1),
                 __builtin_amdgcn_cvt_f32_fp8(c, 2), __builtin_amdgcn_cvt_f32_fp8(c, 3)};
-  return codes4(x, factor);
+  return codes4(x, factor, false);          // codes hold no infinities
+}
+
+// The rows of one wave.  FULL: the page's rows are all new; otherwise passes without a
+// new row are skipped (a single token's page has one).
+template <typename T, int D, bool INTER, int P, bool FULL>
+__device__ __forceinline__ void append_rows(const KvAppendArgs& p, const RopeArgs& rope,
+                                            const LaneMap& m, const T* __restrict__ in, int64_t ld,
+                                            const AppendPage& ap, int64_t page, int head,
+                                            bool is_k, int wrow, int row0, int l) {
+  constexpr int LPR = D / 16;
+  constexpr int RPW = 64 / LPR;               // rows of a wave's pass
+  constexpr int ROWS = append_rows_per_wave(P);
+  constexpr int PASSES = ROWS / RPW;
+  constexpr int WAVES = P / ROWS;
+  const PagedCache& kv = p.cache;
+  const int kept = ap.kept, stop = ap.stop;
+  auto has = [&](int i) { return FULL || (wrow + i * RPW < stop && wrow + (i + 1) * RPW > kept); };
+
+  Chunk8<T> ca[PASSES], cb[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    if (!has(i)) continue;
+    int row = row0 + i * RPW;
+    row = row < kept ? kept : (row >= stop ? stop - 1 : row);   // loads stay on new rows
+    ca[i].load(in + (ap.tok0 + row) * ld + m.c0);
+    cb[i].load(in + (ap.tok0 + row) * ld + m.c1);
+  }
+  float w[16];
+  const bool normed = is_k && p.k_weight;
+  load_weights(is_k ? p.k_weight : nullptr, m, w);
+  Freqs f;
+  if (rope.dim) load_freqs(rope, l, m, f);
+
+  float x[PASSES][16];
+  float top = 0.f;                            // of |x|; NaN does not count
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    if (!has(i)) continue;
+    const int row = row0 + i * RPW;
+    ca[i].unpack(x[i]);
+    cb[i].unpack(x[i] + 8);
+    if (is_k) {
+      float c[8], sn[8];
+      if (rope.dim) turn<false>(ap.pi * P + row, f, rope, l, m, c, sn);
+      norm_turn<LPR, INTER>(x[i], normed, w, rope.eps, m.turns, c, sn);
+    }
+    if (FULL || (row >= kept && row < stop))
+#pragma unroll
+      for (int t = 0; t < 16; ++t) top = fmaxf(top, fabsf(x[i][t]));
+  }
+  // the table entry, asked for before the rows, is first needed here
+  if (page < 0 || page >= kv.num_pages) return;     // (the same for the workgroup)
+  const int64_t at = page * p.Hk + head;
+  uint8_t* __restrict__ codes = (is_k ? kv.k : kv.v) + at * (int64_t)(P * D);
+  float* scale = (is_k ? kv.k_scale : kv.v_scale) + at;
+  const float old_scale = kept ? *scale : 0.f;
+  bool infinite = __any(top == __builtin_huge_valf());
+  if (infinite) {                             // again without the infinities
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int row = row0 + i * RPW;
+      if (has(i) && row >= kept && row < stop)
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const float a = fabsf(x[i][t]);
+          top = fmaxf(top, a < __builtin_huge_valf() ? a : 0.f);
+        }
+    }
+  }
+  top = wave_max(top);
+  if constexpr (WAVES > 1) {
+    __shared__ float s_top[WAVES];
+    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
+    __syncthreads();                          // (and every wave has read the old scale)
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) top = fmaxf(top, s_top[i]);
+  }
+  const float sc = fmaxf(pow2_scale(top), old_scale);
+  const float inv = 1.f / sc;                 // exact: a power of two
+  if (threadIdx.x == 0) *scale = sc;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int row = row0 + i * RPW;
+    uint8_t* dst = codes + row * D;
+    if (FULL || (has(i) && row >= kept && row < stop)) {
+      *reinterpret_cast<uint2*>(dst + m.c0) =
+          make_uint2(codes4(x[i], inv, infinite), codes4(x[i] + 4, inv, infinite));
+      *reinterpret_cast<uint2*>(dst + m.c1) =
+          make_uint2(codes4(x[i] + 8, inv, infinite), codes4(x[i] + 12, inv, infinite));
+    } else if (row < kept && sc > old_scale) {
+      const float factor = old_scale * inv;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint2* q = reinterpret_cast<uint2*>(dst + (h ? m.c1 : m.c0));
+        const uint2 u = *q;
+        *q = make_uint2(recode4(u.x, factor), recode4(u.y, factor));
+      }
+    }
+  }
 }
 
 template <typename T, int D, bool INTER, int P>
-__global__ __launch_bounds__(P <= 32 ? 64 : 2 * P) void kv_append_kernel(KvAppendArgs p) {
+__global__ __launch_bounds__(64 * P / append_rows_per_wave(P), std::is_same<T, bf16>::value ? 5 : 4)
+void kv_append_kernel(KvAppendArgs p) {
   constexpr int LPR = D / 16;
-  constexpr int RPW = 64 / LPR;               // rows of a wave's pass
-  constexpr int PASSES = (P < 32 ? P : 32) / RPW;
-  constexpr int WAVES = P <= 32 ? 1 : P / 32;
   const int head = blockIdx.y;
   const bool is_k = blockIdx.z == 0;
 
@@ -232,88 +356,15 @@ __global__ __launch_bounds__(P <= 32 ? 64 : 2 * P) void kv_append_kernel(KvAppen
   const T* __restrict__ in = static_cast<const T*>(is_k ? p.k_raw : p.v_raw) + head * D;
   const int64_t ld = is_k ? p.ld_k : p.ld_v;
   const int l = threadIdx.x % LPR;
-  const int wrow = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * 32;   // the wave's rows
+  const int wrow = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * append_rows_per_wave(P);   // the wave's rows
   const int row0 = wrow + (threadIdx.x & 63) / LPR;
   RopeArgs rope = p.rope;
   if (!is_k) rope.dim = 0;
   const LaneMap m = lane_map(l, rope);
-  // passes with new rows: a single token's page has one
-  bool has[PASSES];
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i)
-    has[i] = wrow + i * RPW < stop && wrow + (i + 1) * RPW > kept;
-
-  Chunk8<T> ca[PASSES], cb[PASSES];
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    if (!has[i]) continue;
-    int row = row0 + i * RPW;
-    row = row < kept ? kept : (row >= stop ? stop - 1 : row);   // loads stay on new rows
-    ca[i].load(in + (ap.tok0 + row) * ld + m.c0);
-    cb[i].load(in + (ap.tok0 + row) * ld + m.c1);
-  }
-  if (page < 0 || page >= kv.num_pages) return;
-  const int64_t at = page * p.Hk + head;
-  uint8_t* __restrict__ codes = (is_k ? kv.k : kv.v) + at * (int64_t)(P * D);
-  float* scale = (is_k ? kv.k_scale : kv.v_scale) + at;
-  const float old_scale = kept ? *scale : 0.f;
-  float w[16];
-  const bool normed = is_k && p.k_weight;
-  load_weights(is_k ? p.k_weight : nullptr, m, w);
-  double f[8];
-  if (rope.dim) load_freqs(rope, l, m, f);
-
-  float x[PASSES][16];
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    if (!has[i]) continue;
-    const int row = row0 + i * RPW;
-    ca[i].unpack(x[i]);
-    cb[i].unpack(x[i] + 8);
-    if (is_k) {
-      float c[8], sn[8];
-      if (rope.dim) {
-        const double pos = (double)(ap.pi * P + row);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) turn<false>(pos, f[t], rope.factor, c[t], sn[t]);
-      }
-      norm_turn<LPR, INTER>(x[i], normed, w, rope.eps, m.turns, c, sn);
-    }
-    if (row >= kept && row < stop)
-#pragma unroll
-      for (int t = 0; t < 16; ++t) top = fmaxf(top, finite_or_zero(x[i][t]));
-  }
-  top = wave_max(top);
-  if constexpr (WAVES > 1) {
-    __shared__ float s_top[WAVES];
-    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
-    __syncthreads();                          // (and every wave has read the old scale)
-#pragma unroll
-    for (int i = 0; i < WAVES; ++i) top = fmaxf(top, s_top[i]);
-  }
-  const float need = pow2_scale(top);
-  const float sc = fmaxf(need, old_scale);
-  const float inv = 1.f / sc;                 // exact: a power of two
-  if (threadIdx.x == 0) *scale = sc;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int row = row0 + i * RPW;
-    uint8_t* dst = codes + row * D;
-    if (row >= kept && row < stop) {
-      *reinterpret_cast<uint2*>(dst + m.c0) = make_uint2(codes4(x[i], inv), codes4(x[i] + 4, inv));
-      *reinterpret_cast<uint2*>(dst + m.c1) =
-          make_uint2(codes4(x[i] + 8, inv), codes4(x[i] + 12, inv));
-    } else if (row < kept && sc > old_scale) {
-      const float factor = old_scale * inv;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint2* q = reinterpret_cast<uint2*>(dst + (h ? m.c1 : m.c0));
-        const uint2 u = *q;
-        *q = make_uint2(recode4(u.x, factor), recode4(u.y, factor));
-      }
-    }
-  }
+  if (kept == 0 && stop == P)                 // (the same for the workgroup: it has barriers)
+    append_rows<T, D, INTER, P, true>(p, rope, m, in, ld, ap, page, head, is_k, wrow, row0, l);
+  else
+    append_rows<T, D, INTER, P, false>(p, rope, m, in, ld, ap, page, head, is_k, wrow, row0, l);
 }
 
 template <typename T, int D>
@@ -329,10 +380,10 @@ hipError_t launch_append_t(const KvAppendArgs& a, hipStream_t stream) {
   const int P = a.cache.page_size;
   const dim3 grid((unsigned)kv_append_slots(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, P),
                   (unsigned)a.Hk, 2);
-  if (P == 16) kv_append_kernel<T, D, INTER, 16><<<grid, 64, 0, stream>>>(a);
-  else if (P == 32) kv_append_kernel<T, D, INTER, 32><<<grid, 64, 0, stream>>>(a);
-  else if (P == 64) kv_append_kernel<T, D, INTER, 64><<<grid, 128, 0, stream>>>(a);
-  else kv_append_kernel<T, D, INTER, 128><<<grid, 256, 0, stream>>>(a);
+  if (P == 16) kv_append_kernel<T, D, INTER, 16><<<grid, 64 * 16 / append_rows_per_wave(16), 0, stream>>>(a);
+  else if (P == 32) kv_append_kernel<T, D, INTER, 32><<<grid, 64 * 32 / append_rows_per_wave(32), 0, stream>>>(a);
+  else if (P == 64) kv_append_kernel<T, D, INTER, 64><<<grid, 64 * 64 / append_rows_per_wave(64), 0, stream>>>(a);
+  else kv_append_kernel<T, D, INTER, 128><<<grid, 64 * 128 / append_rows_per_wave(128), 0, stream>>>(a);
   return hipGetLastError();
 }
 
