@@ -323,8 +323,7 @@ __device__ __forceinline__ void append_rows(const KvAppendArgs& p, const RopeArg
 }
 
 template <typename T, int D, bool INTER, int P>
-__global__ __launch_bounds__(64 * P / append_rows_per_wave(P), std::is_same<T, bf16>::value ? 5 : 4)
-void kv_append_kernel(KvAppendArgs p) {
+__global__ __launch_bounds__(64 * P / append_rows_per_wave(P), sizeof(T) == 2 ? 5 : 4) void kv_append_kernel(KvAppendArgs p) {
   constexpr int LPR = D / 16;
   const int head = blockIdx.y;
   const bool is_k = blockIdx.z == 0;
