@@ -1,4 +1,5 @@
-"""Build libgdn.so (and its debug twin libgdn_check.so) in-tree with hipcc for gfx950.
+"""Build libgdn.so (and its debug twin libgdn_check.so) in-tree with hipcc for gfx950,
+and the Python extension module that marshals the attention calls.
 
     python gated_delta_rule_gdn_amd/build.py [-v]
 
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdn.so")
 LIB_CHECK = os.path.join(PKG, "libgdn_check.so")
+MODULE = os.path.join(PKG, "_attn_native.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["gdn_api.cpp", "decode.hip", "chunk_fwd.hip", "chunk_fwd_sb.hip", "layer_ops.hip",
@@ -40,8 +42,26 @@ VARIANTS = [(LIB, BUILD_DIR, []),
 MAX_JOBS = 8
 
 
+def module_command() -> list:
+    """g++ on csrc/attn_bind.cpp against this interpreter's and torch's headers."""
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-attributes",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", inc,
+            "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-I", os.path.join(rocm, "include"), os.path.join(CSRC, "attn_bind.cpp"),
+            "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-L", os.path.join(rocm, "lib"), "-lamdhip64"]
+
+
 def build(verbose: bool = False) -> str:
-    jobs = []
+    jobs = [(MODULE, "attn_bind.cpp", None, [*module_command(), "-o", MODULE + ".tmp"])]
     for lib, bdir, flags in VARIANTS:
         os.makedirs(bdir, exist_ok=True)
         for src in SOURCES:
@@ -82,6 +102,7 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, lib)
+    os.replace(MODULE + ".tmp", MODULE)
     return LIB
 
 
