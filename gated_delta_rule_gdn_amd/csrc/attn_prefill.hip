@@ -285,7 +285,8 @@ __device__ __forceinline__ bf16x4 read_tr16(const bf16* p) {
 // 16 bytes for each lane from base + voff + soff straight into LDS at
 // lds + 16 * lane (lds is the same for the wave).  The load is counted by
 // vmcnt like any other; the compiler does not know of it, so wait_tiles()
-// stands before the barrier behind which the bytes are read.
+// stands before the barrier behind which the bytes are read.  (m0 is a reserved
+// register: the compiler sets it before each use of its own.)
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void load_lds16(uint32_t lds, i32x4 base, uint32_t voff, uint32_t soff) {
 #if __HIP_DEVICE_COMPILE__

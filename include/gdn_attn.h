@@ -120,9 +120,9 @@ typedef struct gdn_kv_append_desc {
  * subnormal).  A page whose first row is new is taken as empty, whatever it
  * held.  Infinities do not count towards max|x| and are written as +-448, NaN
  * as NaN.  Rows of a page behind the last token keep their bytes.  seq_lens is
- * not changed; tokens that would lie behind the page table are dropped.  Pages
- * written by one call must belong to one sequence each (else their contents
- * are unspecified).
+ * not changed; tokens that would lie behind the page table are dropped.  A page
+ * written by the call must stand once in the table (else its contents are
+ * unspecified).
  *
  *   cu_seqlens [N + 1] int64 offsets of the new tokens (clamped on the device
  *              as in gdn_chunk_fwd_varlen), or NULL for total_T / N tokens

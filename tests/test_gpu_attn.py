@@ -545,6 +545,182 @@ def test_results_are_the_same_every_time():
         assert torch.equal(d0, gdn.gdn_attn_decode(q, c["k"], c["v"], c["ks"], c["vs"], c["table"], lens))
 
 
+@pytest.mark.parametrize("N", [63, 64, 70, 300, 1100])
+def test_many_sequences(N):
+    """More sequences than lanes of a wave, and than are ranked: packed append, prompt attention and
+    cached attention, sequences of no token among them."""
+    announce(f"many sequences N={N}")
+    Hq, Hk, d, P, dtype = 4, 2, 64, 16, BF
+    g = gen(N)
+    lens = torch.randint(0, 40, (N,), generator=g)
+    lens[torch.rand(N, generator=g) < 0.2] = 0
+    lens[N // 2] = 300
+    bounds = [0] + torch.cumsum(lens, 0).tolist()
+    cu = torch.tensor(bounds)
+    host, dv = prefill_case(bounds[-1], Hq, Hk, d, dtype, N)
+    for window in (0, 7, 5000):
+        o = gdn.gdn_attn_prefill(*dv, cu_seqlens=cu.cuda(), window=window)
+        torch.cuda.synchronize()
+        check_prefill(o, host, bounds, window, None, dtype, d)
+    width = 30
+    num = N * 4 + 40
+    table = torch.full((N, width), -1, dtype=torch.int32)
+    order, at = torch.randperm(num, generator=g).to(torch.int32), 0
+    held = torch.randint(0, 20, (N,), generator=g)
+    for n in range(N):
+        c = -(-int(held[n] + lens[n]) // P)
+        table[n, :c] = order[at:at + c]
+        at += c
+    assert at <= num
+    c = cache_case(1, Hk, d, P, 1, seed=N, spare=num - 1)
+    c["table"] = table
+    ok, ov = cache_oracles(c)
+    e = to_dev(c)
+    gdn.gdn_kv_append(dv[1], dv[2], e["k"], e["v"], e["ks"], e["vs"], e["table"], held.cuda(), cu_seqlens=cu.cuda())
+    torch.cuda.synchronize()
+    for n in range(N):
+        ok.append(n, int(held[n]), host[1][bounds[n]:bounds[n + 1]])
+        ov.append(n, int(held[n]), host[2][bounds[n]:bounds[n + 1]])
+    check_cache(e, ok, ov, "many")
+    for io in (BF, F32):
+        q = torch.randn(N, Hq, d, generator=g).to(io)
+        now = held + lens
+        o = gdn.gdn_attn_decode(q.cuda(), e["k"], e["v"], e["ks"], e["vs"], e["table"], now.cuda())
+        torch.cuda.synchronize()
+        check_decode(o, q, {n: t.cpu() for n, t in e.items()}, now.tolist(), 0, None, io, P, d)
+
+
+def test_caches_beyond_32_bit_offsets():
+    """Pages that lie more than 2^32 bytes into the caches."""
+    announce("cache beyond 4 GiB")
+    Hk, d, P, N = 2, 128, 128, 2
+    num = (1 << 32) // (Hk * P * d) + 64
+    g = gen(1)
+    k = torch.zeros(num, Hk, P, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    v = torch.zeros_like(k.view(torch.uint8)).view(torch.float8_e4m3fn)
+    ks, vs = torch.ones(2, num, Hk, device="cuda")
+    table = torch.tensor([[num - 1, 5, num - 7], [num - 2, num - 30, 0]], dtype=torch.int32)
+    lens = torch.tensor([300, 200])
+    x = torch.randn(500, 2, Hk, d, generator=g).to(BF)
+    cu = torch.tensor([0, 300, 500])
+    gdn.gdn_kv_append(x[:, 0].contiguous().cuda(), x[:, 1].contiguous().cuda(), k, v, ks, vs, table.cuda(),
+                      torch.zeros(2, dtype=torch.int64, device="cuda"), cu_seqlens=cu.cuda())
+    q = torch.randn(N, 4, d, generator=g).to(BF)
+    o = gdn.gdn_attn_decode(q.cuda(), k, v, ks, vs, table.cuda(), lens.cuda())
+    torch.cuda.synchronize()
+    used = table.flatten().long()
+    small = dict(k=k.view(torch.uint8)[used.cuda()].cpu().view(torch.float8_e4m3fn),
+                 v=v.view(torch.uint8)[used.cuda()].cpu().view(torch.float8_e4m3fn),
+                 ks=ks[used.cuda()].cpu(), vs=vs[used.cuda()].cpu(),
+                 table=torch.arange(6, dtype=torch.int32).view(2, 3))
+    ok, ov = cache_oracles({**small, "k": torch.zeros_like(small["k"].view(torch.uint8)).view(torch.float8_e4m3fn),
+                            "v": torch.zeros_like(small["v"].view(torch.uint8)).view(torch.float8_e4m3fn),
+                            "ks": torch.ones(6, Hk), "vs": torch.ones(6, Hk)})
+    for n in range(N):
+        ok.append(n, 0, x[int(cu[n]):int(cu[n + 1]), 0])
+        ov.append(n, 0, x[int(cu[n]):int(cu[n + 1]), 1])
+    assert np.array_equal(u8(small["k"])[:5], ok.codes[:5]) and np.array_equal(u8(small["v"])[:5], ov.codes[:5])
+    check_decode(o, q, small, lens.tolist(), 0, None, BF, P, d)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_beyond_32_bit_offsets(dtype):
+    """Query, key and value rows more than 2^32 bytes into a wide buffer."""
+    announce(f"rows beyond 4 GiB {dtype}")
+    ld, d = 1 << 17, 64
+    T = (1 << 32) // (ld * dtype.itemsize) + 700
+    x = torch.empty(T, ld, dtype=dtype, device="cuda")
+    x[T - 600:, :4 * d] = torch.randn(600, 4 * d, generator=gen(3)).to(dtype).cuda()
+    x[:T - 600, :4 * d] = 1.0
+    q, k, v = x[:, :2 * d].unflatten(1, (2, d)), x[:, 2 * d:3 * d].unflatten(1, (1, d)), x[:, 3 * d:4 * d].unflatten(1, (1, d))
+    cu = torch.tensor([0, T - 600, T - 250, T])
+    o = gdn.gdn_attn_prefill(q, k, v, cu_seqlens=cu.cuda(), window=500)
+    torch.cuda.synchronize()
+    for a, b in ((T - 600, T - 250), (T - 250, T)):
+        ro, ra, reach = oa.attention(q[a:b].cpu(), k[a:b].cpu(), v[a:b].cpu(), 500)
+        within(o[a:b], ro, attn_bound(ro, ra, reach, b - a, d, dtype), "far rows")
+    pos = torch.arange(T).cuda()
+    f = inv_freq(d)
+    qn, kn = gdn.gdn_qk_norm_rope(q, k, positions=pos, inv_freq=dev(f))
+    y = f64(q[T - 9:])
+    ref = oa.rotate(y, np.arange(T - 9, T), f.numpy(), False)
+    within(qn[T - 9:], ref, rope_bound(ref, y, 1.0, dtype), "far norm_rope")
+
+
+def test_calls_on_two_streams_at_once():
+    """Split decodes and appends of two caches on two streams, many in flight: each as if alone."""
+    announce("two streams at once")
+    P, d = 32, 128
+    cases = []
+    for i in range(2):
+        c = to_dev(cache_case(3, 2, d, P, 120, seed=20 + i))
+        q = torch.randn(3, 8, d, generator=gen(i)).to(BF).cuda()
+        lens = torch.tensor([3000 - i, 17, 2048 + i]).cuda()
+        x = torch.randn(3, 2, d, generator=gen(5 + i)).to(BF).cuda()
+        cases.append((c, q, lens, x))
+
+    def run(c, q, lens, x):
+        gdn.gdn_kv_append(x, x, c["k"], c["v"], c["ks"], c["vs"], c["table"], lens)
+        return gdn.gdn_attn_decode(q, c["k"], c["v"], c["ks"], c["vs"], c["table"], lens + 1)
+
+    want = [run(*t) for t in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(*cases[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+
+
+def test_two_captured_graphs_with_a_workspace_each():
+    """Two graphs of split decodes, replayed in turn and after eager work; outputs as the eager calls'."""
+    announce("two graphs")
+    P, d = 32, 128
+    c = to_dev(cache_case(2, 2, d, P, 100, seed=30))
+    graphs = []
+    for i in range(2):
+        q = torch.randn(2, 8, d, generator=gen(i)).to(BF).cuda()
+        lens = torch.tensor([3000, 500 + 100 * i]).cuda()
+        o = torch.empty_like(q)
+        call = lambda q=q, lens=lens, o=o, **kw: gdn.gdn_attn_decode(  # noqa: E731
+            q, c["k"], c["v"], c["ks"], c["vs"], c["table"], lens, o=o, **kw)
+        call()
+        torch.cuda.synchronize()
+        want = o.clone()
+        ws = torch.empty(gdn.gdn_attn_decode_workspace_size(q, c["k"], c["table"]), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(workspace=ws)
+        graphs.append((g, o, want, call))
+    for r in range(3):
+        for g, o, want, call in graphs:
+            o.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for g, o, want, call in graphs:
+            assert torch.equal(o, want), r
+            call()
+
+
+def test_nothing_to_do():
+    """No sequences, no tokens."""
+    e = torch.empty(0, 2, 64, dtype=BF, device="cuda")
+    assert gdn.gdn_attn_prefill(e, e, e).shape == (0, 2, 64)
+    c = to_dev(cache_case(1, 2, 64, 16, 2, seed=1))
+    none = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    n0 = torch.empty(0, dtype=torch.int64, device="cuda")
+    before = u8(c["k"])
+    gdn.gdn_kv_append(e, e, c["k"], c["v"], c["ks"], c["vs"], none, n0)
+    gdn.gdn_kv_append(e, e, c["k"], c["v"], c["ks"], c["vs"], c["table"], torch.zeros(1, dtype=torch.int64, device="cuda"))
+    assert gdn.gdn_attn_decode(e, c["k"], c["v"], c["ks"], c["vs"], none, n0).shape == (0, 2, 64)
+    torch.cuda.synchronize()
+    assert np.array_equal(u8(c["k"]), before)
+
+
 def test_binding_refusals():
     x = torch.zeros(4, 2, 64, dtype=BF, device="cuda")
     with pytest.raises(ValueError, match="dense rows"):
