@@ -58,43 +58,47 @@ __device__ __forceinline__ int wave_sum(int v) {
          __builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48);
 }
 
-// rank_tile_by over at most 1024 sequences: each lane keeps the tiles of up to
-// 16 of them, sequence 64 i + lane in c[i].
+// rank_tile_by over at most 64 M sequences: each lane keeps the tiles of M of
+// them, sequence 64 i + lane in c[i].  Everything fits in 32 bits: the host
+// bounds the tiles.
+template <int M>
 __device__ __forceinline__ PackedItem rank_tile(const int64_t* __restrict__ cu, int N,
-                                                int64_t total, int unit, int64_t rank) {
-  constexpr int kMost = 16;
+                                                int64_t total, int unit, int level, int rank) {
   const int lane = threadIdx.x & 63;
-  int c[kMost];
-  const int used = (N + 63) >> 6;
+  int c[M];
 #pragma unroll
-  for (int i = 0; i < kMost; ++i) {
+  for (int i = 0; i < M; ++i) {
     const int n = 64 * i + lane;
-    c[i] = i < used && n < N ? (int)packed_tiles(cu, n, total, unit) : 0;
+    c[i] = n < N ? (int)packed_tiles(cu, n, total, unit) : 0;
   }
-  auto count = [&](auto f) {                // fits in 32 bits: the host bounds the tiles
+  auto count = [&](auto f) {
     int v = 0;
 #pragma unroll
-    for (int i = 0; i < kMost; ++i)
-      if (i < used) v += (int)f((int64_t)c[i]);
-    return (int64_t)wave_sum(v);
+    for (int i = 0; i < M; ++i) v += f(64 * i + lane, c[i]);
+    return wave_sum(v);
   };
-  auto pick = [&](auto f, int64_t k) {
-    int64_t found = 0;
+  auto pick = [&](auto f, int k) {
+    int found = 0;
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      if (i >= used) continue;
-      uint64_t m = __ballot(f((int64_t)c[i]));
+    for (int i = 0; i < M; ++i) {
+      uint64_t m = __ballot(f(c[i]));
       const int here = __popcll(m);
       if (k >= 0 && k < here) {
-        for (; k > 0; --k) m &= m - 1;
-        found = 64 * i + (__ffsll((unsigned long long)m) - 1);
-        k = -1;
+        for (int j = k; j > 0; --j) m &= m - 1;
+        found = 64 * i + __ffsll((unsigned long long)m) - 1;
       }
-      if (k >= 0) k -= here;
+      k -= here;
     }
     return found;
   };
-  return rank_tile_by(cu, total, unit, rank, count, pick);
+  const RankedTile t = rank_tile_by(N, (int)((total + unit - 1) / unit), level, rank, count, pick);
+  PackedItem r{0, 0, 0, 0};
+  if (t.n < 0) return r;
+  r.n = t.n;
+  r.item = t.item;
+  r.start = clamp_i64(cu[t.n], 0, total);
+  r.end = clamp_i64(cu[t.n + 1], 0, total);
+  return r;
 }
 
 // 8 consecutive elements kept as loaded, so that many rows are in flight at

@@ -52,31 +52,47 @@ GDN_HD bool packed_at_or_before(const int64_t* cu, int64_t n, int64_t total, int
   return clamp_i64(cu[n], 0, total) / unit + extra * n <= idx;
 }
 
-// Tiles of `unit` tokens of packed sequences in falling order of their number
-// within the sequence (equal numbers by sequence): which tile is `rank`-th.
-// None (end <= start) where there are fewer.  count(f) is the sum of f(n) over
-// the N sequences, pick(f, k) the k-th sequence (from 0) with f(n) true.
+// Tiles of `unit` tokens of packed sequences, the dear ones first: which tile is
+// `rank`-th.  A tile costs as much as its number within the sequence, but no
+// more than number `level` (a window).  First come the tiles from `level` on,
+// sequence by sequence, so that neighbours follow each other; then the others
+// in falling order of their number (equal numbers by sequence).  No sequence has
+// more than `most`.  count(f) is the sum of f(n, tiles of n) over the sequences,
+// pick(f, k) the k-th sequence (from 0) with f(tiles) true.
 GDN_HD int64_t packed_tiles(const int64_t* cu, int64_t n, int64_t total, int unit) {
   const int64_t L = clamp_i64(cu[n + 1], 0, total) - clamp_i64(cu[n], 0, total);
   return L > 0 ? (L + unit - 1) / unit : 0;
 }
+struct RankedTile {
+  int n, item;    // sequence, number of the tile in it; n < 0: none
+};
 template <typename Count, typename Pick>
-GDN_HD PackedItem rank_tile_by(const int64_t* cu, int64_t total, int unit, int64_t rank,
-                               Count count, Pick pick) {
-  // largest j with sum_n max(0, tiles_n - j) > rank
-  int64_t lo = 0, hi = (total + unit - 1) / unit;
-  PackedItem r{0, 0, 0, 0};
-  if (count([&](int64_t c) { return c; }) <= rank) return r;
-  while (hi - lo > 1) {
-    const int64_t j = lo + (hi - lo) / 2;
-    if (count([&](int64_t c) { return c > j ? c - j : 0; }) > rank) lo = j; else hi = j;
+GDN_HD RankedTile rank_tile_by(int N, int most, int level, int rank, Count count, Pick pick) {
+  const int dear = count([&](int, int c) { return c > level ? c - level : 0; });
+  if (rank < dear) {
+    // largest n with so many dear tiles before it at most
+    int lo = 0, hi = N, before = 0;
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      const int v = count([&](int n, int c) { return n < mid && c > level ? c - level : 0; });
+      if (v <= rank) { lo = mid; before = v; } else { hi = mid; }
+    }
+    return RankedTile{lo, level + rank - before};
   }
-  const int64_t above = count([&](int64_t c) { return c > lo + 1 ? c - lo - 1 : 0; });
-  r.n = pick([&](int64_t c) { return c > lo; }, rank - above);
-  r.item = lo;
-  r.start = clamp_i64(cu[r.n], 0, total);
-  r.end = clamp_i64(cu[r.n + 1], 0, total);
-  return r;
+  rank -= dear;
+  if (count([&](int, int c) { return c < level ? c : level; }) <= rank) return RankedTile{-1, 0};
+  // largest j with sum_n max(0, min(tiles_n, level) - j) > rank
+  int lo = 0, hi = most < level ? most : level;
+  auto from = [&](int j) {
+    return count([&](int, int c) { return c > j ? (c < level ? c : level) - j : 0; });
+  };
+  int above = 0;                            // from(hi)
+  while (hi - lo > 1) {
+    const int j = lo + (hi - lo) / 2;
+    const int v = from(j);
+    if (v > rank) { lo = j; } else { hi = j; above = v; }
+  }
+  return RankedTile{pick([&](int c) { return c > lo; }, rank - above), lo};
 }
 
 // New rows [kept, stop) of the j-th page that L new tokens (rows a .. a + L of

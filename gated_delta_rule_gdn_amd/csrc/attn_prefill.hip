@@ -41,11 +41,10 @@ struct Tile {
 // Otherwise tiles are dealt round the XCDs, the last tiles of all sequences
 // first.
 //
-// Packed lengths: the same order over tiles by their number in the sequence,
-// found by counting: with c_n tiles in sequence n, sum_n max(0, c_n - j) tiles
-// have number j or more.
+// Packed lengths: the tiles are dealt round the XCDs, the dear ones first
+// (rank_tile_by): found by counting, so nothing is sorted.  (16 prompts, 32768
+// tokens, a window of 2048: 367 us; in the order of the tokens 383 us.)
 constexpr uint32_t kXcds = 8;
-constexpr int64_t kNear = 4096;           // a window that makes all tiles cost about the same
 constexpr int64_t kMaxRanked = 1024;      // sequences that are ranked; more keep their order
 
 template <int BM>
@@ -84,7 +83,6 @@ __device__ __forceinline__ Tile find_tile(const PrefillArgs& p, uint32_t blocks)
     t.hq = (int)(hk * G + head);
     return t;
   }
-  const bool near = p.window > 0 && p.window <= kNear;
   uint32_t unit, head;
   const uint32_t rounds = per / G;
   if (i < rounds * G) {
@@ -98,10 +96,14 @@ __device__ __forceinline__ Tile find_tile(const PrefillArgs& p, uint32_t blocks)
   const uint32_t rank = unit / Hk;
   t.hq = (int)((unit - rank * Hk) * G + head);
   PackedItem it;
-  if (near || p.N > kMaxRanked)
-    it = find_packed(p.cu_seqlens, p.N, p.total_T, BM, 1, (int64_t)rank);
+  // tiles from this number on see a whole window
+  const int level = (int)((p.window > 0 && p.window < p.total_T ? p.window : p.total_T) + BM - 1) / BM;
+  if (p.N <= 64)
+    it = rank_tile<1>(p.cu_seqlens, (int)p.N, p.total_T, BM, level, (int)rank);
+  else if (p.N <= kMaxRanked)
+    it = rank_tile<kMaxRanked / 64>(p.cu_seqlens, (int)p.N, p.total_T, BM, level, (int)rank);
   else
-    it = rank_tile(p.cu_seqlens, (int)p.N, p.total_T, BM, (int64_t)rank);
+    it = find_packed(p.cu_seqlens, p.N, p.total_T, BM, 1, (int64_t)rank);
   t.a = it.start;
   t.L = it.end - it.start;
   t.q0 = it.item * BM;

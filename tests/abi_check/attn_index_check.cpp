@@ -113,30 +113,39 @@ void tiles(std::mt19937& r, bool good) {   // a prefill's query tiles
     for (int64_t t = 0; t < total; ++t) need(seen[t] == 1, "each query computed once");
 }
 
-void ranked_tiles(std::mt19937& r, bool good) {   // the same tiles, the late ones first
+void ranked_tiles(std::mt19937& r, bool good) {   // the same tiles, the dear ones first
   const int64_t N = 1 + r() % (r() % 4 ? 9 : 200);
   int64_t total;
   const auto cu = offsets(r, N, total, good);
   const int BM = r() % 2 ? 32 : 128;
-  std::vector<int64_t> c(N);
-  for (int64_t n = 0; n < N; ++n) c[n] = packed_tiles(cu.data(), n, total, BM);
-  auto count = [&](auto f) { int64_t v = 0; for (int64_t x : c) v += f(x); return v; };
-  auto pick = [&](auto f, int64_t k) {
-    int64_t n = 0;
-    for (; n < N; ++n) if (f(c[n]) && k-- == 0) break;
-    return n < N ? n : 0;
+  const int level = r() % 2 ? (int)(total / BM) + 1 : 1 + (int)(r() % 6);
+  std::vector<int> c(N);
+  for (int64_t n = 0; n < N; ++n) c[n] = (int)packed_tiles(cu.data(), n, total, BM);
+  auto count = [&](auto f) {
+    int v = 0;
+    for (int n = 0; n < (int)N; ++n) v += f(n, c[n]);
+    return v;
+  };
+  auto pick = [&](auto f, int k) {
+    int n = 0;
+    for (; n < (int)N; ++n) if (f(c[n]) && k-- == 0) break;
+    return n < (int)N ? n : 0;
   };
   std::vector<int> seen(total, 0);
   int64_t before = INT64_MAX;
   for (int64_t x = 0; x < total / BM + N; ++x, ++items) {
-    const PackedItem it = rank_tile_by(cu.data(), total, BM, x, count, pick);
-    const int64_t L = it.end - it.start, q0 = it.item * BM;
+    const RankedTile it = rank_tile_by((int)N, (int)((total + BM - 1) / BM), level, (int)x, count, pick);
+    if (it.n < 0) continue;
+    need(it.n < N, "sequence");
+    const int64_t start = clamp_i64(cu[it.n], 0, total), L = clamp_i64(cu[it.n + 1], 0, total) - start;
+    const int64_t q0 = (int64_t)it.item * BM;
     if (q0 < 0 || q0 >= L) continue;
-    need(it.item <= before, "falling order");
-    before = it.item;
+    const int64_t cost = it.item < level ? it.item : level;
+    need(cost <= before, "falling order of the costs");
+    before = cost;
     for (int64_t q = q0; q < q0 + BM && q < L; ++q) {
-      need(it.start + q >= 0 && it.start + q < total, "query row");
-      ++seen[it.start + q];
+      need(start + q >= 0 && start + q < total, "query row");
+      ++seen[start + q];
     }
   }
   if (good)
