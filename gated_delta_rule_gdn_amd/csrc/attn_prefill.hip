@@ -358,6 +358,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
   const uint32_t ck = 16 * k_chunk<D>(r0, pc), cv = 16 * v_chunk<D>(r0, pc);
   const uint32_t lk2 = (uint32_t)p.ld_k * 2, lv2 = (uint32_t)p.ld_v * 2;
   const uint32_t wave_lds = (uint32_t)wave * 1024;
+  const uint32_t k_off = (uint32_t)r0 * lk2 + ck, v_off = (uint32_t)r0 * lv2 + cv;   // of a whole tile
   auto load_tile = [&](const bf16* base, int64_t ld, uint32_t ld2, uint32_t chunk, const bf16* dst,
                        int k0) {
     const i32x4 rs = buffer_at(base + k0 * ld);
@@ -449,11 +450,32 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
   float mx = top(s);
   // One iteration: tile k0's scores are in s, V's buffer is `buf`; leaves the
   // next tile's scores in sn and their maximum in mx.
-  auto step = [&](int k0, int buf, f32x16* s, f32x16* sn) {
+  // INNER: the tiles to load exist and are whole; their loads are then spread
+  // over the score products (all at once they keep a wave from its products for
+  // as long as the address unit takes over four waves' 32 KB: 1.4 % of a 32K
+  // prompt).
+  auto step = [&](auto inner, int k0, int buf, f32x16* s, f32x16* sn) {
+    constexpr bool INNER = decltype(inner)::value;
     wait_tiles();
-    if (k0 + 2 * BN < stop) load_tile(kb_, p.ld_k, lk2, ck, s_k[buf], k0 + 2 * BN);
-    if (k0 + BN < stop) load_tile(vb_, p.ld_v, lv2, cv, s_v[buf ^ 1], k0 + BN);
-    if (k0 >= mine) return;                 // nothing left for this wave to see
+    i32x4 rk, rv;
+    uint32_t ak = 0, av = 0;
+    if constexpr (INNER) {
+      rk = buffer_at(kb_ + (k0 + 2 * BN) * p.ld_k);
+      rv = buffer_at(vb_ + (k0 + BN) * p.ld_v);
+      ak = __builtin_amdgcn_readfirstlane(lds_address(s_k[buf])) + wave_lds;
+      av = __builtin_amdgcn_readfirstlane(lds_address(s_v[buf ^ 1])) + wave_lds;
+    } else {
+      if (k0 + 2 * BN < stop) load_tile(kb_, p.ld_k, lk2, ck, s_k[buf], k0 + 2 * BN);
+      if (k0 + BN < stop) load_tile(vb_, p.ld_v, lv2, cv, s_v[buf ^ 1], k0 + BN);
+      if (k0 >= mine) return;               // nothing left for this wave to see
+    }
+    static_assert(!INNER || 2 * NL <= KB, "a load to every other score product");
+    auto load_part = [&](int e) {           // K's loads, then V's
+      if constexpr (INNER) {
+        if (e < NL) load_lds16(ak + e * 4096, rk, k_off, (uint32_t)(e * RL) * lk2);
+        else if (e < 2 * NL) load_lds16(av + (e - NL) * 4096, rv, v_off, (uint32_t)((e - NL) * RL) * lv2);
+      }
+    };
     // element (t, r) is token k0 + 4 h + at: not seen where at > tq - k0 - 4 h,
     // or at <= that less the window
     const bool front = k0 + BN - 1 > q0, back = window && k0 <= q0 + 31 - window;
@@ -523,6 +545,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
       if (i + AK < NQ) read_k(i + AK);
       if (i >= NQ - AV) read_v(i - (NQ - AV));
       sn[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], q[i / 2], sn[i % 2], 0, 0, 0);
+      if (i % 2 == 1) load_part(i / 2);
 #pragma unroll
       for (int e = EW * i; e < EW * i + EW; ++e) {
         const float x = exp2_fast(__builtin_fmaf(s[e / 16][e % 16], c_scale, -m));
@@ -544,9 +567,15 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
     mx = over_halves(top_n) * c_scale;
   };
   f32x16 s1[2];
-  for (int k0 = lo; k0 < stop; k0 += 2 * BN) {
-    step(k0, 0, s, s1);
-    if (k0 + BN < stop) step(k0 + BN, 1, s1, s);
+  int k0 = lo;
+  // (D 64 has no registers left for the two forms)
+  for (; D == 128 && k0 + 3 * BN < stop && k0 + 4 * BN <= L; k0 += 2 * BN) {
+    step(std::bool_constant<D == 128>{}, k0, 0, s, s1);
+    step(std::bool_constant<D == 128>{}, k0 + BN, 1, s1, s);
+  }
+  for (; k0 < stop; k0 += 2 * BN) {
+    step(std::false_type{}, k0, 0, s, s1);
+    if (k0 + BN < stop) step(std::false_type{}, k0 + BN, 1, s1, s);
   }
   l += __shfl_xor(l, 32);
   const float inv = 1.f / l;                // a query sees itself: l > 0
