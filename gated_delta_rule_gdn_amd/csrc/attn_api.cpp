@@ -204,7 +204,7 @@ gdn_status gdn_kv_append(const gdn_kv_append_desc* d, const int64_t* cu_seqlens,
   const int64_t Tseq = cu_seqlens ? 0 : d->total_T / d->N;
   if ((double)d->total_T > 2.0e9 || (double)d->N > 2.0e9 || d->H_k > 65535 ||
       (double)gdn::kv_append_slots(d->N, d->total_T, Tseq, cu_seqlens != nullptr, d->page_size) *
-              (d->page_size <= 32 ? 64 : 2 * d->page_size) > kMaxThreads)
+              4.0 * d->page_size > kMaxThreads)   // a wave for 16 rows of a page
     return GDN_ERR_UNSUPPORTED;
   if (!k_raw || !v_raw || !aligned16(k_raw) || !aligned16(v_raw) || !aligned16(k_weight) ||
       !aligned(inv_freq, 4) || !aligned(cu_seqlens, 8))
