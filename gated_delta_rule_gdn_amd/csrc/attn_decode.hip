@@ -14,7 +14,10 @@
 // What a workgroup has of a segment is written straight to the output if that
 // is all of it, else as a partial result, and a second kernel joins those.
 // (Where no cache can be longer than kDirect tokens each workgroup has one
-// whole segment, and nothing is joined.)
+// whole segment, and nothing is joined: a round costs a workgroup 1.2 us (fp32
+// 1.6), the second kernel about 5.  32 heads over 4, bf16 / fp32: 64 sequences
+// of 768 tokens 11.3 / 13.9 us so, joined 15.8 / 18.1; 2 sequences of 768 tokens
+// 11.2 / 13.9, joined 12.4 / 13.0; of 1024 tokens 13.7 / 17.0, joined 12.4 / 13.0.)
 //
 // The 4 waves of a workgroup take 32 tokens of a round each, with a running
 // maximum and sum of their own, and join through LDS when the segment ends.
@@ -40,8 +43,7 @@ constexpr int kWaves = 4;
 constexpr int kStep = 32;                 // tokens of a wave's step
 constexpr int kRound = kWaves * kStep;    // tokens of a workgroup's step
 constexpr int64_t kBlocks = 512;         // workgroups that fill the chip: 2 to a CU
-constexpr int kLeast = 4;                // rounds that are worth a workgroup
-constexpr int64_t kDirect = 4 * kRound;   // tokens of a cache that one workgroup takes whole
+constexpr int64_t kDirect = 6 * kRound;   // tokens of a cache that one workgroup takes whole
 constexpr float kNone = -1e30f;           // running maximum (log2 units) before any token
 
 // Two e4m3 codes (low or high half of a dword) as bf16.
@@ -161,7 +163,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
       total += n0 + lane < N ? rounds_of(kv.seq_lens[n0 + lane]) : 0;
     total = wave_sum(total) * (int)per_seq;
     share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-    if (share < kLeast) share = kLeast;
     at = (int)blockIdx.x * share;
     count = total - at < share ? total - at : share;
     if (count <= 0) {
@@ -440,9 +441,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
 // workgroup reads which of the first kernel's begin such a segment, and they
 // share the work.  Few segments (of many parts): a workgroup takes 32 columns
 // of one query, 8 lanes for each of 32 parts at a time.  Many (of few parts):
-// a wave takes a query, D/4 lanes for each part.  (128K tokens of one
-// sequence, 4 segments of 128 parts: 10.9 us with a workgroup to a query,
-// 6.0 us.)
+// a wave takes a query, D/4 lanes for each part.  Bound by latency: the launch,
+// the chains, the parts.  (128K tokens of one sequence, 4 segments of 128
+// parts: 10.9 us with a workgroup to a query, 6.3 us so, 5.2 us with the 32
+// sums joined across lanes first.)
 constexpr int kJoinBlocks = 1024;
 constexpr int kManyChains = 64;
 
@@ -466,13 +468,24 @@ struct JoinSum {
       add(part[D], part[D + 1], *reinterpret_cast<const float4*>(part + col));
     }
   }
+  // over the lanes of the wave that hold the same columns: `apart` lanes apart
+  __device__ __forceinline__ void over_lanes(int apart) {
+#pragma unroll
+    for (int off = 32; off >= apart; off >>= 1) {
+      const float4 u = make_float4(__shfl_xor(r[0], off), __shfl_xor(r[1], off),
+                                   __shfl_xor(r[2], off), __shfl_xor(r[3], off));
+      const float m1 = __shfl_xor(m, off), l1 = __shfl_xor(l, off);
+      add(m1, l1, u);
+    }
+  }
 };
 
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, int qgroups,
                                                              int rows, int blocks) {
   __shared__ int s_start[kBlocks], s_end[kBlocks], s_seg[kBlocks], s_count[kBlocks / 64];
-  __shared__ float s_o[32][36], s_m[32], s_l[32];
+  __shared__ __align__(16) float s_o[kWaves][32];
+  __shared__ float s_m[kWaves], s_l[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // the workgroups that begin a segment others go on with, in order
   int2 chain[kBlocks / kThreads];
@@ -519,13 +532,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, i
       if (row < 0) continue;
       JoinSum<D> a;
       a.gather(p.ws, rows, s_start[k], s_end[k] - s_start[k] + 1, qi, col, lane / LPQ, 64 / LPQ);
-#pragma unroll
-      for (int off = 32; off >= LPQ; off >>= 1) {
-        const float4 u = make_float4(__shfl_xor(a.r[0], off), __shfl_xor(a.r[1], off),
-                                     __shfl_xor(a.r[2], off), __shfl_xor(a.r[3], off));
-        const float m1 = __shfl_xor(a.m, off), l1 = __shfl_xor(a.l, off);
-        a.add(m1, l1, u);
-      }
+      a.over_lanes(LPQ);
       if (lane < LPQ) write(row, col, a);
     }
     return;
@@ -537,11 +544,13 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, i
     const int64_t row = out_row(s_seg[k], qi);
     JoinSum<D> a;
     if (row >= 0) a.gather(p.ws, rows, s_start[k], s_end[k] - s_start[k] + 1, qi, col, gr, 32);
-    *reinterpret_cast<float4*>(&s_o[gr][c4]) = make_float4(a.r[0], a.r[1], a.r[2], a.r[3]);
-    if (c4 == 0) { s_m[gr] = a.m; s_l[gr] = a.l; }
+    a.over_lanes(8);
+    if (lane < 8) *reinterpret_cast<float4*>(&s_o[wave][c4]) = make_float4(a.r[0], a.r[1], a.r[2], a.r[3]);
+    if (lane == 0) { s_m[wave] = a.m; s_l[wave] = a.l; }
     __syncthreads();
     if (tid < 8 && row >= 0) {
-      for (int w = 1; w < 32; ++w) a.add(s_m[w], s_l[w], *reinterpret_cast<const float4*>(&s_o[w][c4]));
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) a.add(s_m[w], s_l[w], *reinterpret_cast<const float4*>(&s_o[w][c4]));
       write(row, col, a);
     }
     __syncthreads();
@@ -573,8 +582,7 @@ AttnDecodePlan attn_decode_plan(int64_t N, int64_t max_tokens, int64_t window, i
   const int64_t rounds = segments * ((max_tokens + kRound - 1) / kRound);
   AttnDecodePlan p{segments, rounds, 0};
   if (max_tokens <= kDirect) return p;
-  const int64_t want = (rounds + kLeast - 1) / kLeast;
-  p.blocks = want < kBlocks ? want : kBlocks;
+  p.blocks = rounds < kBlocks ? rounds : kBlocks;
   p.ws_floats = p.blocks * (2 * (G < 16 ? G : 16) * (d + 4) + 2);
   return p;
 }
