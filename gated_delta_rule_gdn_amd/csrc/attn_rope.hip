@@ -13,9 +13,12 @@
 // chunks of 8.  Which chunks makes both members of every rotary pair meet in
 // one lane, so no value crosses lanes but the row's sum of squares:
 //   half pairs        lane l < dim/16: [8 l, +8) and [dim/2 + 8 l, +8)
-//   interleaved       lane l: [16 l, +8) and [16 l + 8, +8)
-//   not rotated       lane l >= dim/16: [16 l, +8) and [16 l + 8, +8)
-// In both pairings a rotating lane needs the frequencies 8 l .. 8 l + 7.
+//   interleaved       lane l < dim/16: [16 l, +8) and [16 l + 8, +8)
+//   not turned        the other lanes share the rest as half pairs are shared,
+//                     so that neighbours have neighbouring chunks (32768 fp32
+//                     rows of 18 heads of 128: 107 us, with 16 neighbouring
+//                     channels to a lane 143 us)
+// In both pairings a turning lane needs the frequencies 8 l .. 8 l + 7.
 #include "attn_device.hpp"
 
 namespace gdn {
@@ -23,17 +26,21 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Chunk offsets of lane l and whether it rotates.
+// Chunk offsets of lane l, whether it turns, and the first of its frequencies
+// (of 8 that exist where it does not turn).
 struct LaneMap {
-  int c0, c1;
+  int c0, c1, f0;
   bool turns;
 };
+// SPREAD: neighbours have neighbouring chunks where nothing turns
+template <int D, bool INTER, bool SPREAD>
 __device__ __forceinline__ LaneMap lane_map(int l, const RopeArgs& r) {
   LaneMap m;
   m.turns = 16 * l < r.dim;
-  const bool half = m.turns && !r.inter;
-  m.c0 = half ? 8 * l : 16 * l;
-  m.c1 = half ? r.dim / 2 + 8 * l : 16 * l + 8;
+  const bool whole = m.turns ? INTER : !SPREAD;
+  m.c0 = whole ? 16 * l : (m.turns ? 0 : r.dim / 2) + 8 * l;
+  m.c1 = m.c0 + (whole ? 8 : (m.turns ? r.dim : D - r.dim) / 2);
+  m.f0 = m.turns ? 8 * l : 0;
   return m;
 }
 
@@ -49,11 +56,11 @@ __device__ __forceinline__ LaneMap lane_map(int l, const RopeArgs& r) {
 struct Freqs {
   float hi[8], lo[8];                       // inv_freq / 2 pi
 };
-__device__ __forceinline__ void load_freqs(const RopeArgs& r, int l, const LaneMap& m, Freqs& f) {
+__device__ __forceinline__ void load_freqs(const RopeArgs& r, const LaneMap& m, Freqs& f) {
 #pragma clang fp contract(off)             // the products below are meant to be rounded
   constexpr float kHi = 0.15915494f, kLo = (float)(0.15915494309189533577 - (double)kHi);
   float x[8];
-  const float* src = r.inv_freq + (m.turns ? 8 * l : 0);
+  const float* src = r.inv_freq + m.f0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = src[i];
 #pragma unroll
@@ -63,8 +70,8 @@ __device__ __forceinline__ void load_freqs(const RopeArgs& r, int l, const LaneM
   }
 }
 
-template <bool EXACT>
-__device__ __forceinline__ void turn(int64_t pos, const Freqs& f, const RopeArgs& rope, int l,
+template <bool EXACT, int UNROLL>
+__device__ __forceinline__ void turn(int64_t pos, const Freqs& f, const RopeArgs& rope,
                                      const LaneMap& m, float* c, float* s) {
 #pragma clang fp contract(off)
   float r[8];                               // turns in [-1/2, 1/2]
@@ -77,10 +84,11 @@ __device__ __forceinline__ void turn(int64_t pos, const Freqs& f, const RopeArgs
       r[i] = (p - __builtin_rintf(p)) + __builtin_fmaf(x, f.lo[i], e);
     }
   } else {
-    const float* src = rope.inv_freq + (m.turns ? 8 * l : 0);
-#pragma unroll
+    const float* src = rope.inv_freq + m.f0;
+#pragma unroll UNROLL
     for (int i = 0; i < 8; ++i) {
-      const double t = (double)pos * ((double)src[i] * 0.15915494309189533577);
+      const float x = src[i];
+      const double t = (double)pos * ((double)x * 0.15915494309189533577);
       r[i] = (float)(t - __builtin_rint(t));
     }
   }
@@ -134,7 +142,7 @@ __device__ __forceinline__ void load_weights(const float* weight, const LaneMap&
 // before the first value is used.  Blocks run over head groups first, so that
 // a token's whole row is read by workgroups that run together.
 // ---------------------------------------------------------------------------
-constexpr int kHeads = 4;
+constexpr int kHeads = 2;
 
 template <typename T, int D, bool INTER>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs p) {
@@ -151,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs p
   const int l = threadIdx.x % LPR;
   const int64_t r = tb * TB + threadIdx.x / LPR;
   if (r >= p.rows) return;                    // whole rows of lanes leave together
-  const LaneMap m = lane_map(l, p.rope);
+  const LaneMap m = lane_map<D, INTER, true>(l, p.rope);
   const T* __restrict__ in = static_cast<const T*>(is_q ? p.q_raw : p.k_raw) + r * ld;
   T* out = static_cast<T*>(is_q ? p.q : p.k) + r * (int64_t)H * D;
 
@@ -166,8 +174,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs p
   load_weights(weight, m, w);
   if (p.rope.dim) {
     Freqs f;
-    load_freqs(p.rope, l, m, f);
-    turn<std::is_same<T, float>::value>(p.positions[r], f, p.rope, l, m, c, s);
+    load_freqs(p.rope, m, f);
+    turn<std::is_same<T, float>::value, 8>(p.positions[r], f, p.rope, m, c, s);
   }
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
@@ -251,7 +259,7 @@ __device__ __forceinline__ void append_rows(const KvAppendArgs& p, const RopeArg
   const bool normed = is_k && p.k_weight;
   load_weights(is_k ? p.k_weight : nullptr, m, w);
   Freqs f;
-  if (rope.dim) load_freqs(rope, l, m, f);
+  if (rope.dim) load_freqs(rope, m, f);
 
   float x[PASSES][16];
   float top = 0.f;                            // of |x|; NaN does not count
@@ -263,7 +271,7 @@ __device__ __forceinline__ void append_rows(const KvAppendArgs& p, const RopeArg
     cb[i].unpack(x[i] + 8);
     if (is_k) {
       float c[8], sn[8];
-      if (rope.dim) turn<false>(ap.pi * P + row, f, rope, l, m, c, sn);
+      if (rope.dim) turn<false, 1>(ap.pi * P + row, f, rope, m, c, sn);
       norm_turn<LPR, INTER>(x[i], normed, w, rope.eps, m.turns, c, sn);
     }
     if (FULL || (row >= kept && row < stop))
@@ -359,7 +367,7 @@ __global__ __launch_bounds__(64 * P / append_rows_per_wave(P), sizeof(T) == 2 ? 
   const int row0 = wrow + (threadIdx.x & 63) / LPR;
   RopeArgs rope = p.rope;
   if (!is_k) rope.dim = 0;
-  const LaneMap m = lane_map(l, rope);
+  const LaneMap m = lane_map<D, INTER, false>(l, rope);
   if (kept == 0 && stop == P)                 // (the same for the workgroup: it has barriers)
     append_rows<T, D, INTER, P, true>(p, rope, m, in, ld, ap, page, head, is_k, wrow, row0, l);
   else
