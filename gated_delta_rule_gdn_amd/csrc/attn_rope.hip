@@ -14,10 +14,12 @@
 // one lane, so no value crosses lanes but the row's sum of squares:
 //   half pairs        lane l < dim/16: [8 l, +8) and [dim/2 + 8 l, +8)
 //   interleaved       lane l < dim/16: [16 l, +8) and [16 l + 8, +8)
-//   not turned        the other lanes share the rest as half pairs are shared,
-//                     so that neighbours have neighbouring chunks (32768 fp32
-//                     rows of 18 heads of 128: 107 us, with 16 neighbouring
-//                     channels to a lane 143 us)
+//   not turned        norm_rope: the other lanes share the rest as half pairs
+//                     are shared, so that neighbours have neighbouring chunks
+//                     (32768 fp32 rows of 18 heads of 128: 107 us, with 16
+//                     neighbouring channels to a lane 143 us); append: lane l
+//                     has [16 l, +8) and [16 l + 8, +8), whose codes are one
+//                     piece (32768 bf16 tokens of 4 heads: 22.2 us, spread 22.8)
 // In both pairings a turning lane needs the frequencies 8 l .. 8 l + 7.
 #include "attn_device.hpp"
 
@@ -32,7 +34,7 @@ struct LaneMap {
   int c0, c1, f0;
   bool turns;
 };
-// SPREAD: neighbours have neighbouring chunks where nothing turns
+// SPREAD: neighbours have neighbouring chunks where nothing turns.
 template <int D, bool INTER, bool SPREAD>
 __device__ __forceinline__ LaneMap lane_map(int l, const RopeArgs& r) {
   LaneMap m;
@@ -50,9 +52,12 @@ __device__ __forceinline__ LaneMap lane_map(int l, const RopeArgs& r) {
 // kept as two fp32 terms: the leading product's error comes back by an fma, its
 // whole turns leave exactly, and the rest is added (error 2^-25 turns).  Other
 // positions go through 64-bit floats, whose conversions are slow (an append of
-// 32768 tokens, 4 heads: 25.6 us with them for all, 24.0 us so).  Results that are rounded to
-// bf16 or e4m3 take the hardware's sine, whose error (about 2^-20) is far below
-// their half step of 2^-9 or 2^-4; fp32 results take the exact routine.
+// 32768 tokens, 4 heads: 25.6 us with them for all, 24.0 us so).  Results that
+// are rounded to bf16 or e4m3 take the hardware's sine, whose error (about
+// 2^-20) is far below their half step of 2^-8 or 2^-4; fp32 results take the
+// exact routine.  (UNROLL is the far positions' loop: rolled it leaves append,
+// d 64, registers for 8 waves to a SIMD instead of 6; unrolled norm_rope is 18 %
+// faster for near ones.)
 struct Freqs {
   float hi[8], lo[8];                       // inv_freq / 2 pi
 };
@@ -140,7 +145,9 @@ __device__ __forceinline__ void load_weights(const float* weight, const LaneMap&
 // qk_norm_rope.  A thread keeps its lane of one token for kHeads heads of one
 // operand, so the angles are computed once for them and every load is issued
 // before the first value is used.  Blocks run over head groups first, so that
-// a token's whole row is read by workgroups that run together.
+// a token's whole row is read by workgroups that run together.  HBM-bound:
+// 32768 tokens of 18 heads of 128, bf16, 302 MB: 48 us (4 heads to a thread 55,
+// one 50); fp32 107 us (115, 116).
 // ---------------------------------------------------------------------------
 constexpr int kHeads = 2;
 
@@ -192,9 +199,14 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs p
 
 // ---------------------------------------------------------------------------
 // kv_append.  One workgroup for each (page that may get new tokens, head, key
-// or value): it holds the page's new rows in registers, 32 rows to a wave,
+// or value): it holds the page's new rows in registers, 16 rows to a wave,
 // finds their largest magnitude, and writes their codes; where the scale of a
-// page that holds older tokens grows it also rounds those again.
+// page that holds older tokens grows it also rounds those again.  So a row is
+// read once though its scale is known only after the page's last row.  HBM-bound
+// for many tokens (32768 tokens of 4 heads of 128, bf16, pages of 64: 101 MB in
+// 22.2 us, 4.5 TB/s), by latency and the waves that fit where pages are partly
+// filled (213 sequences of 40 tokens, 8 heads of 64, pages of 128: 27.8 us for
+// 26 MB), and by the launch for a token to a sequence (256: 4.3 us).
 //
 // Which pages get tokens is known on the device only.  L new tokens behind a
 // length s touch at most floor(L / P) + 2 pages, so packed sequences own the
