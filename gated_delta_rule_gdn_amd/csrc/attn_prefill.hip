@@ -125,12 +125,15 @@ __device__ __forceinline__ Tile find_tile(const PrefillArgs& p, uint32_t blocks)
 // same queries over the other 16, with a running maximum and sum of their own,
 // and the pairs join through LDS at the end.  Short prompts have few query
 // tiles, and this halves the time that one takes.  The next key tile is loaded
-// into registers while this one is computed.  Bound by fp32 products and the LDS
-// reads that feed them: 4096 tokens, 16 heads of 128: 765 us, 90 TFLOP/s (a plain
-// fp32 product reaches 154).
+// into registers while this one is computed.  Bound by fp32 products and the
+// vector work between them: 4096 tokens, 16 heads of 128: 675 us, 102 TFLOP/s (a
+// plain fp32 product reaches 154).  (Without the bound on registers the compiler
+// moves the sums to the accumulation registers and back in every tile: 790 us;
+// key tiles double-buffered in LDS, which leaves room for two workgroups instead
+// of three: 750 us.)
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ __launch_bounds__(kThreads) void prefill_f32_kernel(PrefillArgs p, uint32_t blocks) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 4 : 3) void prefill_f32_kernel(PrefillArgs p, uint32_t blocks) {
   constexpr int BM = 32, BN = 32, LD = D + 4, KB = D / 32, MT = D / 16;
   constexpr int NL = BN * D / 4 / kThreads;           // 16-byte loads of a thread and tile
   __shared__ __align__(16) float s_k[BN * LD], s_v[BN * LD];
