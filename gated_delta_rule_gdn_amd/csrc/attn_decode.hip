@@ -154,22 +154,18 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
   };
   Round cur;
   int count;                              // rounds of this workgroup
-  int share = 0, more = 0, at = 0;        // rounds of a workgroup, how many have one more; first
-                                          // round here, of all
+  int total = 0, at = 0;                  // rounds of all; first round here
   if (direct) {
     const int n = (int)(blockIdx.x / per_seq);
     cur = begin_round(n, blockIdx.x - (uint32_t)n * per_seq, 0, kv.seq_lens[n]);
     count = cur.rounds;
   } else {
-    int total = 0;
     for (int n0 = 0; n0 < N; n0 += 64)
       total += n0 + lane < N ? rounds_of(kv.seq_lens[n0 + lane]) : 0;
     total = wave_sum(total) * (int)per_seq;
-    share = total / (int)gridDim.x;
-    more = total - share * (int)gridDim.x;
-    const int b = (int)blockIdx.x;
-    at = b * share + (b < more ? b : more);
-    count = share + (b < more ? 1 : 0);
+    const DecodeShare share = decode_share(total, (int)gridDim.x, (int)blockIdx.x);
+    at = share.at;
+    count = share.count;
     if (count <= 0) {
       if (tid == 0) *chain_at(p.ws, prows, D, gridDim.x, blockIdx.x) = make_int2(-1, 0);
       return;
@@ -443,11 +439,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
   }
   if (!direct && tid == 0) {
     const int last = at + count - 1 + (cur.rounds - 1 - cur.r);   // the segment's, of all rounds
-    const int in_more = more * (share + 1);
-    const int owner = last < in_more ? last / (share + 1) : more + (last - in_more) / (share ? share : 1);
     const int seg = cur.n * (int)per_seq + cur.hk * qgroups + cur.qg;
     *chain_at(p.ws, prows, D, gridDim.x, blockIdx.x) =
-        chained ? make_int2(seg, owner) : make_int2(-1, 0);
+        chained ? make_int2(seg, decode_owner(total, (int)gridDim.x, last)) : make_int2(-1, 0);
   }
 }
 

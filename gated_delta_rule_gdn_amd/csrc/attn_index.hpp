@@ -142,4 +142,20 @@ GDN_HD int decode_rounds(int64_t seq_len, int64_t max_pages, int P, int64_t wind
   return decode_span(seq_len, max_pages, P, window, step).rounds(round);
 }
 
+// The rounds of all segments dealt to `blocks` workgroups in order, in shares
+// that differ by one at most: block b has rounds [at, at + count).
+struct DecodeShare {
+  int at, count;
+};
+GDN_HD DecodeShare decode_share(int total, int blocks, int b) {
+  const int each = total / blocks, more = total - each * blocks;
+  return DecodeShare{b * each + (b < more ? b : more), each + (b < more ? 1 : 0)};
+}
+// The block that has round r < total.
+GDN_HD int decode_owner(int total, int blocks, int r) {
+  const int each = total / blocks, more = total - each * blocks;
+  const int in_more = more * (each + 1);
+  return r < in_more ? r / (each + 1) : more + (r - in_more) / (each > 0 ? each : 1);
+}
+
 }  // namespace gdn

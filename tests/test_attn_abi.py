@@ -187,3 +187,8 @@ def test_validation_clean_under_asan_and_ubsan(tmp_path):
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 def test_index_arithmetic_stays_within_the_tensors(tmp_path):
     _run(tmp_path, "attn_index_check", [os.path.join(ROOT, "tests", "abi_check", "attn_index_check.cpp")], False)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_decode_shares_are_equal_and_complete(tmp_path):
+    _run(tmp_path, "attn_share_check", [os.path.join(ROOT, "tests", "abi_check", "attn_share_check.cpp")], False)
