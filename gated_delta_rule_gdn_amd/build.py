@@ -34,6 +34,11 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-I", INCLUDE, "-I", CSRC, "-Wall", "-Wno-unused-function"]
 
 
+# Flags of single sources.  attn_prefill.hip: products take and leave their sums
+# in vector registers; otherwise kernels that fill a CU's LDS with one workgroup
+# keep them in accumulation registers and move them there and back in every tile.
+SOURCE_FLAGS = {"attn_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
 # The product library and its debug twin (-DGDN_CHECK: LDS filled with NaN
 # at kernel start, LDS accesses and block indices checked, every call waits
 # for its kernels and reports GDN_ERR_CHECK on a violation).
@@ -67,7 +72,7 @@ def build(verbose: bool = False) -> str:
         for src in SOURCES:
             obj = os.path.join(bdir, os.path.splitext(src)[0] + ".o")
             lang = ["-x", "hip"] if src.endswith(".hip") else []
-            cmd = ["hipcc", *COMMON, *flags, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+            cmd = ["hipcc", *COMMON, *flags, *SOURCE_FLAGS.get(src, []), *lang, "-c", os.path.join(CSRC, src), "-o", obj]
             jobs.append((lib, src, obj, cmd))
     failed = []
     running = []

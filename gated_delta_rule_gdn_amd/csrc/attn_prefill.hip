@@ -119,6 +119,90 @@ __device__ __forceinline__ Tile find_tile(const PrefillArgs& p, uint32_t blocks)
   return t;
 }
 
+// The products give unseen tokens a weight of zero, and zero times an infinite or
+// NaN value is NaN: such a value would reach queries that do not see it.  A wave
+// whose sums are not all finite looks at the values that its tiles hold and some
+// of its queries [q0, q0 + rows) do not see (tiles end less than 160 tokens from
+// q0 on either side of what is seen), and if any is not finite it computes its
+// rows again by exact_rows, which touches seen tokens only.
+template <typename T, int D>
+__device__ __forceinline__ bool unseen_not_finite(const T* __restrict__ v, int64_t ld, int L,
+                                                  int window, int q0, int rows) {
+  const int lane = threadIdx.x & 63;
+  float z = 0.f;                            // times 0: NaN where a value is not finite
+  auto scan = [&](int from, int to) {
+#pragma unroll 1
+    for (int s = from < 0 ? 0 : from; s < to && s < L; ++s)
+#pragma unroll
+      for (int c = 0; c < D; c += 64) z = __builtin_fmaf((float)v[s * ld + c + lane], 0.f, z);
+  };
+  scan(q0 + 1, q0 + 160);
+  if (window) scan(q0 - window - 160, q0 + rows - window);
+  return __any(z != z);
+}
+
+// Rows [q0, q0 + rows) of a sequence and head by a wave, one after another: 64
+// keys at a time, a score to a lane, then D / 64 columns to a lane.
+template <typename T, int D>
+__device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl, int hk, int window,
+                                           int q0, int rows) {
+  const int lane = threadIdx.x & 63, L = (int)tl.L;
+  const T* kp = static_cast<const T*>(p.k) + tl.a * p.ld_k + hk * D;
+  const T* vp = static_cast<const T*>(p.v) + tl.a * p.ld_v + hk * D;
+  for (int t = q0; t < q0 + rows && t < L; ++t) {
+    const T* qp = static_cast<const T*>(p.q) + (tl.a + t) * p.ld_q + tl.hq * D;
+    float m = kNone, l = 0.f, o[D / 64] = {};
+    for (int s0 = window && t >= window ? t - window + 1 : 0; s0 <= t; s0 += 64) {
+      const int s = s0 + lane <= t ? s0 + lane : t;
+      float x = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 8) {
+        float a[8], b[8];
+        load_f32<8, T>(qp + c, a);
+        load_f32<8, T>(kp + s * p.ld_k + c, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x = __builtin_fmaf(a[i], b[i], x);
+      }
+      x = s0 + lane <= t ? x * p.scale * kLog2e : -__builtin_huge_valf();
+      const float m_new = fmaxf(m, wave_max(x));
+      const float alpha = exp2_fast(m - m_new), w = exp2_fast(x - m_new);
+      m = m_new;
+      float sum = w;
+#pragma unroll
+      for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
+      l = l * alpha + sum;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) o[c] *= alpha;
+#pragma unroll 1
+      for (int i = 0; i < 64 && s0 + i <= t; ++i) {
+        const float wi = (float)(T)__shfl(w, i);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          o[c] = __builtin_fmaf(wi, (float)vp[(s0 + i) * p.ld_v + 64 * c + lane], o[c]);
+      }
+    }
+    T* op = static_cast<T*>(p.o) + ((tl.a + t) * p.Hq + tl.hq) * (int64_t)D + lane;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) op[64 * c] = (T)(o[c] / l);
+  }
+}
+
+// Both, for the end of a kernel: true if the rows are written.  The arguments are
+// read from the kernel's argument segment again, where `p` is its first: kept in
+// registers for this rare end they would spill others (2 % of a prompt).
+template <typename T, int D>
+__device__ __forceinline__ bool rows_again(const Tile& tl, int hk, int window, int q0, int rows) {
+#if __HIP_DEVICE_COMPILE__
+  uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  const PrefillArgs& p = *reinterpret_cast<const PrefillArgs*>(at);
+  const T* v = static_cast<const T*>(p.v) + tl.a * p.ld_v + hk * D;
+  if (!unseen_not_finite<T, D>(v, p.ld_v, (int)tl.L, window, q0, rows)) return false;
+  exact_rows<T, D>(p, tl, hk, window, q0, rows);
+#endif
+  return true;
+}
+
 // ---------------------------------------------------------------------------
 // fp32: v_mfma_f32_16x16x4_f32.  A workgroup has 32 queries; waves 0 and 1 take
 // 16 each over the first 16 tokens of every key tile of 32, waves 2 and 3 the
@@ -255,22 +339,31 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 3) void prefill_f32_kernel(
     if (g == 0) { s_m[16 * wq + j] = m; s_l[16 * wq + j] = l; }
   }
   __syncthreads();
-  if (wk == 1 || tq >= L) return;
+  if (wk == 1) return;
   const float m1 = s_m[16 * wq + j], mm = fmaxf(m, m1);
   const float f0 = exp2_fast(m - mm), f1 = exp2_fast(m1 - mm);
   const float inv = 1.f / (l * f0 + s_l[16 * wq + j] * f1);   // a query sees itself: > 0
-  float* op = static_cast<float*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * g;
+  float z = 0.f;                            // NaN where a sum is not finite
 #pragma unroll
   for (int c = 0; c < MT; ++c) {
     const float4 u = *reinterpret_cast<const float4*>(s_k + (16 * wq + j) * LD + 16 * c + 4 * g);
-    store4<float>(op + 16 * c, (o[c][0] * f0 + u.x * f1) * inv, (o[c][1] * f0 + u.y * f1) * inv,
-                  (o[c][2] * f0 + u.z * f1) * inv, (o[c][3] * f0 + u.w * f1) * inv);
+    o[c][0] = o[c][0] * f0 + u.x * f1;
+    o[c][1] = o[c][1] * f0 + u.y * f1;
+    o[c][2] = o[c][2] * f0 + u.z * f1;
+    o[c][3] = o[c][3] * f0 + u.w * f1;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) z = __builtin_fmaf(o[c][r], 0.f, z);
   }
+  if (__any(z != z) && rows_again<float, D>(tl, hk, window, q0, 16)) return;
+  float* op = static_cast<float*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * g;
+#pragma unroll
+  for (int c = 0; c < MT; ++c)
+    if (tq < L) store4<float>(op + 16 * c, o[c][0] * inv, o[c][1] * inv, o[c][2] * inv, o[c][3] * inv);
 }
 
 // ---------------------------------------------------------------------------
-// bf16: v_mfma_f32_32x32x16_bf16, 32 queries to a wave, 128 to a workgroup,
-// key tiles of 64 tokens in LDS.
+// bf16: v_mfma_f32_32x32x16_bf16, 32 queries to a wave, 128 to a workgroup (64
+// where there are few, see split_keys), key tiles of 64 tokens in LDS.
 //
 // Lane 32 h + i holds, of a 32 x 32 product, column i and rows
 // 8 a + 4 h + b (a, b = 0..3), and supplies 8 k-values.  The score tile's rows
@@ -331,29 +424,35 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
 
+// SPLIT 2: 64 queries to a workgroup; waves 0 and 1 take the even key tiles, 2
+// and 3 the odd ones, with a maximum and sum of their own, and join at the end.
+//
 // The loop over key tiles is pipelined by hand: while the weights of tile i
 // are formed (VALU), the scores of tile i + 1 are on the matrix cores, and
 // while the maximum of tile i + 1 is formed, tile i's product with V is.  K
 // runs one tile ahead of V; both are double-buffered in LDS and loaded one
 // iteration before they are read, with one barrier to an iteration.
-template <int D>
-__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel(PrefillArgs p, uint32_t blocks) {
-  constexpr int BM = 128, BN = 64, KB = D / 16, MT = D / 32;
+template <int D, int SPLIT>
+__global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void prefill_bf16_kernel(PrefillArgs p, uint32_t blocks) {
+  constexpr int WQ = 4 / SPLIT;                       // waves with queries of their own
+  constexpr int BM = 32 * WQ, BN = 64, KB = D / 16, MT = D / 32;
+  constexpr int STEP = BN * SPLIT;                    // keys of an iteration
   constexpr int CH = D / 8;                           // 16-byte chunks of a row
-  constexpr int NL = BN * CH / kThreads;              // chunks a thread loads of a tile
-  constexpr int RL = kThreads / CH;                   // rows of one such load
-  __shared__ __align__(16) bf16 s_k[2][BN * D], s_v[2][BN * D];
+  constexpr int NL = BN * CH / (64 * WQ);             // chunks a thread loads of a tile
+  constexpr int RL = 64 * WQ / CH;                    // rows of one such load
+  __shared__ __align__(16) bf16 s_k[2][STEP * D], s_v[2][STEP * D];
   lds_nan_fill(s_k, sizeof s_k);
   lds_nan_fill(s_v, sizeof s_v);
   const Tile tl = find_tile<BM>(p, blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wq = SPLIT == 1 ? wave : wave % WQ, wk = SPLIT == 1 ? 0 : wave / WQ;
   const int h = lane >> 5, i32 = lane & 31;
   const int hk = tl.hq / (p.Hq / p.Hk);
   const int L = __builtin_amdgcn_readfirstlane((int)tl.L);
   const int qt0 = __builtin_amdgcn_readfirstlane((int)tl.q0);
-  const int q0 = qt0 + 32 * wave;           // the wave's first query
+  const int q0 = qt0 + 32 * wq;             // the wave's first query
   const int tq = q0 + i32;                  // this lane's query
   const bf16* kb_ = static_cast<const bf16*>(p.k) + tl.a * p.ld_k + hk * D;
   const bf16* vb_ = static_cast<const bf16*>(p.v) + tl.a * p.ld_v + hk * D;
@@ -367,24 +466,29 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
   // loads of one tile: row r0 + e RL, permuted so that LDS position pc of row r
   // gets chunk k_chunk(r, pc); rows past the sequence repeat its last one
   // (their scores are masked), so nothing of another sequence is read
-  const int r0 = tid / CH, pc = tid % CH;
+  const int r0 = (SPLIT == 1 ? tid : tid % (64 * WQ)) / CH, pc = tid % CH;
   const uint32_t ck = 16 * k_chunk<D>(r0, pc), cv = 16 * v_chunk<D>(r0, pc);
   const uint32_t lk2 = (uint32_t)p.ld_k * 2, lv2 = (uint32_t)p.ld_v * 2;
-  const uint32_t wave_lds = (uint32_t)wave * 1024;
+  const uint32_t wave_lds = (uint32_t)wq * 1024;
   const uint32_t k_off = (uint32_t)r0 * lk2 + ck, v_off = (uint32_t)r0 * lv2 + cv;   // of a whole tile
-  auto load_tile = [&](const bf16* base, int64_t ld, uint32_t ld2, uint32_t chunk, const bf16* dst,
-                       int k0) {
+  // K's chunks repeat after 16 rows: with 8 rows to a load, the odd loads' differ
+  constexpr uint32_t ODD = D == 128 && RL == 8 ? 128 : 0;
+  static_assert(RL % 16 == 0 || ODD, "the chunks of a thread's rows");
+  const uint32_t k_odd = (uint32_t)r0 * lk2 + (ck ^ ODD);
+  auto load_tile = [&](const bf16* base, int64_t ld, uint32_t ld2, uint32_t chunk, uint32_t odd,
+                       const bf16* dst, int k0) {
     const i32x4 rs = buffer_at(base + k0 * ld);
     const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(dst)) + wave_lds;
     if (k0 + BN <= L) {
-      const uint32_t voff = (uint32_t)r0 * ld2 + chunk;
+      const uint32_t voff[2] = {(uint32_t)r0 * ld2 + chunk, (uint32_t)r0 * ld2 + (chunk ^ odd)};
 #pragma unroll
-      for (int e = 0; e < NL; ++e) load_lds16(at + e * 4096, rs, voff, (uint32_t)(e * RL) * ld2);
+      for (int e = 0; e < NL; ++e)
+        load_lds16(at + e * (1024 * WQ), rs, voff[e % 2], (uint32_t)(e * RL) * ld2);
     } else {
 #pragma unroll
       for (int e = 0; e < NL; ++e) {
         const int row = r0 + e * RL < L - k0 ? r0 + e * RL : L - 1 - k0;
-        load_lds16(at + e * 4096, rs, (uint32_t)row * ld2 + chunk, 0);
+        load_lds16(at + e * (1024 * WQ), rs, (uint32_t)row * ld2 + (e % 2 ? chunk ^ odd : chunk), 0);
       }
     }
   };
@@ -392,8 +496,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
   // The queries come in whole rows too, by way of the second key buffer (waves
   // 0 and 1) and the second value buffer: loads of a fragment's rows straight
   // into registers touch 64 rows each.
-  load_tile(kb_, p.ld_k, lk2, ck, s_k[0], lo);
-  bf16* sq = wave < 2 ? s_k[1] + wave * (32 * D) : s_v[1] + (wave - 2) * (32 * D);
+  const int lo_w = lo + BN * wk;            // this wave's first tile
+  if (lo_w < stop) load_tile(kb_, p.ld_k, lk2, ck, ODD, s_k[0] + wk * BN * D, lo_w);
+  constexpr int HALF = STEP / 32;           // waves whose queries fit into a key buffer
+  bf16* sq = wave < HALF ? s_k[1] + wave * (32 * D) : s_v[1] + (wave - HALF) * (32 * D);
   {
     constexpr int RQ = 64 / CH;             // rows of a wave's load
     const i32x4 rs = buffer_at(static_cast<const bf16*>(p.q) + (tl.a + q0) * p.ld_q + tl.hq * D);
@@ -407,7 +513,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
                                                     16 * k_chunk<D>(row, lane % CH), 0);
     }
   }
-  load_tile(vb_, p.ld_v, lv2, cv, s_v[0], lo);
+  if (lo_w < stop) load_tile(vb_, p.ld_v, lv2, cv, 0u, s_v[0] + wk * BN * D, lo_w);
   wait_tiles();
   bf16x8 q[KB];
   {
@@ -422,7 +528,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
     }
   }
   wait_tiles();                             // every wave has its queries
-  if (lo + BN < stop) load_tile(kb_, p.ld_k, lk2, ck, s_k[1], lo + BN);
+  if (lo_w + STEP < stop) load_tile(kb_, p.ld_k, lk2, ck, ODD, s_k[1] + wk * BN * D, lo_w + STEP);
 
   const float c_scale = fabsf(p.scale) * kLog2e;
   f32x16 o[MT];
@@ -459,7 +565,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
   };
 
   f32x16 s[2];
-  scores(s_k[0], s);
+  scores(s_k[0] + wk * BN * D, s);
   float mx = top(s);
   // One iteration: tile k0's scores are in s, V's buffer is `buf`; leaves the
   // next tile's scores in sn and their maximum in mx.
@@ -473,20 +579,23 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
     i32x4 rk, rv;
     uint32_t ak = 0, av = 0;
     if constexpr (INNER) {
-      rk = buffer_at(kb_ + (k0 + 2 * BN) * p.ld_k);
-      rv = buffer_at(vb_ + (k0 + BN) * p.ld_v);
-      ak = __builtin_amdgcn_readfirstlane(lds_address(s_k[buf])) + wave_lds;
-      av = __builtin_amdgcn_readfirstlane(lds_address(s_v[buf ^ 1])) + wave_lds;
+      rk = buffer_at(kb_ + (k0 + 2 * STEP) * p.ld_k);
+      rv = buffer_at(vb_ + (k0 + STEP) * p.ld_v);
+      ak = __builtin_amdgcn_readfirstlane(lds_address(s_k[buf] + wk * BN * D)) + wave_lds;
+      av = __builtin_amdgcn_readfirstlane(lds_address(s_v[buf ^ 1] + wk * BN * D)) + wave_lds;
     } else {
-      if (k0 + 2 * BN < stop) load_tile(kb_, p.ld_k, lk2, ck, s_k[buf], k0 + 2 * BN);
-      if (k0 + BN < stop) load_tile(vb_, p.ld_v, lv2, cv, s_v[buf ^ 1], k0 + BN);
+      if (k0 + 2 * STEP < stop)
+        load_tile(kb_, p.ld_k, lk2, ck, ODD, s_k[buf] + wk * BN * D, k0 + 2 * STEP);
+      if (k0 + STEP < stop)
+        load_tile(vb_, p.ld_v, lv2, cv, 0u, s_v[buf ^ 1] + wk * BN * D, k0 + STEP);
       if (k0 >= mine) return;               // nothing left for this wave to see
     }
-    static_assert(!INNER || 2 * NL <= KB, "a load to every other score product");
+    constexpr int LP = 2 * KB / (2 * NL);   // score products to a load
+    static_assert(!INNER || LP >= 1, "a place for every load");
     auto load_part = [&](int e) {           // K's loads, then V's
       if constexpr (INNER) {
-        if (e < NL) load_lds16(ak + e * 4096, rk, k_off, (uint32_t)(e * RL) * lk2);
-        else if (e < 2 * NL) load_lds16(av + (e - NL) * 4096, rv, v_off, (uint32_t)((e - NL) * RL) * lv2);
+        if (e < NL) load_lds16(ak + e * (1024 * WQ), rk, e % 2 ? k_odd : k_off, (uint32_t)(e * RL) * lk2);
+        else if (e < 2 * NL) load_lds16(av + (e - NL) * (1024 * WQ), rv, v_off, (uint32_t)((e - NL) * RL) * lv2);
       }
     };
     // element (t, r) is token k0 + 4 h + at: not seen where at > tq - k0 - 4 h,
@@ -531,7 +640,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
     bf16x8 kf[NQ], vf[NP], w[4];
     auto read_k = [&](int i) {
       const int row = 32 * (i % 2) + i32;
-      const bf16* src = s_k[buf ^ 1] + row * D + 8 * k_chunk<D>(row, 2 * (i / 2) + h);
+      const bf16* src = s_k[buf ^ 1] + wk * BN * D + row * D + 8 * k_chunk<D>(row, 2 * (i / 2) + h);
       lds_check(src, 16);
       kf[i] = *reinterpret_cast<const bf16x8*>(src);
     };
@@ -541,7 +650,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
         const int li = lane & 15;
         const int row = 16 * (j / MT) + 8 * half + 4 * h + (li >> 2);
         const int col = 32 * (j % MT) + 16 * ((lane >> 4) & 1) + 4 * (li & 3);
-        const bf16x4 u = read_tr16(s_v[buf] + row * D + 8 * v_chunk<D>(row, col / 8) + col % 8);
+        const bf16x4 u = read_tr16(s_v[buf] + wk * BN * D + row * D + 8 * v_chunk<D>(row, col / 8) + col % 8);
 #pragma unroll
         for (int i = 0; i < 4; ++i) vf[j][4 * half + i] = u[i];
       }
@@ -558,7 +667,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
       if (i + AK < NQ) read_k(i + AK);
       if (i >= NQ - AV) read_v(i - (NQ - AV));
       sn[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], q[i / 2], sn[i % 2], 0, 0, 0);
-      if (i % 2 == 1) load_part(i / 2);
+      if constexpr (INNER) {
+        if (i % LP == LP - 1) load_part(i / LP);
+      }
 #pragma unroll
       for (int e = EW * i; e < EW * i + EW; ++e) {
         const float x = exp2_fast(__builtin_fmaf(s[e / 16][e % 16], c_scale, -m));
@@ -581,22 +692,56 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
   };
   f32x16 s1[2];
   int k0 = lo;
+  const int dk = BN * wk;
   // (D 64 has no registers left for the two forms)
-  for (; D == 128 && k0 + 3 * BN < stop && k0 + 4 * BN <= L; k0 += 2 * BN) {
-    step(std::bool_constant<D == 128>{}, k0, 0, s, s1);
-    step(std::bool_constant<D == 128>{}, k0 + BN, 1, s1, s);
+  for (; D == 128 && k0 + 3 * STEP < stop && k0 + 4 * STEP <= L; k0 += 2 * STEP) {
+    step(std::bool_constant<D == 128>{}, k0 + dk, 0, s, s1);
+    step(std::bool_constant<D == 128>{}, k0 + dk + STEP, 1, s1, s);
   }
-  for (; k0 < stop; k0 += 2 * BN) {
-    step(std::false_type{}, k0, 0, s, s1);
-    if (k0 + BN < stop) step(std::false_type{}, k0 + BN, 1, s1, s);
+  for (; k0 < stop; k0 += 2 * STEP) {
+    step(std::false_type{}, k0 + dk, 0, s, s1);
+    if (k0 + STEP < stop) step(std::false_type{}, k0 + dk + STEP, 1, s1, s);
   }
   l += __shfl_xor(l, 32);
+  if constexpr (SPLIT == 2) {               // the second half hands over through V's tiles
+    wait_tiles();
+    float* so = reinterpret_cast<float*>(&s_v[0][0]) + wq * (16 * MT * 64) + lane;
+    float* sm = reinterpret_cast<float*>(&s_k[1][0]) + wq * 128 + lane;
+    static_assert(WQ * 16 * MT * 64 * sizeof(float) <= sizeof s_v && BM <= STEP, "the sums fit");
+    if (wk == 1) {
+#pragma unroll
+      for (int c = 0; c < MT; ++c)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          lds_check(so + (16 * c + r) * 64, 4);
+          so[(16 * c + r) * 64] = o[c][r];
+        }
+      sm[0] = m;
+      sm[64] = l;
+    }
+    wait_tiles();
+    if (wk == 1) return;
+    const float m1 = sm[0], mm = fmaxf(m, m1);
+    const float f0 = exp2_fast(m - mm), f1 = exp2_fast(m1 - mm);
+    l = l * f0 + sm[64] * f1;
+#pragma unroll
+    for (int c = 0; c < MT; ++c)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[c][r] = o[c][r] * f0 + so[(16 * c + r) * 64] * f1;
+  }
   const float inv = 1.f / l;                // a query sees itself: l > 0
-  // rows leave through LDS (this wave's quarter of the key tiles, which no wave
+  // rows leave through LDS (this wave's part of the key tiles, which no wave
   // reads any more), so that a store covers whole rows
-  wait_tiles();
-  static_assert(BM == 2 * BN, "the waves' rows fill the key tiles");
-  bf16* so = &s_k[0][0] + wave * 32 * D;
+  if constexpr (SPLIT == 1) wait_tiles();
+  static_assert(BM <= 2 * STEP, "the waves' rows fit into the key tiles");
+  float z[4] = {0.f, 0.f, 0.f, 0.f};        // NaN where a sum is not finite
+#pragma unroll
+  for (int c = 0; c < MT; ++c)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) z[r % 4] = __builtin_fmaf(o[c][r], 0.f, z[r % 4]);
+  z[0] += z[1] + (z[2] + z[3]);
+  if (__any(z[0] != z[0]) && rows_again<bf16, D>(tl, hk, window, q0, 32)) return;
+  bf16* so = &s_k[0][0] + wq * 32 * D;
 #pragma unroll
   for (int c = 0; c < MT; ++c)
 #pragma unroll
@@ -615,23 +760,46 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_bf16_kernel
   }
 }
 
-}  // namespace
-
-int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType io) {
-  const int64_t bm = io == DType::F32 ? 32 : 128;
+int64_t blocks_of(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, int64_t bm) {
   return (packed ? total_T / bm + N : N * ((Tseq + bm - 1) / bm)) * Hq;
 }
 
+// With few query tiles a CU has one workgroup or none, and the last tile's walk
+// over its keys is the call's time: then two waves share a tile's keys.  It costs
+// a tile twice the LDS and a hand-over, so not where a walk is short, nor where
+// the tiles fill the CUs twice anyway.  (us with 128 queries to a workgroup / 64
+// and the keys shared, d 128: 2048 tokens, 8 heads 36.7 / 23.2; 512 tokens, 16
+// heads 13.2 / 10.8; 2 prompts of 704 tokens in all, 12 heads 12.7 / 11.6; 4 of
+// 512, 16 heads 8.7 / 8.9; with 256 workgroups of the first kind: 4096 tokens, 8
+// heads 69 / 48.7, 1024 tokens, 32 heads 22.5 / 22.2; with 512: 2048 tokens, 32
+// heads 47 / 58.)
+bool split_keys(const PrefillArgs& a, int64_t blocks) {
+  const int64_t len = a.cu_seqlens ? a.total_T / a.N : a.Tseq;
+  const int64_t keys = a.window > 0 && a.window < len ? a.window : len;
+  return blocks <= 256 && keys >= 256;
+}
+
+}  // namespace
+
+int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType io) {
+  return blocks_of(N, total_T, Tseq, packed, Hq, io == DType::F32 ? 32 : 128);
+}
+
 hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t stream) {
-  const int64_t blocks =
-      prefill_blocks(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, a.Hq, a.io);
+  const bool packed = a.cu_seqlens != nullptr;
+  const int64_t blocks = prefill_blocks(a.N, a.total_T, a.Tseq, packed, a.Hq, a.io);
   const dim3 grid((unsigned)blocks);
   if (a.io == DType::F32) {
     if (a.d == 128) prefill_f32_kernel<128><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
     else prefill_f32_kernel<64><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
+  } else if (split_keys(a, blocks)) {
+    const int64_t twice = blocks_of(a.N, a.total_T, a.Tseq, packed, a.Hq, 64);
+    const dim3 grid2((unsigned)twice);
+    if (a.d == 128) prefill_bf16_kernel<128, 2><<<grid2, kThreads, 0, stream>>>(a, (uint32_t)twice);
+    else prefill_bf16_kernel<64, 2><<<grid2, kThreads, 0, stream>>>(a, (uint32_t)twice);
   } else {
-    if (a.d == 128) prefill_bf16_kernel<128><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
-    else prefill_bf16_kernel<64><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
+    if (a.d == 128) prefill_bf16_kernel<128, 1><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
+    else prefill_bf16_kernel<64, 1><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
   }
   return hipGetLastError();
 }

@@ -156,7 +156,8 @@ typedef struct gdn_attn_prefill_desc {
  * gdn_attn_prefill -- o_t = sum_s p_ts v_s with p_ts = softmax over s of
  * scale * q_t . k_s, s running over the tokens of t's own sequence up to t
  * (the last `window` of them).  Statistics and sums in fp32; with bf16 io the
- * weights are rounded to bf16 for the product with v.
+ * weights are rounded to bf16 for the product with v.  Tokens that t does not
+ * see have no part in o_t, infinite and NaN keys and values included.
  *
  *   cu_seqlens [N + 1] int64 offsets (clamped on the device as in
  *              gdn_chunk_fwd_varlen), or NULL for total_T / N tokens each

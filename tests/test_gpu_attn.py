@@ -748,3 +748,60 @@ def test_binding_refusals():
         gdn.gdn_attn_decode(x, f8, f8.clone(), sc, sc, t, n.int())
     with pytest.raises(ValueError, match="N \\+ 1"):
         gdn.gdn_kv_append(x, x, f8, f8.clone(), sc, sc.clone(), t, n, cu_seqlens=n[:3])
+
+
+@pytest.mark.parametrize("window", [0, 256, 300, 700])
+@pytest.mark.parametrize("Hq,Hk,d", [(4, 2, 128), (3, 3, 64), (7, 1, 128)])
+def test_prefill_few_long_prompts(Hq, Hk, d, window):
+    """Few query tiles with many keys each (two waves share a tile's keys)."""
+    announce(f"prefill few Hq={Hq} Hk={Hk} d={d} window={window}")
+    lens = [0, 1, 64, 65, 129, 770, 63, 0, 1500]
+    bounds = [0] + list(np.cumsum(lens))
+    host, dv = prefill_case(bounds[-1], Hq, Hk, d, BF, 31 + Hq)
+    o = gdn.gdn_attn_prefill(*dv, cu_seqlens=torch.tensor(bounds).cuda(), window=window)
+    torch.cuda.synchronize()
+    check_prefill(o, host, bounds, window, None, BF, d)
+
+
+@pytest.mark.parametrize("T", [1, 63, 64, 65, 127, 128, 129, 256, 257, 320, 385, 449])
+def test_prefill_one_prompt_of_every_tile_edge(T):
+    announce(f"prefill one prompt T={T}")
+    for d in (64, 128):
+        host, dv = prefill_case(T, 2, 1, d, BF, T)
+        for window in (0, 256, 257):
+            o = gdn.gdn_attn_prefill(*dv, window=window)
+            torch.cuda.synchronize()
+            check_prefill(o, host, [0, T], window, None, BF, d)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [0, 40, 256])
+@pytest.mark.parametrize("T,d", [(200, 128), (400, 64), (400, 128)])
+def test_prefill_values_that_a_query_does_not_see(T, d, window, dtype):
+    """Infinite and NaN values and keys reach the queries that see their token and no other, not those of
+    the same tile either."""
+    announce(f"prefill unseen T={T} d={d} window={window} {dtype}")
+    host, _ = prefill_case(T, 2, 1, d, dtype, T + window)
+    q, k, v = [t.clone().contiguous() for t in host]
+    for j in (0, 5, 70, 100, 133, T - 2, T - 1):
+        sees = torch.arange(T) >= j
+        if window:
+            sees &= torch.arange(T) < j + window
+        clean = v.clone()
+        clean[j, 0, 7] = 0
+        ro, ra, reach = oa.attention(q, k, clean, window, 0.05)
+        bound = attn_bound(ro, ra, reach, T, d, dtype)
+        for bad in (math.nan, math.inf, -math.inf):
+            w = clean.clone()
+            w[j, 0, 7] = bad
+            o = gdn.gdn_attn_prefill(q.cuda(), k.cuda(), w.cuda(), window=window, scale=0.05).cpu()
+            hit = o[sees][:, :, 7]
+            assert bool(hit.isnan().all()) if math.isnan(bad) else bool((hit == bad).all()), (j, bad)
+            o[:, :, 7] = torch.where(sees[:, None], torch.as_tensor(ro[:, :, 7]).to(o.dtype), o[:, :, 7])
+            within(o, ro, bound, f"value {bad} at {j}")
+        kk = k.clone()
+        kk[j, 0, 3] = math.nan
+        o = gdn.gdn_attn_prefill(q.cuda(), kk.cuda(), clean.cuda(), window=window, scale=0.05).cpu()
+        assert bool(o[sees].isnan().all()), j
+        o[sees] = torch.as_tensor(ro).to(o.dtype)[sees]
+        within(o, ro, bound, f"key at {j}")
