@@ -192,7 +192,16 @@ float scale_of(PyObject* o, int64_t d) {
 
 template <typename Fn>
 Fn function(PyObject* o) { return reinterpret_cast<Fn>(PyLong_AsVoidPtr(o)); }
-void* handle(PyObject* o) { return PyLong_AsVoidPtr(o); }
+void* handle(PyObject* o) {
+  void* p = PyLong_AsVoidPtr(o);
+  if (!p && PyErr_Occurred()) { PyErr_Clear(); throw Refused("stream is no handle of a stream"); }
+  return p;
+}
+bool truth(PyObject* o, const char* name) {
+  const int x = PyObject_IsTrue(o);
+  if (x < 0) { PyErr_Clear(); throw Refused(std::string(name) + " must be true or false"); }
+  return x != 0;
+}
 
 // Runs `call` with dev as the current device.
 template <typename F>
@@ -261,14 +270,15 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* pos = dense(a[3], "positions", dev, {rows}, ScalarType::Long);
     const void* qw = dense(a[5], "q_weight", dev, {d}, ScalarType::Float);
     const void* kw = dense(a[6], "k_weight", dev, {d}, ScalarType::Float);
-    desc.rope_mode = PyObject_IsTrue(a[7]) ? GDN_ROPE_INTERLEAVED : GDN_ROPE_HALF;
+    desc.rope_mode = truth(a[7], "interleaved") ? GDN_ROPE_INTERLEAVED : GDN_ROPE_HALF;
     desc.rope_scale = (float)number(a[8], "rope_scale");
     desc.eps = (float)number(a[9], "eps");
     const auto fn = function<decltype(&gdn_qk_norm_rope)>(a[0]);
+    void* stream = handle(a[12]);
     return on_device(dev, [&] {
       return fn(&desc, q_in, k_in, static_cast<const float*>(qw), static_cast<const float*>(kw),
                 desc.rope_dim ? static_cast<const int64_t*>(pos) : nullptr, freqs, q, k,
-                handle(a[12]));
+                stream);
     });
   });
 }
@@ -300,13 +310,14 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float* freqs;
     desc.rope_dim = rope_of(a[10], dev, &freqs);
     const void* kw = dense(a[11], "k_weight", dev, {c.d}, ScalarType::Float);
-    desc.rope_mode = PyObject_IsTrue(a[12]) ? GDN_ROPE_INTERLEAVED : GDN_ROPE_HALF;
+    desc.rope_mode = truth(a[12], "interleaved") ? GDN_ROPE_INTERLEAVED : GDN_ROPE_HALF;
     desc.rope_scale = (float)number(a[13], "rope_scale");
     desc.eps = (float)number(a[14], "eps");
     const auto fn = function<decltype(&gdn_kv_append)>(a[0]);
+    void* stream = handle(a[15]);
     return on_device(dev, [&] {
       return fn(&desc, cu, c.lens, c.table, k_in, v_in, static_cast<const float*>(kw), freqs, c.k,
-                c.v, c.ks, c.vs, handle(a[15]));
+                c.v, c.ks, c.vs, stream);
     });
   });
 }
@@ -333,7 +344,8 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     desc.scale = scale_of(a[7], d);
     void* o = dense(a[8], "o", dev, {T, desc.H_q, d}, io);
     const auto fn = function<decltype(&gdn_attn_prefill)>(a[0]);
-    return on_device(dev, [&] { return fn(&desc, cu, q_in, k_in, v_in, o, handle(a[9])); });
+    void* stream = handle(a[9]);
+    return on_device(dev, [&] { return fn(&desc, cu, q_in, k_in, v_in, o, stream); });
   });
 }
 
@@ -370,8 +382,9 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       bytes = t.nbytes();
     }
     const auto fn = function<decltype(&gdn_attn_decode)>(a[0]);
+    void* stream = handle(a[13]);
     return on_device(dev, [&] {
-      return fn(&desc, q_in, c.k, c.v, c.ks, c.vs, c.table, c.lens, o, ws, bytes, handle(a[13]));
+      return fn(&desc, q_in, c.k, c.v, c.ks, c.vs, c.table, c.lens, o, ws, bytes, stream);
     });
   });
 }

@@ -28,8 +28,8 @@
  *    [N] int64 is clamped into [0, max_pages * page_size] on the device.  So
  *    neither a bad table nor a bad length makes a kernel touch memory outside
  *    the arguments.
- *  - Non-finite inputs: a token's non-finite q, k or v makes outputs of its own
- *    sequence undefined, never those of another sequence.
+ *  - Non-finite inputs: a token's non-finite q spoils its own output, its k and
+ *    v the outputs of the queries that see it, and nothing else.
  */
 #ifndef GDN_ATTN_H
 #define GDN_ATTN_H
@@ -69,8 +69,8 @@ typedef struct gdn_qk_desc {
  *       t = positions[r] * inv_freq[i],  f = rope_scale,  i < rope_dim / 2
  *
  * for the channel pairs (a, b) of rope_mode; channels from rope_dim on are
- * not rotated.  The angle is formed and reduced in 64-bit floats, so far
- * positions lose nothing; frequencies scaled for long contexts come in through
+ * not rotated.  The angle is formed and reduced to 2^-25 of a turn at every
+ * position, so far ones lose nothing; frequencies scaled for long contexts come in through
  * inv_freq and rope_scale.  The rest is fp32, rounded once at the end.
  *
  *   q_raw     [rows, H_q, d] io_dtype, row stride ld_q (NULL when H_q == 0)

@@ -805,3 +805,52 @@ def test_prefill_values_that_a_query_does_not_see(T, d, window, dtype):
         assert bool(o[sees].isnan().all()), j
         o[sees] = torch.as_tensor(ro).to(o.dtype)[sees]
         within(o, ro, bound, f"key at {j}")
+
+
+@pytest.mark.parametrize("N,T,Hq,Hk", [(2, 300, 8, 4), (8, 257, 2, 1), (1, 600, 16, 8), (4, 300, 12, 2), (1, 2048, 16, 2)])
+def test_prefill_few_equal_prompts(N, T, Hq, Hk):
+    """The same in every order that tiles of equal prompts are dealt in."""
+    announce(f"prefill few equal N={N} T={T} Hq={Hq} Hk={Hk}")
+    for d in (64, 128):
+        host, dv = prefill_case(N * T, Hq, Hk, d, BF, N + T + d)
+        o = gdn.gdn_attn_prefill(*dv, N=N)
+        torch.cuda.synchronize()
+        check_prefill(o, host, list(range(0, N * T + 1, T)), 0, None, BF, d)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("P,d,rope", [(16, 64, 32), (32, 128, 64), (128, 128, 96), (64, 64, 16)])
+def test_append_part_of_the_head_turned(P, d, rope, inter, dtype):
+    """Partly rotated and interleaved keys, with norm, at positions on both sides of 2^24 (where the
+    angles' arithmetic changes), some behind older tokens of their page."""
+    announce(f"append P={P} d={d} rope={rope} inter={inter} {dtype}")
+    Hk, new = 2, 10
+    width = (1 << 24) // P + 2
+    f, w = inv_freq(rope), 1 + 0.1 * torch.randn(d, generator=gen(2))
+    for at in (0, (1 << 24) - 5, (1 << 24) + P):
+        c = cache_case(1, Hk, d, P, 3, seed=P + d)
+        first = at // P
+        few = c["table"]
+        c["table"] = torch.full((1, width + 2), -1, dtype=torch.int32)
+        c["table"][:, first:first + 2] = few[:, :2]
+        ok, ov = cache_oracles(c)
+        g = to_dev(c)
+        x = torch.randn(2, new, Hk, d, generator=gen(at % 97)).to(dtype)
+        lens = torch.tensor([at])
+        gdn.gdn_kv_append(x[0].cuda(), x[1].cuda(), g["k"], g["v"], g["ks"], g["vs"], g["table"], lens.cuda(),
+                          inv_freq=f.cuda(), k_weight=w.cuda(), interleaved=inter)
+        torch.cuda.synchronize()
+        ok.append(0, at, oa.norm_rope(x[0], w, at + np.arange(new), f.numpy(), inter))
+        ov.append(0, at, x[1])
+        check_cache(g, ok, ov, f"at {at}", k_bound=0.01)
+
+
+def test_binding_refuses_what_is_no_flag_and_no_stream():
+    x = torch.zeros(4, 2, 64, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="true or false"):
+        gdn.gdn_qk_norm_rope(x, interleaved=torch.zeros(2))
+    with pytest.raises(ValueError, match="stream"):
+        gdn.gdn_qk_norm_rope(x, q=x.clone(), stream=1 << 80)
+    gdn.gdn_qk_norm_rope(x)
+    torch.cuda.synchronize()
