@@ -11,16 +11,17 @@
 //
 // A head of D channels is held by D/16 lanes with 16 channels each, in two
 // chunks of 8.  Which chunks makes both members of every rotary pair meet in
-// one lane, so no value crosses lanes but the row's sum of squares:
-//   half pairs        lane l < dim/16: [8 l, +8) and [dim/2 + 8 l, +8)
-//   interleaved       lane l < dim/16: [16 l, +8) and [16 l + 8, +8)
-//   not turned        norm_rope: the other lanes share the rest as half pairs
-//                     are shared, so that neighbours have neighbouring chunks
-//                     (32768 fp32 rows of 18 heads of 128: 107 us, with 16
-//                     neighbouring channels to a lane 143 us); append: lane l
-//                     has [16 l, +8) and [16 l + 8, +8), whose codes are one
-//                     piece (32768 bf16 tokens of 4 heads: 22.2 us, spread 22.8)
-// In both pairings a turning lane needs the frequencies 8 l .. 8 l + 7.
+// one lane, so no value crosses lanes but the row's sum of squares.  Lanes l <
+// dim/16 turn, and hold
+//   half pairs    [8 l, +8) and [dim/2 + 8 l, +8), frequencies 8 l .. 8 l + 7;
+//   interleaved   norm_rope: the same chunks, so that neighbours have
+//                 neighbouring ones, frequencies 4 l .. 4 l + 3 and dim/4 + 4 l
+//                 .. dim/4 + 4 l + 3; append: [16 l, +16), as half pairs.
+// The others share the rest: norm_rope [8 l', +8) and the same behind half of
+// it, append [16 l, +16).  (norm_rope, 32768 fp32 rows of 18 heads of 128, with
+// 16 neighbouring channels to a lane / spread: interleaved 141 / 109 us, not
+// turned 143 / 107; bf16 55 / 48, 52 / 46.  append, whose codes of 16 channels are
+// one piece: 32768 bf16 tokens of 4 heads 22.2 / 22.8 us.)
 #include "attn_device.hpp"
 
 namespace gdn {
@@ -28,21 +29,22 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Chunk offsets of lane l, whether it turns, and the first of its frequencies
-// (of 8 that exist where it does not turn).
+// Chunk offsets of lane l, whether it turns, and its frequencies: f0 .. f0 + 3
+// and f0 + gap .. f0 + gap + 3 (some that exist where it does not turn).
+// SPREAD: neighbours have neighbouring chunks.
 struct LaneMap {
-  int c0, c1, f0;
+  int c0, c1, f0, gap;
   bool turns;
 };
-// SPREAD: neighbours have neighbouring chunks where nothing turns.
 template <int D, bool INTER, bool SPREAD>
 __device__ __forceinline__ LaneMap lane_map(int l, const RopeArgs& r) {
   LaneMap m;
   m.turns = 16 * l < r.dim;
-  const bool whole = m.turns ? INTER : !SPREAD;
+  const bool whole = !SPREAD && (INTER || !m.turns);
   m.c0 = whole ? 16 * l : (m.turns ? 0 : r.dim / 2) + 8 * l;
   m.c1 = m.c0 + (whole ? 8 : (m.turns ? r.dim : D - r.dim) / 2);
-  m.f0 = m.turns ? 8 * l : 0;
+  m.f0 = m.turns ? (INTER && SPREAD ? 4 : 8) * l : 0;
+  m.gap = INTER && SPREAD && m.turns ? r.dim / 4 : 4;
   return m;
 }
 
@@ -67,7 +69,7 @@ __device__ __forceinline__ void load_freqs(const RopeArgs& r, const LaneMap& m, 
   float x[8];
   const float* src = r.inv_freq + m.f0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = src[i];
+  for (int i = 0; i < 8; ++i) x[i] = src[i < 4 ? i : m.gap + i - 4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     f.hi[i] = x[i] * kHi;
@@ -92,7 +94,7 @@ __device__ __forceinline__ void turn(int64_t pos, const Freqs& f, const RopeArgs
     const float* src = rope.inv_freq + m.f0;
 #pragma unroll UNROLL
     for (int i = 0; i < 8; ++i) {
-      const float x = src[i];
+      const float x = src[i < 4 ? i : m.gap + i - 4];
       const double t = (double)pos * ((double)x * 0.15915494309189533577);
       r[i] = (float)(t - __builtin_rint(t));
     }
