@@ -448,13 +448,14 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
 // Joins the parts of the segments that lie in several workgroups.  Every
 // workgroup reads which of the first kernel's begin such a segment, and they
 // share the work.  Few segments (of many parts): a workgroup takes 32 columns
-// of one query, 8 lanes for each of 32 parts at a time.  Many (of few parts):
-// a wave takes a query, D/4 lanes for each part.  Bound by latency: the launch,
+// of one query, 8 lanes for each of 32 parts at a time.  More of those than
+// workgroups (segments of few parts): a wave takes a query, D/4 lanes for each
+// part.  (56 segments of 16 queries, with the first kernel: 41 us so, 44 by
+// columns; 32 of 8 queries, by columns 15.0, by queries 16.4.)  Bound by latency: the launch,
 // the chains, the parts.  (128K tokens of one sequence, 4 segments of 128
 // parts: 10.9 us with a workgroup to a query, 6.3 us so, 5.2 us with the 32
 // sums joined across lanes first.)
 constexpr int kJoinBlocks = 1024;
-constexpr int kManyChains = 64;
 
 template <int D>
 struct JoinSum {
@@ -531,7 +532,8 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, i
     store4<T>(static_cast<T*>(p.o) + row * D + col, a.r[0] * inv, a.r[1] * inv, a.r[2] * inv,
               a.r[3] * inv);
   };
-  if (chains > kManyChains) {
+  constexpr int CP = D / 32;                // column parts
+  if (chains * rows * CP > (int)gridDim.x) {
     constexpr int LPQ = D / 4;
     const int col = 4 * (lane % LPQ);
     for (int it = blockIdx.x * kWaves + wave; it < chains * rows; it += gridDim.x * kWaves) {
@@ -545,7 +547,6 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, i
     }
     return;
   }
-  constexpr int CP = D / 32;                // column parts
   const int gr = tid / 8, c4 = 4 * (tid % 8);
   for (int it = blockIdx.x; it < chains * rows * CP; it += gridDim.x) {
     const int k = it / (rows * CP), qi = it / CP % rows, col = 32 * (it % CP) + c4;
