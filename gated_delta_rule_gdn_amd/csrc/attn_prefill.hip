@@ -141,21 +141,29 @@ __device__ __forceinline__ bool unseen_not_finite(const T* __restrict__ v, int64
   return __any(z != z);
 }
 
+// Says that x points to global memory, as a kernel's own arguments do.
+template <typename T>
+__device__ __forceinline__ const T* in_global(const void* x) {
+  return (const T*)(const __attribute__((address_space(1))) T*)x;
+}
+
 // Rows [q0, q0 + rows) of a sequence and head by a wave, one after another: 64
-// keys at a time, a score to a lane, then D / 64 columns to a lane.
+// keys at a time, a score to a lane, then D / 64 columns to a lane.  Bound by the
+// latency of its loads (a prompt of 4096 tokens, 16 heads, with one NaN value: up
+// to 13 ms for the wave that it sends here, 0.11 ms without; 32768 tokens 114).
 template <typename T, int D>
 __device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl, int hk, int window,
                                            int q0, int rows) {
   const int lane = threadIdx.x & 63, L = (int)tl.L;
-  const T* kp = static_cast<const T*>(p.k) + tl.a * p.ld_k + hk * D;
-  const T* vp = static_cast<const T*>(p.v) + tl.a * p.ld_v + hk * D;
+  const T* kp = in_global<T>(p.k) + tl.a * p.ld_k + hk * D;
+  const T* vp = in_global<T>(p.v) + tl.a * p.ld_v + hk * D;
   for (int t = q0; t < q0 + rows && t < L; ++t) {
-    const T* qp = static_cast<const T*>(p.q) + (tl.a + t) * p.ld_q + tl.hq * D;
+    const T* qp = in_global<T>(p.q) + (tl.a + t) * p.ld_q + tl.hq * D;
     float m = kNone, l = 0.f, o[D / 64] = {};
     for (int s0 = window && t >= window ? t - window + 1 : 0; s0 <= t; s0 += 64) {
       const int s = s0 + lane <= t ? s0 + lane : t;
       float x = 0.f;
-#pragma unroll 1
+#pragma unroll 4
       for (int c = 0; c < D; c += 8) {
         float a[8], b[8];
         load_f32<8, T>(qp + c, a);
@@ -174,11 +182,22 @@ __device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl,
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) o[c] *= alpha;
 #pragma unroll 1
-      for (int i = 0; i < 64 && s0 + i <= t; ++i) {
-        const float wi = (float)(T)__shfl(w, i);
+      for (int i0 = 0; i0 < 64 && s0 + i0 <= t; i0 += 16) {
+        float y[16][D / 64];                // values of 16 keys (t's again behind t)
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          o[c] = __builtin_fmaf(wi, (float)vp[(s0 + i) * p.ld_v + 64 * c + lane], o[c]);
+        for (int i = 0; i < 16; ++i) {
+          const int u = s0 + i0 + i;
+          const T* row = vp + (u < t ? u : t) * p.ld_v + lane;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) y[i][c] = (float)row[64 * c];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float wi = (float)(T)__shfl(w, i0 + i);
+          const bool seen = s0 + i0 + i <= t;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) o[c] = seen ? __builtin_fmaf(wi, y[i][c], o[c]) : o[c];
+        }
       }
     }
     T* op = static_cast<T*>(p.o) + ((tl.a + t) * p.Hq + tl.hq) * (int64_t)D + lane;
@@ -195,8 +214,8 @@ __device__ __forceinline__ bool rows_again(const Tile& tl, int hk, int window, i
 #if __HIP_DEVICE_COMPILE__
   uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+s"(at));
-  const PrefillArgs& p = *reinterpret_cast<const PrefillArgs*>(at);
-  const T* v = static_cast<const T*>(p.v) + tl.a * p.ld_v + hk * D;
+  const PrefillArgs p = *reinterpret_cast<const PrefillArgs*>(at);
+  const T* v = in_global<T>(p.v) + tl.a * p.ld_v + hk * D;
   if (!unseen_not_finite<T, D>(v, p.ld_v, (int)tl.L, window, q0, rows)) return false;
   exact_rows<T, D>(p, tl, hk, window, q0, rows);
 #endif
