@@ -57,9 +57,8 @@ __device__ __forceinline__ LaneMap lane_map(int l, const RopeArgs& r) {
 // 32768 tokens, 4 heads: 25.6 us with them for all, 24.0 us so).  Results that
 // are rounded to bf16 or e4m3 take the hardware's sine, whose error (about
 // 2^-20) is far below their half step of 2^-8 or 2^-4; fp32 results take the
-// exact routine.  (UNROLL is the far positions' loop: rolled it leaves append,
-// d 64, registers for 8 waves to a SIMD instead of 6; unrolled norm_rope is 18 %
-// faster for near ones.)
+// exact routine.  (UNROLL is the far positions' loop: rolled it leaves append
+// registers; unrolled norm_rope is 18 % faster for near ones.)
 struct Freqs {
   float hi[8], lo[8];                       // inv_freq / 2 pi
 };
@@ -201,21 +200,25 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs p
 
 // ---------------------------------------------------------------------------
 // kv_append.  One workgroup for each (page that may get new tokens, head, key
-// or value): it holds the page's new rows in registers, 16 rows to a wave,
-// finds their largest magnitude, and writes their codes; where the scale of a
-// page that holds older tokens grows it also rounds those again.  So a row is
-// read once though its scale is known only after the page's last row.  HBM-bound
-// for many tokens (32768 tokens of 4 heads of 128, bf16, pages of 64: 101 MB in
-// 22.2 us, 4.5 TB/s), by latency and the waves that fit where pages are partly
-// filled (213 sequences of 40 tokens, 8 heads of 64, pages of 128: 27.8 us for
-// 26 MB), and by the launch for a token to a sequence (256: 4.3 us).
+// or value): it holds the page's new rows in registers, finds their largest
+// magnitude, and writes their codes; where the scale of a page that holds older
+// tokens grows it also rounds those again.  So a row is read once though its scale
+// is known only after the page's last row.  HBM-bound for many tokens (32768
+// tokens of 4 heads of 128, bf16, pages of 64: 101 MB in 22 us, 4.6 TB/s), by
+// latency and the waves that fit where pages are partly filled (213 sequences of
+// 40 tokens, 8 heads of 64, pages of 128: 20 us for 26 MB), and by the launch for
+// a token to a sequence (256: 4.3 us).
+//
+// A wave takes two passes of 1024 / D rows: as many registers as 5 waves to a
+// SIMD leave.  (One pass at D 64: 27.8 us for the 213 sequences; four at D 128
+// spill, 32768 tokens in pages of 128: 50 us instead of 24.)
 //
 // Which pages get tokens is known on the device only.  L new tokens behind a
 // length s touch at most floor(L / P) + 2 pages, so packed sequences own the
 // slots floor(cu[n] / P) + 2 n onwards and slots past a sequence's last page
 // leave at once.
 // ---------------------------------------------------------------------------
-constexpr int append_rows_per_wave(int P) { return P < 16 ? P : 16; }
+constexpr int append_rows_per_wave(int P, int D) { return P < 2048 / D ? P : 2048 / D; }
 
 __device__ __forceinline__ float pow2_scale(float amax) {
   // least 2^e with amax <= 448 2^e: amax = m 2^x, m in [1, 2), and 448 = 1.75 2^8
@@ -253,7 +256,7 @@ __device__ __forceinline__ void append_rows(const KvAppendArgs& p, const RopeArg
                                             bool is_k, int wrow, int row0, int l) {
   constexpr int LPR = D / 16;
   constexpr int RPW = 64 / LPR;               // rows of a wave's pass
-  constexpr int ROWS = append_rows_per_wave(P);
+  constexpr int ROWS = append_rows_per_wave(P, D);
   constexpr int PASSES = ROWS / RPW;
   constexpr int WAVES = P / ROWS;
   const PagedCache& kv = p.cache;
@@ -345,7 +348,7 @@ __device__ __forceinline__ void append_rows(const KvAppendArgs& p, const RopeArg
 }
 
 template <typename T, int D, bool INTER, int P>
-__global__ __launch_bounds__(64 * P / append_rows_per_wave(P), sizeof(T) == 2 ? 5 : 4) void kv_append_kernel(KvAppendArgs p) {
+__global__ __launch_bounds__(64 * P / append_rows_per_wave(P, D), sizeof(T) == 2 ? 5 : 4) void kv_append_kernel(KvAppendArgs p) {
   constexpr int LPR = D / 16;
   const int head = blockIdx.y;
   const bool is_k = blockIdx.z == 0;
@@ -377,7 +380,8 @@ __global__ __launch_bounds__(64 * P / append_rows_per_wave(P), sizeof(T) == 2 ? 
   const T* __restrict__ in = static_cast<const T*>(is_k ? p.k_raw : p.v_raw) + head * D;
   const int64_t ld = is_k ? p.ld_k : p.ld_v;
   const int l = threadIdx.x % LPR;
-  const int wrow = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * append_rows_per_wave(P);   // the wave's rows
+  // the wave's rows
+  const int wrow = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * append_rows_per_wave(P, D);
   const int row0 = wrow + (threadIdx.x & 63) / LPR;
   RopeArgs rope = p.rope;
   if (!is_k) rope.dim = 0;
@@ -401,10 +405,11 @@ hipError_t launch_append_t(const KvAppendArgs& a, hipStream_t stream) {
   const int P = a.cache.page_size;
   const dim3 grid((unsigned)kv_append_slots(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, P),
                   (unsigned)a.Hk, 2);
-  if (P == 16) kv_append_kernel<T, D, INTER, 16><<<grid, 64 * 16 / append_rows_per_wave(16), 0, stream>>>(a);
-  else if (P == 32) kv_append_kernel<T, D, INTER, 32><<<grid, 64 * 32 / append_rows_per_wave(32), 0, stream>>>(a);
-  else if (P == 64) kv_append_kernel<T, D, INTER, 64><<<grid, 64 * 64 / append_rows_per_wave(64), 0, stream>>>(a);
-  else kv_append_kernel<T, D, INTER, 128><<<grid, 64 * 128 / append_rows_per_wave(128), 0, stream>>>(a);
+  auto threads = [](int page) { return 64 * page / append_rows_per_wave(page, D); };
+  if (P == 16) kv_append_kernel<T, D, INTER, 16><<<grid, threads(16), 0, stream>>>(a);
+  else if (P == 32) kv_append_kernel<T, D, INTER, 32><<<grid, threads(32), 0, stream>>>(a);
+  else if (P == 64) kv_append_kernel<T, D, INTER, 64><<<grid, threads(64), 0, stream>>>(a);
+  else kv_append_kernel<T, D, INTER, 128><<<grid, threads(128), 0, stream>>>(a);
   return hipGetLastError();
 }
 
