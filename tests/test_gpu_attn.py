@@ -854,3 +854,15 @@ def test_binding_refuses_what_is_no_flag_and_no_stream():
         gdn.gdn_qk_norm_rope(x, q=x.clone(), stream=1 << 80)
     gdn.gdn_qk_norm_rope(x)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("window", [0, 300])
+def test_prefill_many_prompts_of_one_head(window):
+    """Packed prompts that more than a wave's lanes rank, few tiles in all."""
+    announce(f"prefill many prompts of one head, window={window}")
+    lens = torch.randint(0, 600, (70,), generator=gen(5)).tolist()
+    bounds = [0] + list(np.cumsum(lens))
+    host, dv = prefill_case(bounds[-1], 1, 1, 128, BF, 17)
+    o = gdn.gdn_attn_prefill(*dv, cu_seqlens=torch.tensor(bounds).cuda(), window=window)
+    torch.cuda.synchronize()
+    check_prefill(o, host, bounds, window, None, BF, 128)
