@@ -224,10 +224,11 @@ __device__ __forceinline__ bool rows_again(const Tile& tl, int hk, int window, i
 
 // ---------------------------------------------------------------------------
 // fp32: v_mfma_f32_16x16x4_f32.  A workgroup has 32 queries; waves 0 and 1 take
-// 16 each over the first 16 tokens of every key tile of 32, waves 2 and 3 the
-// same queries over the other 16, with a running maximum and sum of their own,
-// and the pairs join through LDS at the end.  Short prompts have few query
-// tiles, and this halves the time that one takes.  The next key tile is loaded
+// 16 each over the first 16 tokens of every key tile of 16 KW, waves 2 and 3 the
+// same queries over the next 16, and so on, with a running maximum and sum of
+// their own, and they join through LDS at the end.  Short prompts have few query
+// tiles, and this divides the time that one takes (KW 4 where there are few, see
+// split_f32, else 2).  The next key tile is loaded
 // into registers while this one is computed.  Bound by fp32 products and the
 // vector work between them: 4096 tokens, 16 heads of 128: 675 us, 102 TFLOP/s (a
 // plain fp32 product reaches 154).  (Without the bound on registers the compiler
@@ -235,14 +236,15 @@ __device__ __forceinline__ bool rows_again(const Tile& tl, int hk, int window, i
 // key tiles double-buffered in LDS, which leaves room for two workgroups instead
 // of three: 750 us.)
 // ---------------------------------------------------------------------------
-template <int D>
-__global__ __launch_bounds__(kThreads, D == 64 ? 4 : 3) void prefill_f32_kernel(PrefillArgs p, uint32_t blocks) {
-  constexpr int BM = 32, BN = 32, LD = D + 4, KB = D / 32, MT = D / 16;
-  constexpr int NL = BN * D / 4 / kThreads;           // 16-byte loads of a thread and tile
-  __shared__ __align__(16) float s_k[BN * LD], s_v[BN * LD];
-  __shared__ float s_m[32], s_l[32];
-  lds_nan_fill(s_k, sizeof s_k);
-  lds_nan_fill(s_v, sizeof s_v);
+template <int D, int KW>
+__global__ __launch_bounds__(128 * KW, KW == 4 ? 2 : D == 64 ? 4 : 3) void prefill_f32_kernel(PrefillArgs p, uint32_t blocks) {
+  constexpr int BM = 32, BN = 16 * KW, LD = D + 4, KB = D / 32, MT = D / 16;
+  constexpr int NT = 128 * KW;                        // threads
+  constexpr int NL = BN * D / 4 / NT;                 // 16-byte loads of a thread and tile
+  __shared__ __align__(16) float s_kv[2 * BN * LD];
+  __shared__ float s_m[KW - 1][32], s_l[KW - 1][32];
+  lds_nan_fill(s_kv, sizeof s_kv);
+  float *s_k = s_kv, *s_v = s_kv + BN * LD;
   const Tile tl = find_tile<BM>(p, blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -264,7 +266,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 3) void prefill_f32_kernel(
   auto load_tile = [&](int k0) {            // rows past the sequence are zero: they may
 #pragma unroll                              // belong to another one
     for (int e = 0; e < NL; ++e) {
-      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+      const int row = (e * NT + tid) / (D / 4), c = 4 * ((e * NT + tid) % (D / 4));
       kr[e] = vr[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k0 + row < L) {
         kr[e] = *reinterpret_cast<const float4*>(kb_ + (int64_t)(k0 + row) * p.ld_k + c);
@@ -295,7 +297,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 3) void prefill_f32_kernel(
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < NL; ++e) {
-      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+      const int row = (e * NT + tid) / (D / 4), c = 4 * ((e * NT + tid) % (D / 4));
       lds_check(s_k + row * LD + c, 16);
       *reinterpret_cast<float4*>(s_k + row * LD + c) = kr[e];
       *reinterpret_cast<float4*>(s_v + row * LD + c) = vr[e];
@@ -345,34 +347,41 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 3) void prefill_f32_kernel(
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
 
-  // waves 2 and 3 hand over through the key tile
-  static_assert(32 * LD <= BN * LD, "32 queries of sums");
+  // the other waves of the same queries hand over through the tiles
+  static_assert((KW - 1) * 32 <= 2 * BN, "32 queries of sums for each");
   __syncthreads();
-  if (wk == 1) {
+  if (wk > 0) {
 #pragma unroll
     for (int c = 0; c < MT; ++c) {
-      float* dst = s_k + (16 * wq + j) * LD + 16 * c + 4 * g;
+      float* dst = s_kv + ((wk - 1) * 32 + 16 * wq + j) * LD + 16 * c + 4 * g;
       lds_check(dst, 16);
       *reinterpret_cast<float4*>(dst) = make_float4(o[c][0], o[c][1], o[c][2], o[c][3]);
     }
-    if (g == 0) { s_m[16 * wq + j] = m; s_l[16 * wq + j] = l; }
+    if (g == 0) { s_m[wk - 1][16 * wq + j] = m; s_l[wk - 1][16 * wq + j] = l; }
   }
   __syncthreads();
-  if (wk == 1) return;
-  const float m1 = s_m[16 * wq + j], mm = fmaxf(m, m1);
-  const float f0 = exp2_fast(m - mm), f1 = exp2_fast(m1 - mm);
-  const float inv = 1.f / (l * f0 + s_l[16 * wq + j] * f1);   // a query sees itself: > 0
+  if (wk > 0) return;
+#pragma unroll
+  for (int w = 0; w < KW - 1; ++w) {
+    const float m1 = s_m[w][16 * wq + j], mm = fmaxf(m, m1);
+    const float f0 = exp2_fast(m - mm), f1 = exp2_fast(m1 - mm);
+    m = mm;
+    l = l * f0 + s_l[w][16 * wq + j] * f1;
+#pragma unroll
+    for (int c = 0; c < MT; ++c) {
+      const float4 u = *reinterpret_cast<const float4*>(s_kv + (w * 32 + 16 * wq + j) * LD + 16 * c + 4 * g);
+      o[c][0] = o[c][0] * f0 + u.x * f1;
+      o[c][1] = o[c][1] * f0 + u.y * f1;
+      o[c][2] = o[c][2] * f0 + u.z * f1;
+      o[c][3] = o[c][3] * f0 + u.w * f1;
+    }
+  }
+  const float inv = 1.f / l;                // a query sees itself: > 0
   float z = 0.f;                            // NaN where a sum is not finite
 #pragma unroll
-  for (int c = 0; c < MT; ++c) {
-    const float4 u = *reinterpret_cast<const float4*>(s_k + (16 * wq + j) * LD + 16 * c + 4 * g);
-    o[c][0] = o[c][0] * f0 + u.x * f1;
-    o[c][1] = o[c][1] * f0 + u.y * f1;
-    o[c][2] = o[c][2] * f0 + u.z * f1;
-    o[c][3] = o[c][3] * f0 + u.w * f1;
+  for (int c = 0; c < MT; ++c)
 #pragma unroll
     for (int r = 0; r < 4; ++r) z = __builtin_fmaf(o[c][r], 0.f, z);
-  }
   if (__any(z != z) && rows_again<float, D>(tl, hk, window, q0, 16)) return;
   float* op = static_cast<float*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * g;
 #pragma unroll
@@ -382,7 +391,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 3) void prefill_f32_kernel(
 
 // ---------------------------------------------------------------------------
 // bf16: v_mfma_f32_32x32x16_bf16, 32 queries to a wave, 128 to a workgroup (64
-// where there are few, see split_keys), key tiles of 64 tokens in LDS.
+// where there are few, see split_bf16), key tiles of 64 tokens in LDS.
 //
 // Lane 32 h + i holds, of a 32 x 32 product, column i and rows
 // 8 a + 4 h + b (a, b = 0..3), and supplies 8 k-values.  The score tile's rows
@@ -784,19 +793,24 @@ int64_t blocks_of(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq,
 }
 
 // With few query tiles a CU has one workgroup or none, and the last tile's walk
-// over its keys is the call's time: then two waves share a tile's keys.  It costs
+// over its keys is the call's time: then more waves share a tile's keys.  It costs
 // a tile twice the LDS and a hand-over, so not where a walk is short, nor where
-// the tiles fill the CUs twice anyway.  (us with 128 queries to a workgroup / 64
-// and the keys shared, d 128: 2048 tokens, 8 heads 36.7 / 23.2; 512 tokens, 16
-// heads 13.2 / 10.8; 2 prompts of 704 tokens in all, 12 heads 12.7 / 11.6; 4 of
-// 512, 16 heads 8.7 / 8.9; with 256 workgroups of the first kind: 4096 tokens, 8
-// heads 69 / 48.7, 1024 tokens, 32 heads 22.5 / 22.2; with 512: 2048 tokens, 32
-// heads 47 / 58.)
-bool split_keys(const PrefillArgs& a, int64_t blocks) {
+// the tiles fill the CUs anyway.  The mean keys of a prompt's last query:
+int64_t mean_keys(const PrefillArgs& a) {
   const int64_t len = a.cu_seqlens ? a.total_T / a.N : a.Tseq;
-  const int64_t keys = a.window > 0 && a.window < len ? a.window : len;
-  return blocks <= 256 && keys >= 256;
+  return a.window > 0 && a.window < len ? a.window : len;
 }
+// bf16, us with 128 queries to a workgroup / 64 and the keys shared, d 128: 2048
+// tokens, 8 heads 36.7 / 23.2; 512 tokens, 16 heads 13.2 / 10.8; 2 prompts of 704
+// tokens in all, 12 heads 12.7 / 11.6; 4 of 512, 16 heads 8.7 / 8.9; with 256
+// workgroups of the first kind: 4096 tokens, 8 heads 69 / 48.7, 1024 tokens, 32
+// heads 22.5 / 22.2; with 512: 2048 tokens, 32 heads 47 / 58.
+bool split_bf16(int64_t blocks, int64_t keys) { return blocks <= 256 && keys >= 256; }
+// fp32, us with 4 / 8 waves to 32 queries, d 128: 2352 tokens, 2 heads 138 / 118;
+// 3 prompts of 257 tokens in all, 4 heads of 64 7.9 / 7.6; 24 prompts of 304, 8
+// heads 8.5 / 9.3; with 512 workgroups: 2048 tokens, 8 heads 146 / 114; with 2048:
+// 4096 tokens, 16 heads 673 / 838.
+bool split_f32(int64_t blocks, int64_t keys) { return blocks <= 512 && keys >= 64; }
 
 }  // namespace
 
@@ -807,11 +821,17 @@ int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, in
 hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t stream) {
   const bool packed = a.cu_seqlens != nullptr;
   const int64_t blocks = prefill_blocks(a.N, a.total_T, a.Tseq, packed, a.Hq, a.io);
+  const int64_t keys = mean_keys(a);
   const dim3 grid((unsigned)blocks);
   if (a.io == DType::F32) {
-    if (a.d == 128) prefill_f32_kernel<128><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
-    else prefill_f32_kernel<64><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
-  } else if (split_keys(a, blocks)) {
+    if (split_f32(blocks, keys)) {
+      if (a.d == 128) prefill_f32_kernel<128, 4><<<grid, 512, 0, stream>>>(a, (uint32_t)blocks);
+      else prefill_f32_kernel<64, 4><<<grid, 512, 0, stream>>>(a, (uint32_t)blocks);
+    } else {
+      if (a.d == 128) prefill_f32_kernel<128, 2><<<grid, 256, 0, stream>>>(a, (uint32_t)blocks);
+      else prefill_f32_kernel<64, 2><<<grid, 256, 0, stream>>>(a, (uint32_t)blocks);
+    }
+  } else if (split_bf16(blocks, keys)) {
     const int64_t twice = blocks_of(a.N, a.total_T, a.Tseq, packed, a.Hq, 64);
     const dim3 grid2((unsigned)twice);
     if (a.d == 128) prefill_bf16_kernel<128, 2><<<grid2, kThreads, 0, stream>>>(a, (uint32_t)twice);

@@ -866,3 +866,17 @@ def test_prefill_many_prompts_of_one_head(window):
     o = gdn.gdn_attn_prefill(*dv, cu_seqlens=torch.tensor(bounds).cuda(), window=window)
     torch.cuda.synchronize()
     check_prefill(o, host, bounds, window, None, BF, 128)
+
+
+@pytest.mark.parametrize("window", [0, 64, 65, 300])
+@pytest.mark.parametrize("Hq,Hk,d", [(4, 2, 128), (3, 3, 64), (16, 1, 128)])
+def test_prefill_fp32_few_and_many_tiles(Hq, Hk, d, window):
+    """fp32: few query tiles (more waves to a tile's keys) and many of them."""
+    announce(f"prefill fp32 Hq={Hq} Hk={Hk} d={d} window={window}")
+    lens = [0, 1, 64, 65, 129, 330, 63, 0, 400]
+    bounds = [0] + list(np.cumsum(lens))
+    host, dv = prefill_case(bounds[-1], Hq, Hk, d, F32, 41 + Hq)
+    for N in (len(lens), 1):                 # the same rows as one prompt of 1052 tokens
+        o = gdn.gdn_attn_prefill(*dv, cu_seqlens=torch.tensor(bounds if N > 1 else [0, bounds[-1]]).cuda(), window=window)
+        torch.cuda.synchronize()
+        check_prefill(o, host, bounds if N > 1 else [0, bounds[-1]], window, None, F32, d)

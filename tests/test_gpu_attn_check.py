@@ -29,6 +29,7 @@ CASES = {
     "prefill, equal lengths": lambda: ta.test_prefill_equal_lengths_and_scales(3, 100, BF),
     "prefill, few long prompts": lambda: ta.test_prefill_few_long_prompts(4, 2, 128, 300),
     "prefill, few long prompts, d 64": lambda: ta.test_prefill_few_long_prompts(3, 3, 64, 0),
+    "prefill fp32, few and many tiles": lambda: ta.test_prefill_fp32_few_and_many_tiles(3, 3, 64, 65),
     "prefill, unseen values": lambda: ta.test_prefill_values_that_a_query_does_not_see(400, 128, 40, BF),
     "prefill, malformed offsets": ta.test_prefill_malformed_offsets_stay_in_bounds,
     "decode bf16": lambda: ta.test_decode(21, 3, 128, 64, 0, BF),
