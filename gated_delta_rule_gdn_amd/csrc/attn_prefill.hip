@@ -804,8 +804,13 @@ int64_t mean_keys(const PrefillArgs& a) {
 // tokens, 8 heads 36.7 / 23.2; 512 tokens, 16 heads 13.2 / 10.8; 2 prompts of 704
 // tokens in all, 12 heads 12.7 / 11.6; 4 of 512, 16 heads 8.7 / 8.9; with 256
 // workgroups of the first kind: 4096 tokens, 8 heads 69 / 48.7, 1024 tokens, 32
-// heads 22.5 / 22.2; with 512: 2048 tokens, 32 heads 47 / 58.
-bool split_bf16(int64_t blocks, int64_t keys) { return blocks <= 256 && keys >= 256; }
+// heads 22.5 / 22.2; with 512: 2048 tokens, 32 heads 47 / 58.  At d 64 two
+// workgroups of the second kind fit a CU: 288, 2048 tokens, 18 heads 30.0 / 21.5;
+// 384, 24 heads 29.5 / 25.7; 448, 28 heads 29.8 / 29.1; 315, 9 prompts of 640, 7
+// heads 12.6 / 13.7.
+bool split_bf16(int64_t blocks, int64_t keys, int d) {
+  return blocks <= 256 ? keys >= 256 : d == 64 && blocks <= 384 && keys >= 768;
+}
 // fp32, us with 4 / 8 waves to 32 queries, d 128: 2352 tokens, 2 heads 138 / 118;
 // 3 prompts of 257 tokens in all, 4 heads of 64 7.9 / 7.6; 24 prompts of 304, 8
 // heads 8.5 / 9.3; with 512 workgroups: 2048 tokens, 8 heads 146 / 114; with 2048:
@@ -831,7 +836,7 @@ hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t stream) {
       if (a.d == 128) prefill_f32_kernel<128, 2><<<grid, 256, 0, stream>>>(a, (uint32_t)blocks);
       else prefill_f32_kernel<64, 2><<<grid, 256, 0, stream>>>(a, (uint32_t)blocks);
     }
-  } else if (split_bf16(blocks, keys)) {
+  } else if (split_bf16(blocks, keys, a.d)) {
     const int64_t twice = blocks_of(a.N, a.total_T, a.Tseq, packed, a.Hq, 64);
     const dim3 grid2((unsigned)twice);
     if (a.d == 128) prefill_bf16_kernel<128, 2><<<grid2, kThreads, 0, stream>>>(a, (uint32_t)twice);
