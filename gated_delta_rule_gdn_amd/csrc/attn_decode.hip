@@ -160,8 +160,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
     cur = begin_round(n, blockIdx.x - (uint32_t)n * per_seq, 0, kv.seq_lens[n]);
     count = cur.rounds;
   } else {
-    for (int n0 = 0; n0 < N; n0 += 64)
-      total += n0 + lane < N ? rounds_of(kv.seq_lens[n0 + lane]) : 0;
+    // the lengths of 64 sequences, a lane each; of the first 64 read once
+    const int64_t first_lens = lane < N ? kv.seq_lens[lane] : 0;
+    auto lens_from = [&](int n0) {
+      return n0 == 0 ? first_lens : n0 + lane < N ? kv.seq_lens[n0 + lane] : 0;
+    };
+    for (int n0 = 0; n0 < N; n0 += 64) total += n0 + lane < N ? rounds_of(lens_from(n0)) : 0;
     total = wave_sum(total) * (int)per_seq;
     const DecodeShare share = decode_share(total, (int)gridDim.x, (int)blockIdx.x);
     at = share.at;
@@ -172,7 +176,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
     }
     int before = 0;                       // rounds of the sequences before n
     for (int n0 = 0;; n0 += 64) {
-      const int mine = (n0 + lane < N ? rounds_of(kv.seq_lens[n0 + lane]) : 0) * (int)per_seq;
+      const int64_t lens = lens_from(n0);
+      const int mine = (n0 + lane < N ? rounds_of(lens) : 0) * (int)per_seq;
       const int all = wave_sum(mine);
       if (before + all <= at && n0 + 64 < N) { before += all; continue; }
       int upto = mine;                    // inclusive scan over the lanes
@@ -185,7 +190,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
       const int i = past ? __ffsll((unsigned long long)past) - 1 : 0;
       const int n = n0 + i;
       before += __builtin_amdgcn_readlane(upto, i) - __builtin_amdgcn_readlane(mine, i);
-      const int64_t seq_len = kv.seq_lens[n];
+      const int64_t seq_len = read_lane(lens, i);
       const int rn = rounds_of(seq_len);
       const int seg = (at - before) / rn;
       cur = begin_round(n, (uint32_t)seg, at - before - seg * rn, seq_len);
