@@ -192,7 +192,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
       before += __builtin_amdgcn_readlane(upto, i) - __builtin_amdgcn_readlane(mine, i);
       const int64_t seq_len = read_lane(lens, i);
       const int rn = rounds_of(seq_len);
-      const int seg = (at - before) / rn;
+      int seg = (at - before) / rn;
+      if (seg > (int)per_seq - 1) seg = (int)per_seq - 1;   // (lengths that change meanwhile)
       cur = begin_round(n, (uint32_t)seg, at - before - seg * rn, seq_len);
       break;
     }
@@ -520,7 +521,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnDecodeArgs p, i
     if (chain[i].x >= 0) {
       const int k = before + __popcll(m & ((1ull << lane) - 1));
       s_start[k] = i * kThreads + tid;
-      s_end[k] = chain[i].y;
+      s_end[k] = chain[i].y < blocks ? chain[i].y : blocks - 1;
       s_seg[k] = chain[i].x;
     }
   }
