@@ -628,7 +628,10 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
     };
     // element (t, r) is token k0 + 4 h + at: not seen where at > tq - k0 - 4 h,
     // or at <= that less the window
-    const bool front = k0 + BN - 1 > q0, back = window && k0 <= q0 + 31 - window;
+    // (k0, the tiles and the queries' first are multiples of 64, so an inner tile ends
+    // before the workgroup's queries; without the code of its mask a 32K prompt is 2 %
+    // faster)
+    const bool front = !INNER && k0 + BN - 1 > q0, back = window && k0 <= q0 + 31 - window;
     if (front) {
       const int last = tq - k0 - 4 * h;
 #pragma unroll
