@@ -452,6 +452,8 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
 
+// WIN: with the code of a window's mask (calls without a window are 1 to 2 % faster
+// without it: 8 prompts of 4096 tokens 553 / 546 us, 4 short ones 9.0 / 8.8).
 // SPLIT 2: 64 queries to a workgroup; waves 0 and 1 take the even key tiles, 2
 // and 3 the odd ones, with a maximum and sum of their own, and join at the end.
 //
@@ -460,7 +462,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // while the maximum of tile i + 1 is formed, tile i's product with V is.  K
 // runs one tile ahead of V; both are double-buffered in LDS and loaded one
 // iteration before they are read, with one barrier to an iteration.
-template <int D, int SPLIT>
+template <int D, int SPLIT, bool WIN>
 __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void prefill_bf16_kernel(PrefillArgs p, uint32_t blocks) {
   constexpr int WQ = 4 / SPLIT;                       // waves with queries of their own
   constexpr int BM = 32 * WQ, BN = 64, KB = D / 16, MT = D / 32;
@@ -485,7 +487,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
   const bf16* kb_ = static_cast<const bf16*>(p.k) + tl.a * p.ld_k + hk * D;
   const bf16* vb_ = static_cast<const bf16*>(p.v) + tl.a * p.ld_v + hk * D;
 
-  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
+  const int window = WIN && p.window > 0 && p.window < L ? (int)p.window : 0;
   int lo = window ? qt0 - window + 1 : 0;             // first key that the tile sees
   lo = lo < 0 ? 0 : lo / BN * BN;
   const int stop = qt0 + BM < L ? qt0 + BM : L;
@@ -820,6 +822,19 @@ bool split_bf16(int64_t blocks, int64_t keys, int d) {
 // 4096 tokens, 16 heads 673 / 838.
 bool split_f32(int64_t blocks, int64_t keys) { return blocks <= 512 && keys >= 64; }
 
+template <int SPLIT>
+void launch_bf16(const PrefillArgs& a, int64_t blocks, hipStream_t stream) {
+  const dim3 grid((unsigned)blocks);
+  const uint32_t n = (uint32_t)blocks;
+  if (a.d == 128) {
+    if (a.window) prefill_bf16_kernel<128, SPLIT, true><<<grid, kThreads, 0, stream>>>(a, n);
+    else prefill_bf16_kernel<128, SPLIT, false><<<grid, kThreads, 0, stream>>>(a, n);
+  } else {
+    if (a.window) prefill_bf16_kernel<64, SPLIT, true><<<grid, kThreads, 0, stream>>>(a, n);
+    else prefill_bf16_kernel<64, SPLIT, false><<<grid, kThreads, 0, stream>>>(a, n);
+  }
+}
+
 }  // namespace
 
 int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType io) {
@@ -841,12 +856,9 @@ hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t stream) {
     }
   } else if (split_bf16(blocks, keys, a.d)) {
     const int64_t twice = blocks_of(a.N, a.total_T, a.Tseq, packed, a.Hq, 64);
-    const dim3 grid2((unsigned)twice);
-    if (a.d == 128) prefill_bf16_kernel<128, 2><<<grid2, kThreads, 0, stream>>>(a, (uint32_t)twice);
-    else prefill_bf16_kernel<64, 2><<<grid2, kThreads, 0, stream>>>(a, (uint32_t)twice);
+    launch_bf16<2>(a, twice, stream);
   } else {
-    if (a.d == 128) prefill_bf16_kernel<128, 1><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
-    else prefill_bf16_kernel<64, 1><<<grid, kThreads, 0, stream>>>(a, (uint32_t)blocks);
+    launch_bf16<1>(a, blocks, stream);
   }
   return hipGetLastError();
 }
