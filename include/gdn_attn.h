@@ -29,7 +29,10 @@
  *    neither a bad table nor a bad length makes a kernel touch memory outside
  *    the arguments.
  *  - Non-finite inputs: a token's non-finite q spoils its own output, its k and
- *    v the outputs of the queries that see it, and nothing else.
+ *    v the outputs of the queries that see it, and nothing else.  The weights
+ *    of a sum are below 2^8 before it is divided by theirs, so values are
+ *    summed without overflow while 2^8 sum |v| over the seen tokens is finite
+ *    in fp32.
  */
 #ifndef GDN_ATTN_H
 #define GDN_ATTN_H
