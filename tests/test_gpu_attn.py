@@ -880,3 +880,20 @@ def test_prefill_fp32_few_and_many_tiles(Hq, Hk, d, window):
         o = gdn.gdn_attn_prefill(*dv, cu_seqlens=torch.tensor(bounds if N > 1 else [0, bounds[-1]]).cuda(), window=window)
         torch.cuda.synchronize()
         check_prefill(o, host, bounds if N > 1 else [0, bounds[-1]], window, None, F32, d)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [130, 400])
+def test_prefill_query_that_is_not_finite(T, dtype):
+    """A NaN or infinite query spoils its own row only."""
+    announce(f"prefill NaN query T={T} {dtype}")
+    host, _ = prefill_case(T, 2, 1, 128, dtype, T)
+    q, k, v = [t.clone().contiguous() for t in host]
+    ro, ra, reach = oa.attention(q, k, v)
+    bound = attn_bound(ro, ra, reach, T, 128, dtype)
+    for j, bad in ((0, math.nan), (77, math.inf), (T - 1, math.nan)):
+        w = q.clone()
+        w[j, 1, 9] = bad
+        o = gdn.gdn_attn_prefill(w.cuda(), k.cuda(), v.cuda()).cpu()
+        o[j, 1] = torch.as_tensor(ro[j, 1]).to(o.dtype)
+        within(o, ro, bound, f"query {bad} at {j}")
