@@ -308,6 +308,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
       for (int r = 0; r < 4; ++r) x[4 * t + r] = acc[r] * (s.ks[t] * c_scale);
     }
     if (edge) {
+      // a first tile wholly before the window may be a page of its own, whose scale may be no
+      // number: 0 times it is not 0 (a second tile never is: steps begin at multiples of 32)
+      if (t0 + 16 <= lo) s.vs[0] = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t tok = t0 + 16 * (i / 4) + 4 * g + i % 4;

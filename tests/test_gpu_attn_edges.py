@@ -1,0 +1,42 @@
+"""GPU parity of the attention operators at the edges of their documented
+ranges, against the definitions in 64 bits."""
+import math
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+from attn_helpers import BF, F32, attn_bound, cache_case, cache_oracles, f64, gen, inv_freq, rope_bound, u8, within
+from helpers import announce
+from oracle import attention as oa
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU hosts, skipped there
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import gated_delta_rule_gdn_amd as gdn  # noqa: E402
+import test_gpu_attn as ta  # noqa: E402
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window,lens,width", [(12, [37, 28, 44], 3), (1000, [1025, 1080, 1016], 80)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_decode_scales_of_pages_before_the_window(window, lens, width, bad, dtype):
+    """Pages that lie wholly before the window have no part in the output, whatever their codes and scales,
+    also where the window begins in the second half of a step of 32 tokens (pages of 16; caches that one
+    workgroup takes whole, and joined ones)."""
+    announce(f"decode before the window window={window} bad={bad} {dtype}")
+    P, d = 16, 128
+    c = cache_case(len(lens), 2, d, P, width, seed=41)
+    for n, L in enumerate(lens):
+        for page in c["table"][n, :(L - window) // P].long():
+            for x in "kv":
+                c[x].view(torch.uint8)[page] = 0x7f
+                c[x + "s"][page] = bad
+    q = torch.randn(len(lens), 6, d, generator=gen(7)).to(dtype)
+    g = ta.to_dev(c)
+    o = gdn.gdn_attn_decode(q.cuda(), g["k"], g["v"], g["ks"], g["vs"], g["table"], torch.tensor(lens).cuda(), window=window)
+    torch.cuda.synchronize()
+    ta.check_decode(o, q, c, lens, window, None, dtype, P, d)
