@@ -16,7 +16,7 @@
 // and ends anywhere.
 // What a workgroup has of a segment is written straight to the output if that
 // is all of it, else as a partial result, and a second kernel joins those.
-// (Where no cache can be longer than kDirect tokens each workgroup has one
+// (Where no cache can be longer than kDecodeDirect tokens each workgroup has one
 // whole segment, and nothing is joined: a round costs a workgroup 1.2 us (fp32
 // 1.6), the second kernel about 5.  32 heads over 4, bf16 / fp32: 64 sequences
 // of 768 tokens 11.3 / 13.9 us so, joined 15.8 / 18.1; 2 sequences of 768 tokens
@@ -43,10 +43,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-constexpr int kStep = 32;                 // tokens of a wave's step
-constexpr int kRound = kWaves * kStep;    // tokens of a workgroup's step
-constexpr int64_t kBlocks = 512;         // workgroups that fill the chip: 2 to a CU
-constexpr int64_t kDirect = 6 * kRound;   // tokens of a cache that one workgroup takes whole
+constexpr int kStep = kDecodeStep;
+constexpr int kRound = kDecodeRound;
+constexpr int64_t kBlocks = kDecodeBlocks;
+static_assert(kRound == kWaves * kStep, "a step for each wave");
 constexpr float kNone = -1e30f;           // running maximum (log2 units) before any token
 
 // Two e4m3 codes (low or high half of a dword) as bf16.
@@ -592,18 +592,11 @@ hipError_t launch_t(const AttnDecodeArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// The tokens that a sequence can hold are known on the host (the width of the
-// page table), its length is not.
 AttnDecodePlan attn_decode_plan(int64_t N, int64_t max_tokens, int64_t window, int Hq, int Hk,
                                 int d) {
-  if (window > 0 && window + kStep < max_tokens) max_tokens = window + kStep;
-  const int64_t G = Hq / Hk, segments = N * Hk * ((G + 15) / 16);
-  const int64_t rounds = segments * ((max_tokens + kRound - 1) / kRound);
-  AttnDecodePlan p{segments, rounds, 0};
-  if (max_tokens <= kDirect) return p;
-  p.blocks = rounds < kBlocks ? rounds : kBlocks;
-  p.ws_floats = p.blocks * (2 * (G < 16 ? G : 16) * (d + 4) + 2);
-  return p;
+  const DecodePlan p = decode_plan(N, max_tokens, window, Hq, Hk);
+  return AttnDecodePlan{p.blocks, p.rounds,
+                        p.part_rows ? p.blocks * (2 * p.part_rows * (d + 4) + 2) : 0};
 }
 
 hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t stream) {

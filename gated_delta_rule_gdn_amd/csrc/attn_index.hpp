@@ -119,6 +119,25 @@ GDN_HD AppendPage append_page(int64_t seq_len, int64_t max_pages, int P, int64_t
   return r;
 }
 
+// How a decode call divides the caches.  The tokens that a sequence can hold are
+// known on the host (the width of the page table), its length is not.
+constexpr int kDecodeStep = 32;                     // tokens of a wave's step
+constexpr int kDecodeRound = 4 * kDecodeStep;       // of a workgroup's: 4 waves
+constexpr int64_t kDecodeBlocks = 512;              // workgroups that fill the chip: 2 to a CU
+constexpr int64_t kDecodeDirect = 6 * kDecodeRound; // tokens of a cache that one workgroup takes whole
+struct DecodePlan {
+  int64_t blocks, rounds;  // workgroups; most rounds of work there can be
+  int64_t part_rows;       // rows of a partial result; 0: every workgroup has a whole segment
+};
+GDN_HD DecodePlan decode_plan(int64_t N, int64_t max_tokens, int64_t window, int Hq, int Hk) {
+  // (a window may be as large as its type: nothing is added to it before it is small)
+  if (window > 0 && window < max_tokens - kDecodeStep) max_tokens = window + kDecodeStep;
+  const int64_t G = Hq / Hk, segments = N * Hk * ((G + 15) / 16);
+  const int64_t rounds = segments * ((max_tokens + kDecodeRound - 1) / kDecodeRound);
+  if (max_tokens <= kDecodeDirect) return DecodePlan{segments, rounds, 0};
+  return DecodePlan{rounds < kDecodeBlocks ? rounds : kDecodeBlocks, rounds, G < 16 ? G : 16};
+}
+
 // Tokens [lo, len) that a decode step sees.  They are taken in rounds of
 // `round` tokens from `first` on, a multiple of `step`; a sequence without
 // tokens has one (empty) round.

@@ -192,3 +192,16 @@ def test_index_arithmetic_stays_within_the_tensors(tmp_path):
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 def test_decode_shares_are_equal_and_complete(tmp_path):
     _run(tmp_path, "attn_share_check", [os.path.join(ROOT, "tests", "abi_check", "attn_share_check.cpp")], False)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_decode_plan_holds_for_windows_of_any_size(tmp_path):
+    _run(tmp_path, "attn_plan_check", [os.path.join(ROOT, "tests", "abi_check", "attn_plan_check.cpp")], False)
+
+
+@pytest.mark.parametrize("window", [2 ** 40, 2 ** 63 - 33, 2 ** 63 - 32, 2 ** 63 - 1])
+def test_decode_workspace_of_a_window_that_hides_nothing(window):
+    """A window beyond the cache is none: the call shares the same work in the same way."""
+    size = lambda w: gdn.lib.gdn_attn_decode_workspace_size(ctypes.byref(  # noqa: E731
+        gdn.GdnAttnDecodeDesc(1, 4096, 2048, w, 32, 4, 128, 64, BF, 0.1)))
+    assert size(window) == size(0) > 0

@@ -40,3 +40,21 @@ def test_decode_scales_of_pages_before_the_window(window, lens, width, bad, dtyp
     o = gdn.gdn_attn_decode(q.cuda(), g["k"], g["v"], g["ks"], g["vs"], g["table"], torch.tensor(lens).cuda(), window=window)
     torch.cuda.synchronize()
     ta.check_decode(o, q, c, lens, window, None, dtype, P, d)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [2 ** 63 - 32, 2 ** 63 - 1])
+def test_windows_of_any_size(window, dtype):
+    """A window beyond every token is none, bit for bit in decode."""
+    announce(f"window {window} {dtype}")
+    P, d, lens = 16, 128, [1, 37, 2000]
+    c = cache_case(len(lens), 2, d, P, 125, seed=5)
+    g = ta.to_dev(c)
+    q = torch.randn(len(lens), 4, d, generator=gen(2)).to(dtype).cuda()
+    run = lambda w: gdn.gdn_attn_decode(q, g["k"], g["v"], g["ks"], g["vs"], g["table"], torch.tensor(lens).cuda(), window=w)  # noqa: E731
+    assert torch.equal(run(window), run(0))
+    host, dv = ta.prefill_case(500, 4, 2, d, dtype, 9)
+    cu = torch.tensor([0, 70, 500])
+    for offsets in (None, cu.cuda()):
+        o = gdn.gdn_attn_prefill(*dv, cu_seqlens=offsets, window=window)
+        ta.check_prefill(o, host, [0, 500] if offsets is None else cu.tolist(), 0, None, dtype, d)
