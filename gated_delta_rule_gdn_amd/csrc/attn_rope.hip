@@ -52,15 +52,18 @@ __device__ __forceinline__ LaneMap lane_map(int l, const RopeArgs& r) {
 // in turns, reduced; pos * freq alone would lose 2^-24 of a far position's
 // angle.  Positions below 2^24 are exact in fp32, and the frequency in turns is
 // kept as two fp32 terms: the leading product's error comes back by an fma, its
-// whole turns leave exactly, and the rest is added (error 2^-25 turns).  Other
-// positions go through 64-bit floats, whose conversions are slow (an append of
-// 32768 tokens, 4 heads: 25.6 us with them for all, 24.0 us so).  Results that
+// whole turns leave exactly, and the rest is added: an error of 2^-25 turns up
+// to 2^22 turns, which frequencies of at most 1 stay below.  Other angles go
+// the same way in two 64-bit terms (positions are exact there up to 2^53), whose
+// conversions and products are slow (an append of 32768 tokens, 4 heads: 25.6 us
+// with one 64-bit term for all, 24.0 us so).  Results that
 // are rounded to bf16 or e4m3 take the hardware's sine, whose error (about
 // 2^-20) is far below their half step of 2^-8 or 2^-4; fp32 results take the
-// exact routine.  (UNROLL is the far positions' loop: rolled it leaves append
+// exact routine.  (UNROLL is the far angles' loop: rolled it leaves append
 // registers; unrolled norm_rope is 18 % faster for near ones.)
 struct Freqs {
   float hi[8], lo[8];                       // inv_freq / 2 pi
+  float most;                               // largest of |hi|
 };
 __device__ __forceinline__ void load_freqs(const RopeArgs& r, const LaneMap& m, Freqs& f) {
 #pragma clang fp contract(off)             // the products below are meant to be rounded
@@ -73,6 +76,7 @@ __device__ __forceinline__ void load_freqs(const RopeArgs& r, const LaneMap& m, 
   for (int i = 0; i < 8; ++i) {
     f.hi[i] = x[i] * kHi;
     f.lo[i] = __builtin_fmaf(x[i], kLo, __builtin_fmaf(x[i], kHi, -f.hi[i]));
+    f.most = i ? fmaxf(f.most, fabsf(f.hi[i])) : fabsf(f.hi[i]);
   }
 }
 
@@ -81,8 +85,8 @@ __device__ __forceinline__ void turn(int64_t pos, const Freqs& f, const RopeArgs
                                      const LaneMap& m, float* c, float* s) {
 #pragma clang fp contract(off)
   float r[8];                               // turns in [-1/2, 1/2]
-  if (pos < (1 << 24) && pos > -(1 << 24)) {
-    const float x = (float)(int)pos;
+  const float x = (float)(int)pos;          // (of near positions)
+  if (pos < (1 << 24) && pos > -(1 << 24) && fabsf(x) * f.most < 0x1p22f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float p = x * f.hi[i];
@@ -93,8 +97,11 @@ __device__ __forceinline__ void turn(int64_t pos, const Freqs& f, const RopeArgs
     const float* src = rope.inv_freq + m.f0;
 #pragma unroll UNROLL
     for (int i = 0; i < 8; ++i) {
-      const float x = src[i < 4 ? i : m.gap + i - 4];
-      const double t = (double)pos * ((double)x * 0.15915494309189533577);
+      constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / 2 pi
+      const double w = src[i < 4 ? i : m.gap + i - 4], at = (double)pos;
+      const double c1 = w * kHi, c2 = __builtin_fma(w, kHi, -c1) + w * kLo;
+      const double p = at * c1, e = __builtin_fma(at, c1, -p);
+      const double t = (p - __builtin_rint(p)) + __builtin_fma(at, c2, e);
       r[i] = (float)(t - __builtin_rint(t));
     }
   }

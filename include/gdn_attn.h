@@ -73,8 +73,10 @@ typedef struct gdn_qk_desc {
  *
  * for the channel pairs (a, b) of rope_mode; channels from rope_dim on are
  * not rotated.  The angle is formed and reduced to 2^-25 of a turn at every
- * position, so far ones lose nothing; frequencies scaled for long contexts come in through
- * inv_freq and rope_scale.  The rest is fp32, rounded once at the end.
+ * position up to +-2^53 and frequency up to 2^24, so far ones lose nothing;
+ * frequencies scaled for long contexts come in through inv_freq and rope_scale.
+ * The rest is fp32, rounded once at the end: x^2 is formed in it, so |x| < 2^60,
+ * and where eps is 0 the mean of a row's squares must be a normal number.
  *
  *   q_raw     [rows, H_q, d] io_dtype, row stride ld_q (NULL when H_q == 0)
  *   k_raw     [rows, H_k, d] io_dtype, row stride ld_k (NULL when H_k == 0)

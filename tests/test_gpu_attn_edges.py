@@ -58,3 +58,34 @@ def test_windows_of_any_size(window, dtype):
     for offsets in (None, cu.cuda()):
         o = gdn.gdn_attn_prefill(*dv, cu_seqlens=offsets, window=window)
         ta.check_prefill(o, host, [0, 500] if offsets is None else cu.tolist(), 0, None, dtype, d)
+
+
+def spin(x, pos, f, inter):
+    """x [rows, H, d] rotated by pos * f, each angle reduced in rational numbers."""
+    two_pi = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+    turn = np.array([[float(Fraction(int(p)) * Fraction(float(w)) / two_pi % 1) for w in f] for p in pos])
+    c, s = np.cos(2 * np.pi * turn)[:, None], np.sin(2 * np.pi * turn)[:, None]
+    y, half = f64(x).copy(), len(f)
+    ia = slice(0, 2 * half, 2) if inter else slice(0, half)
+    ib = slice(1, 2 * half, 2) if inter else slice(half, 2 * half)
+    a, b = f64(x)[..., ia], f64(x)[..., ib]
+    y[..., ia], y[..., ib] = a * c - b * s, b * c + a * s
+    return y
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("grow", [1.0, 64.0, 1e4])
+def test_norm_rope_angles_at_every_position(grow, inter, dtype):
+    """The angle's error is 2^-25 of a turn at near and far positions alike, and for frequencies above 1 too
+    (products up to 2^53 times 1, or 2^24 times 10^4): the bound has no term that grows with the position."""
+    announce(f"norm_rope angles grow={grow} inter={inter} {dtype}")
+    d, most = 64, 53 if grow == 1.0 else 40
+    pos = [0, 1, -1, 4097, (1 << 24) - 1, 1 << 24, -(1 << 24), (1 << 24) + 1, 12345678, (1 << 31) + 5, -(1 << 33) - 7]
+    pos += [(1 << e) - 3 * e for e in range(25, most + 1, 2)] + [(1 << most) - 1]
+    f = inv_freq(d) * grow
+    x = torch.randn(len(pos), 2, d, generator=gen(3)).to(dtype)
+    q, _ = gdn.gdn_qk_norm_rope(x.cuda(), positions=torch.tensor(pos).cuda(), inv_freq=f.cuda(), interleaved=inter)
+    torch.cuda.synchronize()
+    ref = spin(x, pos, f.tolist(), inter)
+    within(q, ref, rope_bound(ref, f64(x), 1.0, dtype), "angles")
