@@ -47,7 +47,6 @@ constexpr int kStep = kDecodeStep;
 constexpr int kRound = kDecodeRound;
 constexpr int64_t kBlocks = kDecodeBlocks;
 static_assert(kRound == kWaves * kStep, "a step for each wave");
-constexpr float kNone = -1e30f;           // running maximum (log2 units) before any token
 
 // Two e4m3 codes (low or high half of a dword) as bf16.
 template <bool HI>
@@ -341,7 +340,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(AttnDecodeArgs
     bf16x8 w[NT];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float e = exp2_fast(x[i] - m);
+      const float e = weight_of(x[i], m);
       l += e;
       bf16 t[NT];
       split_terms<NT>(e * s.vs[i / 4], t);

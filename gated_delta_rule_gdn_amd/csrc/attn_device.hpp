@@ -12,6 +12,18 @@ namespace gdn {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+// Running maximum (log2 units) before any token: at or below every finite score, and
+// a masked one (-inf) less it is -inf.
+constexpr float kNone = -3.402823466e+38f;
+
+// The weight of a score x that is at most a little above the running maximum m.  Both
+// are rounded, so their difference is small for the largest however large they are;
+// fused with the product that gives x it would be off by half a step of m.
+__device__ __forceinline__ float weight_of(float x, float m) {
+#pragma clang fp contract(off)
+  return exp2_fast(x - m);
+}
+
 __device__ __forceinline__ int64_t read_lane(int64_t x, int lane) {
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane);
   const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)x >> 32), lane);

@@ -25,7 +25,6 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kNone = -1e30f;           // running maximum (log2 units) before any token
 
 // One workgroup's query tile: queries [q0, q0 + BM) of the sequence that is
 // rows [a, a + L) of the packed tensors, and a query head.
@@ -125,6 +124,11 @@ __device__ __forceinline__ Tile find_tile(const PrefillArgs& p, uint32_t blocks)
 // of its queries [q0, q0 + rows) do not see (tiles end less than 160 tokens from
 // q0 on either side of what is seen), and if any is not finite it computes its
 // rows again by exact_rows, which touches seen tokens only.
+// So does a wave of the bf16 kernel whose running maximum was huge: its weights
+// are 2^(s c - m) with an unrounded product and m off by half a step, the same
+// factor on all of a query's weights and so none on its output, until it leaves
+// the range of fp32.  Below 2^24 it is 2 at most.  (The product rounded first
+// takes another instruction for each of 32 weights.)
 template <typename T, int D>
 __device__ __forceinline__ bool unseen_not_finite(const T* __restrict__ v, int64_t ld, int L,
                                                   int window, int q0, int rows) {
@@ -155,6 +159,7 @@ template <typename T, int D>
 __device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl, int hk, int window,
                                            int q0, int rows) {
   const int lane = threadIdx.x & 63, L = (int)tl.L;
+  const float c_scale = p.scale * kLog2e;
   const T* kp = in_global<T>(p.k) + tl.a * p.ld_k + hk * D;
   const T* vp = in_global<T>(p.v) + tl.a * p.ld_v + hk * D;
   for (int t = q0; t < q0 + rows && t < L; ++t) {
@@ -171,9 +176,9 @@ __device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl,
 #pragma unroll
         for (int i = 0; i < 8; ++i) x = __builtin_fmaf(a[i], b[i], x);
       }
-      x = s0 + lane <= t ? x * p.scale * kLog2e : -__builtin_huge_valf();
+      x = s0 + lane <= t ? x * c_scale : -__builtin_huge_valf();
       const float m_new = fmaxf(m, wave_max(x));
-      const float alpha = exp2_fast(m - m_new), w = exp2_fast(x - m_new);
+      const float alpha = exp2_fast(m - m_new), w = weight_of(x, m_new);
       m = m_new;
       float sum = w;
 #pragma unroll
@@ -206,17 +211,19 @@ __device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl,
   }
 }
 
-// Both, for the end of a kernel: true if the rows are written.  The arguments are
+// Both, for the end of a kernel: true if the rows are written (always if `huge`, the
+// wave's maximum was).  The arguments are
 // read from the kernel's argument segment again, where `p` is its first: kept in
 // registers for this rare end they would spill others (2 % of a prompt).
 template <typename T, int D>
-__device__ __forceinline__ bool rows_again(const Tile& tl, int hk, int window, int q0, int rows) {
+__device__ __forceinline__ bool rows_again(const Tile& tl, int hk, int window, int q0, int rows,
+                                           bool huge) {
 #if __HIP_DEVICE_COMPILE__
   uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+s"(at));
   const PrefillArgs p = *reinterpret_cast<const PrefillArgs*>(at);
   const T* v = in_global<T>(p.v) + tl.a * p.ld_v + hk * D;
-  if (!unseen_not_finite<T, D>(v, p.ld_v, (int)tl.L, window, q0, rows)) return false;
+  if (!huge && !unseen_not_finite<T, D>(v, p.ld_v, (int)tl.L, window, q0, rows)) return false;
   exact_rows<T, D>(p, tl, hk, window, q0, rows);
 #endif
   return true;
@@ -336,7 +343,7 @@ __global__ __launch_bounds__(128 * KW, KW == 4 ? 2 : D == 64 ? 4 : 3) void prefi
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float e = exp2_fast(x[r] - m);
+      const float e = weight_of(x[r], m);
       l += e;
       const float* vl = s_v + (16 * wk + 4 * g + r) * LD + j;
 #pragma unroll
@@ -376,13 +383,13 @@ __global__ __launch_bounds__(128 * KW, KW == 4 ? 2 : D == 64 ? 4 : 3) void prefi
       o[c][3] = o[c][3] * f0 + u.w * f1;
     }
   }
-  const float inv = 1.f / l;                // a query sees itself: > 0
+  const float inv = 1.f / l;                // a query sees itself, with a score above kNone: > 0
   float z = 0.f;                            // NaN where a sum is not finite
 #pragma unroll
   for (int c = 0; c < MT; ++c)
 #pragma unroll
     for (int r = 0; r < 4; ++r) z = __builtin_fmaf(o[c][r], 0.f, z);
-  if (__any(z != z) && rows_again<float, D>(tl, hk, window, q0, 16)) return;
+  if (__any(z != z) && rows_again<float, D>(tl, hk, window, q0, 16, false)) return;
   float* op = static_cast<float*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * g;
 #pragma unroll
   for (int c = 0; c < MT; ++c)
@@ -567,7 +574,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[c][r] = 0.f;
   float m = kNone, l = 0.f;
-
+  bool huge = false;                        // some query's m was 2^24 or more (see above)
 
   auto scores = [&](const bf16* kt, f32x16* s) {
 #pragma unroll
@@ -657,6 +664,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
     if (__any(mx > m + 8.f)) {
       const float m_new = fmaxf(m, mx);
       const float alpha = exp2_fast(m - m_new);
+      huge |= __any(fabsf(m_new) >= 0x1p24f && fabsf(m_new) < -kNone) != 0;
       m = m_new;
       l *= alpha;
 #pragma unroll
@@ -740,6 +748,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
     wait_tiles();
     float* so = reinterpret_cast<float*>(&s_v[0][0]) + wq * (16 * MT * 64) + lane;
     float* sm = reinterpret_cast<float*>(&s_k[1][0]) + wq * 128 + lane;
+    uint32_t* s_huge = reinterpret_cast<uint32_t*>(&s_k[1][0]) + WQ * 128;
     static_assert(WQ * 16 * MT * 64 * sizeof(float) <= sizeof s_v && BM <= STEP, "the sums fit");
     if (wk == 1) {
 #pragma unroll
@@ -751,9 +760,11 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
         }
       sm[0] = m;
       sm[64] = l;
+      if (lane == 0) s_huge[wq] = huge;
     }
     wait_tiles();
     if (wk == 1) return;
+    huge |= s_huge[wq] != 0;
     const float m1 = sm[0], mm = fmaxf(m, m1);
     const float f0 = exp2_fast(m - mm), f1 = exp2_fast(m1 - mm);
     l = l * f0 + sm[64] * f1;
@@ -762,7 +773,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[c][r] = o[c][r] * f0 + so[(16 * c + r) * 64] * f1;
   }
-  const float inv = 1.f / l;                // a query sees itself: l > 0
+  const float inv = 1.f / l;                // a query sees itself, with a score above kNone: > 0
   // rows leave through LDS (this wave's part of the key tiles, which no wave
   // reads any more), so that a store covers whole rows
   if constexpr (SPLIT == 1) wait_tiles();
@@ -773,7 +784,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
 #pragma unroll
     for (int r = 0; r < 16; ++r) z[r % 4] = __builtin_fmaf(o[c][r], 0.f, z[r % 4]);
   z[0] += z[1] + (z[2] + z[3]);
-  if (__any(z[0] != z[0]) && rows_again<bf16, D>(tl, hk, window, q0, 32)) return;
+  if ((huge || __any(z[0] != z[0])) && rows_again<bf16, D>(tl, hk, window, q0, 32, huge)) return;
   bf16* so = &s_k[0][0] + wq * 32 * D;
 #pragma unroll
   for (int c = 0; c < MT; ++c)

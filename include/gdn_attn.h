@@ -30,9 +30,12 @@
  *    the arguments.
  *  - Non-finite inputs: a token's non-finite q spoils its own output, its k and
  *    v the outputs of the queries that see it, and nothing else.  The weights
- *    of a sum are below 2^8 before it is divided by theirs, so values are
- *    summed without overflow while 2^8 sum |v| over the seen tokens is finite
- *    in fp32.
+ *    of a sum are below 2^9 before it is divided by theirs, so values are
+ *    summed without overflow while 2^9 sum |v| over the seen tokens (in a cache,
+ *    and 2^9 times its pages' scales) is finite in fp32.
+ *  - Scores are formed in fp32 as (q . k) (scale log2 e) and may be of any size
+ *    there: both factors and the score below 2^127.  (gdn_attn_prefill in bf16
+ *    computes rows whose scores reach 2^24 one after another, which is slow.)
  */
 #ifndef GDN_ATTN_H
 #define GDN_ATTN_H

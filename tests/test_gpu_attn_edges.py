@@ -89,3 +89,70 @@ def test_norm_rope_angles_at_every_position(grow, inter, dtype):
     torch.cuda.synchronize()
     ref = spin(x, pos, f.tolist(), inter)
     within(q, ref, rope_bound(ref, f64(x), 1.0, dtype), "angles")
+
+
+def ties(score, v, window):
+    """Attention where scores are equal or far apart: the mean of the values of the largest; and of |v|."""
+    T = len(v)
+    o, a = np.zeros((T,) + v.shape[1:]), np.zeros((T,) + v.shape[1:])
+    for t in range(T):
+        lo = max(0, t + 1 - window) if window else 0
+        top = score[lo:t + 1] == score[lo:t + 1].max()
+        o[t], a[t] = v[lo:t + 1][top].mean(0), np.abs(v[lo:t + 1][top]).mean(0)
+    return o, a
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,window,d", [(1, 0, 128), (40, 0, 64), (300, 0, 128), (300, 50, 64), (600, 0, 128)])
+@pytest.mark.parametrize("size", [8, 14, 20, 56])
+def test_prefill_scores_of_any_finite_size(size, T, window, d, dtype):
+    """Scores around +-2^(2 size): equal ones share the weight, the others are too far apart for any. The
+    products are exact, so equal scores are equal in the kernels too, and the bound has no term for their error."""
+    announce(f"prefill scores 2^{2 * size} T={T} window={window} d={d} {dtype}")
+    g = gen(T + size)
+    c = (1 + torch.randint(0, 8, (T,), generator=g) / 8) * (torch.randint(0, 2, (T,), generator=g) * 2 - 1)
+    c[0] = -c[0].abs()
+    q, k = torch.zeros(T, 2, d), torch.zeros(T, 1, d)
+    q[..., 3] = 2.0 ** size
+    k[:, 0, 3] = c * 2.0 ** size
+    v = torch.randn(T, 1, d, generator=g).to(dtype)
+    for scale in (0.125, -0.125):
+        o = gdn.gdn_attn_prefill(q.to(dtype).cuda(), k.to(dtype).cuda(), v.cuda(), window=window, scale=scale)
+        ro, ra = ties(np.sign(scale) * f64(c), f64(v), window)
+        ro, ra = np.repeat(ro, 2, 1), np.repeat(ra, 2, 1)
+        within(o, ro, attn_bound(ro, ra, 0.0, T, d, dtype), f"scale {scale}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("width", [8, 160])
+@pytest.mark.parametrize("size", [8, 14, 20, 56])
+def test_decode_scores_of_any_finite_size(size, width, dtype):
+    """The same over a cache that one workgroup takes whole and over a joined one."""
+    announce(f"decode scores 2^{2 * size} width={width} {dtype}")
+    P, d, Hk = 16, 128, 2
+    lens = [1, 2, 33, width * P - 5, 0]
+    c = cache_case(len(lens), Hk, d, P, width, seed=size)
+    g = gen(size)
+    code = (1 + torch.randint(0, 8, c["k"].shape[:3], generator=g) / 8) * (torch.randint(0, 2, c["k"].shape[:3], generator=g) * 2 - 1)
+    code = -code.abs() if size == 56 else code
+    k = torch.zeros(c["k"].shape)
+    k[..., 5] = code
+    c["k"], c["ks"] = k.to(torch.float8_e4m3fn), torch.full_like(c["ks"], 2.0 ** size)
+    _, ov = cache_oracles(c)
+    q = torch.zeros(len(lens), 4, d)
+    q[..., 5] = 2.0 ** size
+    e = ta.to_dev(c)
+    for scale in (0.125, -0.125):
+        o = gdn.gdn_attn_decode(q.to(dtype).cuda(), e["k"], e["v"], e["ks"], e["vs"], e["table"],
+                                torch.tensor(lens).cuda(), scale=scale)
+        for n, L in enumerate(lens):
+            if L == 0:
+                assert bool((o[n] == 0).all())
+                continue
+            v, _ = ov.tokens(n, L)
+            at = [(int(c["table"][n, t // P]), t % P) for t in range(L)]
+            for h in range(4):
+                s = np.sign(scale) * np.array([float(code[p, h // 2, r]) for p, r in at])
+                top = s == s.max()
+                ro, ra = v[top, h // 2].mean(0), np.abs(v[top, h // 2]).mean(0)
+                within(o[n, h], ro, attn_bound(ro, ra, 0.0, L, d, dtype), f"sequence {n} head {h} scale {scale}")
