@@ -498,7 +498,9 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
   int lo = window ? qt0 - window + 1 : 0;             // first key that the tile sees
   lo = lo < 0 ? 0 : lo / BN * BN;
   const int stop = qt0 + BM < L ? qt0 + BM : L;
-  const int mine = q0 + 32 < stop ? q0 + 32 : stop;   // this wave needs keys before it
+  // this wave needs keys before it; behind the prompt's end it has no queries: it
+  // loads its share of the tiles and computes nothing
+  const int mine = q0 >= L ? 0 : q0 + 32 < stop ? q0 + 32 : stop;
 
   // loads of one tile: row r0 + e RL, permuted so that LDS position pc of row r
   // gets chunk k_chunk(r, pc); rows past the sequence repeat its last one
@@ -602,10 +604,15 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
   };
 
   f32x16 s[2];
-  scores(s_k[0] + wk * BN * D, s);
-  float mx = top(s);
+  float mx = kNone;
+  if (lo_w < mine) {
+    check_true(q0 < L && lo_w < stop);      // the queries and the tile were loaded
+    scores(s_k[0] + wk * BN * D, s);
+    mx = top(s);
+  }
   // One iteration: tile k0's scores are in s, V's buffer is `buf`; leaves the
-  // next tile's scores in sn and their maximum in mx.
+  // next tile's scores in sn and their maximum in mx (behind the last tile: of what
+  // the buffer holds, and nothing reads them).
   // INNER: the tiles to load exist and are whole; their loads are then spread
   // over the score products (all at once they keep a wave from its products for
   // as long as the address unit takes over four waves' 32 KB: 1.4 % of a 32K
@@ -627,6 +634,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
         load_tile(vb_, p.ld_v, lv2, cv, 0u, s_v[buf ^ 1] + wk * BN * D, k0 + STEP);
       if (k0 >= mine) return;               // nothing left for this wave to see
     }
+    check_true(q0 < L);
     constexpr int LP = 2 * KB / (2 * NL);   // score products to a load
     static_assert(!INNER || LP >= 1, "a place for every load");
     auto load_part = [&](int e) {           // K's loads, then V's
@@ -735,7 +743,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
   int k0 = lo;
   const int dk = BN * wk;
   // (D 64 has no registers left for the two forms)
-  for (; D == 128 && k0 + 3 * STEP < stop && k0 + 4 * STEP <= L; k0 += 2 * STEP) {
+  for (; D == 128 && q0 < L && k0 + 3 * STEP < stop && k0 + 4 * STEP <= L; k0 += 2 * STEP) {
     step(std::bool_constant<D == 128>{}, k0 + dk, 0, s, s1);
     step(std::bool_constant<D == 128>{}, k0 + dk + STEP, 1, s1, s);
   }
@@ -777,6 +785,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
   // rows leave through LDS (this wave's part of the key tiles, which no wave
   // reads any more), so that a store covers whole rows
   if constexpr (SPLIT == 1) wait_tiles();
+  if (q0 >= L) return;
   static_assert(BM <= 2 * STEP, "the waves' rows fit into the key tiles");
   float z[4] = {0.f, 0.f, 0.f, 0.f};        // NaN where a sum is not finite
 #pragma unroll

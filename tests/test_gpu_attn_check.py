@@ -52,3 +52,15 @@ def check_library():
 @pytest.mark.parametrize("case", list(CASES))
 def test_parity_under_lds_checks(check_library, case):
     CASES[case]()
+
+
+@pytest.mark.parametrize("window", [0, 16, 300])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[1, 129, 0, 190], [500, 33, 1217], [2048 + 65], [1, 2, 3, 31] * 40])
+def test_waves_without_queries_compute_nothing(check_library, lens, d, window):
+    """The last tile of a prompt may have waves whose queries all lie behind its end: nothing is loaded for
+    them, and they form no scores of what the LDS held before (a condition of the debug library's kernels)."""
+    bounds = [0] + list(ta.np.cumsum(lens))
+    host, dv = ta.prefill_case(bounds[-1], 4, 2, d, BF, 51)
+    o = ta.gdn.gdn_attn_prefill(*dv, cu_seqlens=torch.tensor(bounds).cuda(), window=window)
+    ta.check_prefill(o, host, bounds, window, None, BF, d)
