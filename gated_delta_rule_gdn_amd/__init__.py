@@ -2,7 +2,8 @@
 
 The computation lives in libgdn.so (C ABI, include/gdn.h and, for the
 softmax-attention layers of hybrids, include/gdn_attn.h), built from the HIP
-sources under csrc/.  This package holds the thin ctypes binding only.
+sources under csrc/.  This package holds the thin bindings only: ctypes, and for
+the attention calls an extension module (attn.py), without which they alone raise.
 """
 from .gdn import (  # noqa: F401
     GDN_BF16, GDN_ERR_CHECK, GDN_ERR_HIP, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_F32,

@@ -15,11 +15,30 @@ from torch._C import _cuda_getCurrentRawStream
 
 from .gdn import _DT, GDN_OK, GdnError, lib
 
-try:
-    from . import _attn_native as _native
-except ImportError as e:
-    raise ImportError(f"the extension module _attn_native is missing or does not load ({e}): build it with "
-                      "`python gated_delta_rule_gdn_amd/build.py`") from e
+
+class _Missing:
+    """In place of an extension module that does not load: the attention calls raise,
+    the rest of the package needs nothing of it."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the extension module _attn_native is missing or does not load ({self.why}): build it "
+                          "with `python gated_delta_rule_gdn_amd/build.py`")
+
+
+def _load_native():
+    # the file's name holds the Python that it is for, the module the torch
+    try:
+        from . import _attn_native as native
+    except ImportError as e:
+        return _Missing(e)
+    here = torch.__version__.split("+")[0]
+    return native if native.torch_version == here else _Missing(f"built for torch {native.torch_version}, this is {here}")
+
+
+_native = _load_native()
 
 GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
 ATTN_ABI_VERSION = 1

@@ -14,6 +14,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,7 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdn.so")
 LIB_CHECK = os.path.join(PKG, "libgdn_check.so")
-MODULE = os.path.join(PKG, "_attn_native.so")
+MODULE = os.path.join(PKG, "_attn_native" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["gdn_api.cpp", "decode.hip", "chunk_fwd.hip", "chunk_fwd_sb.hip", "layer_ops.hip",
@@ -49,8 +50,6 @@ MAX_JOBS = 8
 
 def module_command() -> list:
     """g++ on csrc/attn_bind.cpp against this interpreter's and torch's headers."""
-    import sysconfig
-
     import torch
 
     inc = os.path.join(os.path.dirname(torch.__file__), "include")

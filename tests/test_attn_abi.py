@@ -8,6 +8,8 @@ import os
 import re
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 import pytest
 import torch
@@ -205,3 +207,36 @@ def test_decode_workspace_of_a_window_that_hides_nothing(window):
     size = lambda w: gdn.lib.gdn_attn_decode_workspace_size(ctypes.byref(  # noqa: E731
         gdn.GdnAttnDecodeDesc(1, 4096, 2048, w, 32, 4, 128, 64, BF, 0.1)))
     assert size(window) == size(0) > 0
+
+
+def _python(code):
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout
+
+
+@pytest.mark.parametrize("how", ["missing", "other torch"])
+def test_package_works_without_the_extension_module(how):
+    """The delta rule needs libgdn.so alone; the attention calls say what is missing."""
+    stand_in = "None" if how == "missing" else "types.SimpleNamespace(torch_version='0.0.1')"
+    out = _python(f"""
+import sys, types, torch
+sys.modules["gated_delta_rule_gdn_amd._attn_native"] = {stand_in}
+if {how == "other torch"}:
+    import importlib.machinery
+    sys.modules["gated_delta_rule_gdn_amd._attn_native"].__spec__ = importlib.machinery.ModuleSpec("x", None)
+import gated_delta_rule_gdn_amd as gdn
+assert gdn.abi_version() > 0 and gdn.attn_abi_version() == 1
+x = torch.zeros(4, 2, 64)
+try:
+    gdn.gdn_kv_append(x, x, x, x, x, x, x, x)
+except ImportError as e:
+    print("refused:", e)
+""")
+    assert "refused:" in out and "build.py" in out
+
+
+def test_extension_module_names_the_python_and_torch_it_is_for():
+    from gated_delta_rule_gdn_amd import attn
+    assert attn._native.__file__.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert attn._native.torch_version == torch.__version__.split("+")[0]
