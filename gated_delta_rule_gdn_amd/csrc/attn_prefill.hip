@@ -428,16 +428,21 @@ __device__ __forceinline__ bf16x4 read_tr16(const bf16* p) {
 // 16 bytes for each lane from base + voff + soff straight into LDS at
 // lds + 16 * lane (lds is the same for the wave).  The load is counted by
 // vmcnt like any other; the compiler does not know of it, so wait_tiles()
-// stands before the barrier behind which the bytes are read.  (m0 is a reserved
-// register: the compiler sets it before each use of its own.)
+// stands before the barrier behind which the bytes are read.  m0 is set in the same
+// block and named as clobbered; the compiler warns that it is a reserved register,
+// which it sets before each use of its own.  (As an operand "{m0}" its writes are
+// merged across the blocks, and tiles land in the wrong place.)
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void load_lds16(uint32_t lds, i32x4 base, uint32_t voff, uint32_t soff) {
 #if __HIP_DEVICE_COMPILE__
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
       "s_nop 0\n\t"
       "buffer_load_dwordx4 %1, %2, %3 offen lds"
-      ::"s"(lds), "v"(voff), "s"(base), "s"(soff) : "memory");
+      ::"s"(lds), "v"(voff), "s"(base), "s"(soff) : "memory", "m0");
+#pragma clang diagnostic pop
 #endif
 }
 // This wave's loads have landed and its LDS reads are done; then all waves'.
@@ -841,6 +846,12 @@ bool split_bf16(int64_t blocks, int64_t keys, int d) {
 // heads 8.5 / 9.3; with 512 workgroups: 2048 tokens, 8 heads 146 / 114; with 2048:
 // 4096 tokens, 16 heads 673 / 838.
 bool split_f32(int64_t blocks, int64_t keys) { return blocks <= 512 && keys >= 64; }
+
+// rows_again reads PrefillArgs where a kernel's arguments begin.
+using PrefillKernel = void (*)(PrefillArgs, uint32_t);
+static_assert(std::is_same<decltype(&prefill_bf16_kernel<128, 1, true>), PrefillKernel>::value &&
+                  std::is_same<decltype(&prefill_f32_kernel<128, 2>), PrefillKernel>::value,
+              "PrefillArgs is the first argument");
 
 template <int SPLIT>
 void launch_bf16(const PrefillArgs& a, int64_t blocks, hipStream_t stream) {
