@@ -156,3 +156,82 @@ def test_decode_scores_of_any_finite_size(size, width, dtype):
                 top = s == s.max()
                 ro, ra = v[top, h // 2].mean(0), np.abs(v[top, h // 2]).mean(0)
                 within(o[n, h], ro, attn_bound(ro, ra, 0.0, L, d, dtype), f"sequence {n} head {h} scale {scale}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("P,d,rope", [(16, 64, 32), (128, 128, 96), (64, 64, 64)])
+def test_append_scaled_rotation_and_large_eps(P, d, rope, dtype):
+    """rope_scale and eps reach the cached keys as they reach the queries."""
+    announce(f"append rope_scale eps P={P} d={d} rope={rope} {dtype}")
+    Hk, held, new = 2, 5, P + 9
+    c = cache_case(1, Hk, d, P, 3, seed=P)
+    ok, ov = cache_oracles(c)
+    g = ta.to_dev(c)
+    f, w = inv_freq(rope), 1 + 0.1 * torch.randn(d, generator=gen(2))
+    x = torch.randn(2, new, Hk, d, generator=gen(6)).to(dtype)
+    gdn.gdn_kv_append(x[0].cuda(), x[1].cuda(), g["k"], g["v"], g["ks"], g["vs"], g["table"], torch.tensor([held]).cuda(),
+                      inv_freq=f.cuda(), k_weight=w.cuda(), rope_scale=1.25, eps=3.0)
+    torch.cuda.synchronize()
+    ok.append(0, held, oa.norm_rope(x[0], w, held + np.arange(new), f.numpy(), False, 1.25, 3.0))
+    ov.append(0, held, x[1])
+    ta.check_cache(g, ok, ov, "scaled", k_bound=0.01)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("P,d", [(128, 128), (128, 64), (64, 128), (16, 64)])
+def test_append_infinities_in_one_waves_rows(P, d, dtype):
+    """Infinities and NaN among some rows of a page that several waves write, behind older tokens that are
+    rounded again: they move no scale, saturate, and stay NaN."""
+    announce(f"append infinities P={P} d={d} {dtype}")
+    Hk, held = 2, P // 4 + 3
+    c = cache_case(2, Hk, d, P, 2, seed=P + d)
+    ok, ov = cache_oracles(c)
+    g = ta.to_dev(c)
+    new = P - held
+    x = 30 * torch.randn(2, 2, new, Hk, d, generator=gen(8))     # larger than the page's older values: its scale grows
+    x[:, 0, new // 2, :, 3], x[:, 0, new // 2, :, 9], x[:, 0, new // 2, :, 11] = math.inf, -math.inf, math.nan
+    x[:, 1, -1, 0] = math.inf
+    x = x.to(dtype)
+    gdn.gdn_kv_append(x[0].flatten(0, 1).cuda(), x[1].flatten(0, 1).cuda(), g["k"], g["v"], g["ks"], g["vs"], g["table"],
+                      torch.full((2,), held).cuda())
+    torch.cuda.synchronize()
+    for n in range(2):
+        ok.append(n, held, x[0, n])
+        ov.append(n, held, x[1, n])
+    for name, want in (("k", ok), ("v", ov)):
+        assert np.array_equal(f64(g[name + "s"]), want.scale), name
+        got, ref = oa.E4M3[u8(g[name])], oa.E4M3[want.codes]
+        assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.array_equal(got[~np.isnan(ref)], ref[~np.isnan(ref)]), name
+    assert bool((f64(g["vs"])[c["table"][:, 0].numpy()] > f64(c["vs"])[c["table"][:, 0].numpy()]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("width", [10, 160])
+def test_decode_query_that_is_not_finite(width, dtype):
+    """A NaN or infinite query head spoils its own output only, in a group whose heads share every product,
+    over a cache that one workgroup takes whole and over a joined one."""
+    announce(f"decode NaN query width={width} {dtype}")
+    P, d = 16, 128
+    lens = [1, 100, width * P]
+    c = cache_case(len(lens), 2, d, P, width, seed=3)
+    g = ta.to_dev(c)
+    q = torch.randn(len(lens), 10, d, generator=gen(5)).to(dtype)
+    run = lambda x: gdn.gdn_attn_decode(x.cuda(), g["k"], g["v"], g["ks"], g["vs"], g["table"], torch.tensor(lens).cuda())  # noqa: E731
+    want = run(q)
+    ta.check_decode(want, q, c, lens, 0, None, dtype, P, d)
+    for n, h, bad in ((0, 0, math.nan), (1, 7, math.inf), (2, 4, math.nan), (2, 9, -math.inf)):
+        w = q.clone()
+        w[n, h, 17] = bad
+        o = run(w)
+        o[n, h] = want[n, h]
+        assert torch.equal(o, want), (n, h, bad)
+
+
+@pytest.mark.parametrize("T,Hq,Hk,d,window", [(2500, 2, 1, 128, 0), (2500, 2, 2, 64, 0), (2500, 2, 1, 128, 700), (2500, 12, 2, 64, 0)])
+def test_prefill_long_fp32(T, Hq, Hk, d, window):
+    """fp32 prompts of many key tiles."""
+    announce(f"prefill fp32 T={T} Hq={Hq} Hk={Hk} d={d} window={window}")
+    host, dv = ta.prefill_case(T, Hq, Hk, d, F32, T + d)
+    o = gdn.gdn_attn_prefill(*dv, window=window)
+    torch.cuda.synchronize()
+    ta.check_prefill(o, host, [0, T], window, None, F32, d)
