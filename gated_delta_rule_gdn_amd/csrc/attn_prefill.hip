@@ -10,7 +10,10 @@
 // so that a lane holds scores of one query only: the maximum and the sum are
 // reduced in registers and across 2 (or 4) lanes, and the weights are, as they
 // lie in the score accumulators, the k-values this lane supplies to the second
-// product.  No weight crosses lanes or LDS.
+// product.  No weight crosses lanes or LDS.  The bf16 kernel rounds the weights to
+// bf16 for it, half a step of 2^-8 of each like the output's own rounding (error
+// against 64 bits 2.1e-3 for 8 prompts of 4096 tokens, 1.6e-3 with fp32 weights):
+// in two terms they would take half as many products again.
 //
 // 4 d flops to a key that a query sees, against a few bytes: bound by the matrix
 // cores, and with them by power (the clock falls to about 1.8 GHz).  bf16, 16
