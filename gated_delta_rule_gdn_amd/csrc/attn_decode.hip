@@ -6,7 +6,8 @@
 // t over the tokens that the sequence's pages hold (the last `window` of
 // them).  Every code is read once; a token's 2 d bytes take 4 d flops for
 // each of the group's query heads, so the kernel is bound by HBM (256 caches,
-// 730 MB, in 149 us with the join, 4.9 TB/s; one of 128K tokens, 134 MB, in 26 us).
+// 730 MB, in 148 to 161 us with the join, by the card: 4.5 to 4.9 TB/s; one of 128K
+// tokens, 134 MB, in 26 us, 35.5 with the join and its launch).
 //
 // The work is cut into rounds of 128 tokens of one segment: a sequence, a key
 // head and up to 16 query heads of its group.  The rounds of all segments, in
@@ -18,9 +19,10 @@
 // is all of it, else as a partial result, and a second kernel joins those.
 // (Where no cache can be longer than kDecodeDirect tokens each workgroup has one
 // whole segment, and nothing is joined: a round costs a workgroup 1.2 us (fp32
-// 1.6), the second kernel about 5.  32 heads over 4, bf16 / fp32: 64 sequences
-// of 768 tokens 11.3 / 13.9 us so, joined 15.8 / 18.1; 2 sequences of 768 tokens
-// 11.2 / 13.9, joined 12.4 / 13.0; of 1024 tokens 13.7 / 17.0, joined 12.4 / 13.0.)
+// 1.6), the second kernel about 5.  32 heads over 4, bf16 / fp32: 64 sequences of
+// 768 tokens 15.4 / 18.0 us so, joined 18.9 / 20.6; 2 sequences of 768 tokens 11.6 /
+// 14.7, joined 10.8 / 11.8; of 1024 tokens, 64 sequences 18.9 / 22.3, joined 21.4 /
+// 23.3, 2 sequences 15.1 / 18.7, joined 11.0 / 11.9.)
 //
 // The 4 waves of a workgroup take 32 tokens of a round each, with a running
 // maximum and sum of their own, and join through LDS when the segment ends.

@@ -17,10 +17,11 @@
 //
 // 4 d flops to a key that a query sees, against a few bytes: bound by the matrix
 // cores, and with them by power (the clock falls to about 1.8 GHz).  bf16, 16
-// heads of 128: one prompt of 32768 tokens over 2 key heads 3.72 ms, 1182 TFLOP/s
-// (a plain product of 8192 x 8192 x 8192 reaches 1212); 8 prompts of 4096 over 16
-// key heads 519 us, 1059 TFLOP/s; 16 prompts, 32768 tokens in all, a window of
-// 2048, 352 us, 980 TFLOP/s.  Short prompts wait for memory at both ends of a tile (about 6 us
+// heads of 128: one prompt of 32768 tokens over 2 key heads 3.66 to 3.89 ms on
+// different cards, 1130 to 1200 TFLOP/s (a plain product of 8192 x 8192 x 8192
+// reaches 1212); 8 prompts of 4096 over 16 key heads 527 to 549 us, 1000 to 1043
+// TFLOP/s; 16 prompts, 32768 tokens in all, a window of 2048, 337 to 361 us, 954 to
+// 1022 TFLOP/s.  Short prompts wait for memory at both ends of a tile (about 6 us
 // of each workgroup).
 #include "attn_device.hpp"
 
@@ -468,7 +469,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 // WIN: with the code of a window's mask (calls without a window are 1 to 2 % faster
-// without it: 8 prompts of 4096 tokens 553 / 546 us, 4 short ones 9.0 / 8.8).
+// without it: 8 prompts of 4096 tokens 546 / 540 us, 4 short ones 11.0 / 10.7).
 // SPLIT 2: 64 queries to a workgroup; waves 0 and 1 take the even key tiles, 2
 // and 3 the odd ones, with a maximum and sum of their own, and join at the end.
 //
@@ -834,20 +835,20 @@ int64_t mean_keys(const PrefillArgs& a) {
   return a.window > 0 && a.window < len ? a.window : len;
 }
 // bf16, us with 128 queries to a workgroup / 64 and the keys shared, d 128: 2048
-// tokens, 8 heads 36.7 / 23.2; 512 tokens, 16 heads 13.2 / 10.8; 2 prompts of 704
-// tokens in all, 12 heads 12.7 / 11.6; 4 of 512, 16 heads 8.7 / 8.9; with 256
-// workgroups of the first kind: 4096 tokens, 8 heads 69 / 48.7, 1024 tokens, 32
-// heads 22.5 / 22.2; with 512: 2048 tokens, 32 heads 47 / 58.  At d 64 two
-// workgroups of the second kind fit a CU: 288, 2048 tokens, 18 heads 30.0 / 21.5;
-// 384, 24 heads 29.5 / 25.7; 448, 28 heads 29.8 / 29.1; 315, 9 prompts of 640, 7
-// heads 12.6 / 13.7.
+// tokens, 8 heads 32.9 / 22.2; 512 tokens, 16 heads 13.0 / 10.9; 2 prompts of 704
+// tokens in all, 12 heads 13.6 / 12.2; 4 of 128, 16 heads 8.1 / 7.7; with 256
+// workgroups of the first kind: 4096 tokens, 8 heads 62 / 50, 1024 tokens, 32
+// heads 21.6 / 22.8; with 512: 2048 tokens, 32 heads 46 / 67.  At d 64 two
+// workgroups of the second kind fit a CU: 288, 2048 tokens, 18 heads 28.1 / 20.0;
+// 384, 24 heads 28.8 / 25.9; 448, 28 heads 29.8 / 29.9; 315, 9 prompts of 640, 7
+// heads 12.8 / 14.2.
 bool split_bf16(int64_t blocks, int64_t keys, int d) {
   return blocks <= 256 ? keys >= 256 : d == 64 && blocks <= 384 && keys >= 768;
 }
-// fp32, us with 4 / 8 waves to 32 queries, d 128: 2352 tokens, 2 heads 138 / 118;
-// 3 prompts of 257 tokens in all, 4 heads of 64 7.9 / 7.6; 24 prompts of 304, 8
-// heads 8.5 / 9.3; with 512 workgroups: 2048 tokens, 8 heads 146 / 114; with 2048:
-// 4096 tokens, 16 heads 673 / 838.
+// fp32, us with 4 / 8 waves to 32 queries, d 128: 2352 tokens, 2 heads 138 / 121;
+// 3 prompts of 257 tokens in all, 4 heads of 64 8.9 / 8.5; 24 prompts of 304 in all,
+// 8 heads 8.4 / 9.4; with 512 workgroups: 2048 tokens, 8 heads 147 / 123; with 2048:
+// 4096 tokens, 16 heads 677 / 853.
 bool split_f32(int64_t blocks, int64_t keys) { return blocks <= 512 && keys >= 64; }
 
 // rows_again reads PrefillArgs where a kernel's arguments begin.

@@ -19,9 +19,10 @@
 //                 .. dim/4 + 4 l + 3; append: [16 l, +16), as half pairs.
 // The others share the rest: norm_rope [8 l', +8) and the same behind half of
 // it, append [16 l, +16).  (norm_rope, 32768 fp32 rows of 18 heads of 128, with
-// 16 neighbouring channels to a lane / spread: interleaved 141 / 109 us, not
-// turned 143 / 107; bf16 55 / 48, 52 / 46.  append, whose codes of 16 channels are
-// one piece: 32768 bf16 tokens of 4 heads 22.2 / 22.8 us.)
+// 16 neighbouring channels to a lane / spread: interleaved 132 / 109 us, not
+// turned 153 / 108; bf16 57.8 / 54.7, 57.3 / 54.6.  append, whose codes of 16
+// channels are one piece: no difference, 32768 bf16 tokens of 4 heads 25.9 / 25.6.
+// These times and those below are on inputs that the caches do not hold.)
 #include "attn_device.hpp"
 
 namespace gdn {
@@ -55,12 +56,13 @@ __device__ __forceinline__ LaneMap lane_map(int l, const RopeArgs& r) {
 // whole turns leave exactly, and the rest is added: an error of 2^-25 turns up
 // to 2^22 turns, which frequencies of at most 1 stay below.  Other angles go
 // the same way in two 64-bit terms (positions are exact there up to 2^53), whose
-// conversions and products are slow (an append of 32768 tokens, 4 heads: 25.6 us
-// with one 64-bit term for all, 24.0 us so).  Results that
+// conversions and products are slow (an append of 32768 tokens, 4 heads: 32.9 us
+// with them for all, 25.9 us so).  Results that
 // are rounded to bf16 or e4m3 take the hardware's sine, whose error (about
 // 2^-20) is far below their half step of 2^-8 or 2^-4; fp32 results take the
 // exact routine.  (UNROLL is the far angles' loop: rolled it leaves append
-// registers; unrolled norm_rope is 18 % faster for near ones.)
+// registers; 32768 rows of far positions in norm_rope, rolled / unrolled: bf16 70 /
+// 55 us, fp32 121 / 111.)
 struct Freqs {
   float hi[8], lo[8];                       // inv_freq / 2 pi
   float most;                               // largest of |hi|
@@ -154,8 +156,8 @@ __device__ __forceinline__ void load_weights(const float* weight, const LaneMap&
 // operand, so the angles are computed once for them and every load is issued
 // before the first value is used.  Blocks run over head groups first, so that
 // a token's whole row is read by workgroups that run together.  HBM-bound:
-// 32768 tokens of 18 heads of 128, bf16, 302 MB: 48 us (4 heads to a thread 55,
-// one 50); fp32 107 us (115, 116).
+// 32768 tokens of 18 heads of 128, bf16, 302 MB: 54.6 us, 5.5 TB/s (4 heads to a
+// thread 61.2, one 55.5); fp32 109 us (117, 118).
 // ---------------------------------------------------------------------------
 constexpr int kHeads = 2;
 
@@ -211,14 +213,14 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkNormRopeArgs p
 // magnitude, and writes their codes; where the scale of a page that holds older
 // tokens grows it also rounds those again.  So a row is read once though its scale
 // is known only after the page's last row.  HBM-bound for many tokens (32768
-// tokens of 4 heads of 128, bf16, pages of 64: 101 MB in 22 us, 4.6 TB/s), by
-// latency and the waves that fit where pages are partly filled (213 sequences of
-// 40 tokens, 8 heads of 64, pages of 128: 20 us for 26 MB), and by the launch for
-// a token to a sequence (256: 4.3 us).
+// tokens of 4 heads of 128, bf16, pages of 64: 101 MB in 24 us, 4.2 TB/s; fp32
+// 168 MB in 41 us), by latency and the waves that fit where pages are partly filled
+// (213 sequences of 40 tokens, 8 heads of 64, pages of 128: 24 us for 26 MB), and
+// by the launch for a token to a sequence (256: 4.3 us).
 //
 // A wave takes two passes of 1024 / D rows: as many registers as 5 waves to a
-// SIMD leave.  (One pass at D 64: 27.8 us for the 213 sequences; four at D 128
-// spill, 32768 tokens in pages of 128: 50 us instead of 24.)
+// SIMD leave.  (One pass at D 64: 32.3 us for the 213 sequences; four at D 128
+// spill, 32768 tokens in pages of 128: 56.6 us instead of 29.8.)
 //
 // Which pages get tokens is known on the device only.  L new tokens behind a
 // length s touch at most floor(L / P) + 2 pages, so packed sequences own the
