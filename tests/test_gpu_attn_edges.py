@@ -235,3 +235,35 @@ def test_prefill_long_fp32(T, Hq, Hk, d, window):
     o = gdn.gdn_attn_prefill(*dv, window=window)
     torch.cuda.synchronize()
     ta.check_prefill(o, host, [0, T], window, None, F32, d)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_of_a_model_gone_nan(dtype):
+    """Values that are all NaN give NaN, in a time of the same order: every wave computes its rows again
+    for them, but no row walks on through its keys once all of its columns are NaN."""
+    announce(f"prefill all NaN {dtype}")
+    T = 8192
+    q, k, v = torch.randn(T, 8, 64, generator=gen(1)), torch.randn(T, 2, 64, generator=gen(2)), torch.randn(T, 2, 64, generator=gen(3))
+    q, k, v = [t.to(dtype).cuda() for t in (q, k, v)]
+    nan = torch.full_like(v, math.nan)
+    o = torch.empty_like(q)
+
+    def best(values):
+        times = []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            gdn.gdn_attn_prefill(q, k, values, o=o)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    clean = best(v)
+    slow = best(nan)
+    assert bool(o.isnan().all())
+    assert slow < 20 * clean, (slow, clean)
+    late = v.clone()
+    late[T - 100] = math.nan                 # the rows before it see none
+    gdn.gdn_attn_prefill(q, k, late, o=o)
+    assert bool(o[:T - 100].isfinite().all()) and bool(o[T - 100:].isnan().all())
