@@ -56,7 +56,7 @@ def test_parity_under_lds_checks(check_library, case):
 
 @pytest.mark.parametrize("window", [0, 16, 300])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("lens", [[1, 129, 0, 190], [500, 33, 1217], [2048 + 65], [1, 2, 3, 31] * 40])
+@pytest.mark.parametrize("lens", [[1, 129, 0, 190], [500, 33, 1217], [2048 + 65], [1, 2, 3, 31] * 40, [1133] * 8])
 def test_waves_without_queries_compute_nothing(check_library, lens, d, window):
     """The last tile of a prompt may have waves whose queries all lie behind its end: nothing is loaded for
     them, and they form no scores of what the LDS held before (a condition of the debug library's kernels)."""

@@ -267,3 +267,50 @@ def test_prefill_of_a_model_gone_nan(dtype):
     late[T - 100] = math.nan                 # the rows before it see none
     gdn.gdn_attn_prefill(q, k, late, o=o)
     assert bool(o[:T - 100].isfinite().all()) and bool(o[T - 100:].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [0, 600])
+def test_prefill_large_scores_among_many_tiles(window, dtype):
+    """As above where the query tiles fill the chip, among ordinary rows: huge scores in some heads only."""
+    announce(f"prefill large scores, many tiles, window={window} {dtype}")
+    T, Hq, d = 1133, 32, 128
+    host, _ = ta.prefill_case(T, Hq, 8, d, dtype, 3)
+    q, k, v = [t.clone().contiguous() for t in host]
+    c = (1 + torch.randint(0, 8, (T,), generator=gen(4)) / 8) * (torch.randint(0, 2, (T,), generator=gen(5)) * 2 - 1)
+    q[:, 8:12], k[:, 2] = 0, 0
+    q[:, 8:12, 3] = 2.0 ** 20
+    k[:, 2, 3] = c * 2.0 ** 20
+    o = gdn.gdn_attn_prefill(q.cuda(), k.cuda(), v.cuda(), window=window, scale=0.125)
+    ro, ra = ties(f64(c), f64(v[:, 2:3]), window)
+    ro, ra = np.repeat(ro, 4, 1), np.repeat(ra, 4, 1)
+    within(o[:, 8:12], ro, attn_bound(ro, ra, 0.0, T, d, dtype), "huge scores")
+    rest = [h for h in range(Hq) if not 8 <= h < 12]
+    kr = [h for h in range(8) if h != 2]
+    ro, ra, reach = oa.attention(q[:, rest], k[:, kr], v[:, kr], window, 0.125)
+    within(o[:, rest], ro, attn_bound(ro, ra, reach, T, d, dtype), "ordinary heads")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N,T,Hq,Hk,window", [(300, 3, 4, 2, 0), (257, 1, 3, 3, 0), (64, 33, 8, 1, 5), (40, 129, 2, 2, 64)])
+def test_prefill_many_equal_prompts(N, T, Hq, Hk, window, dtype):
+    announce(f"prefill many equal N={N} T={T} Hq={Hq} Hk={Hk} window={window} {dtype}")
+    host, dv = ta.prefill_case(N * T, Hq, Hk, 64, dtype, N + T)
+    o = gdn.gdn_attn_prefill(*dv, N=N, window=window)
+    torch.cuda.synchronize()
+    ta.check_prefill(o, host, list(range(0, N * T + 1, T)), window, None, dtype, 64)
+
+
+def test_default_stream_given_as_a_handle():
+    """Stream 0, as a number: the default stream, for calls that allocate too."""
+    announce("stream 0")
+    c = cache_case(2, 2, 64, 16, 90, seed=6)
+    g = ta.to_dev(c)
+    q = torch.randn(2, 4, 64, generator=gen(1)).to(BF).cuda()
+    lens = torch.tensor([1400, 3]).cuda()
+    args = (q, g["k"], g["v"], g["ks"], g["vs"], g["table"], lens)
+    want = gdn.gdn_attn_decode(*args)
+    assert torch.equal(gdn.gdn_attn_decode(*args, stream=0), want)
+    assert torch.equal(gdn.gdn_attn_decode(*args, stream=torch.cuda.current_stream()), want)
+    x = torch.randn(5, 2, 64, generator=gen(2)).cuda()
+    assert torch.equal(gdn.gdn_qk_norm_rope(x, stream=0)[0], x)
