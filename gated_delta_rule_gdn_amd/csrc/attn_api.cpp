@@ -9,15 +9,23 @@
 #include <cstdint>
 #include <cstdio>
 
-#include "api_common.hpp"
+#include "attn_checks.hpp"
 #include "attn_kernels.hpp"
 
 namespace {
 
 using gdn::Span;
+using gdn::aligned;
 using gdn::aligned16;
+using gdn::apart;
+using gdn::check_head;
+using gdn::check_rope;
+using gdn::check_rows;
 using gdn::dtype_bytes;
+using gdn::kMaxElems;
+using gdn::kMaxThreads;
 using gdn::overlaps;
+using gdn::rows_span;
 using gdn::span;
 using gdn::to_dtype;
 
@@ -32,37 +40,6 @@ gdn_status launched(hipError_t e) {
     return GDN_ERR_CHECK;
   }
 #endif
-  return GDN_OK;
-}
-
-constexpr double kMaxElems = 2.0e15;                 // of any tensor
-constexpr double kMaxThreads = 4294967295.0;         // of a grid
-
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-gdn_status check_head(int32_t d, int32_t io) {
-  if (io != GDN_F32 && io != GDN_BF16) return GDN_ERR_INVALID_ARG;
-  if (d < 1) return GDN_ERR_INVALID_ARG;
-  return d == 64 || d == 128 ? GDN_OK : GDN_ERR_UNSUPPORTED;
-}
-
-// A strided operand of `rows` rows of H heads.
-gdn_status check_rows(int64_t rows, int64_t ld, int32_t H, int32_t d) {
-  const int64_t cols = (int64_t)H * d;
-  if (cols > (int64_t(1) << 22)) return GDN_ERR_UNSUPPORTED;
-  if (ld < cols || ld % 8 != 0 || ld > (int64_t(1) << 24)) return GDN_ERR_INVALID_ARG;
-  if ((double)rows * (double)ld > kMaxElems) return GDN_ERR_INVALID_ARG;
-  return GDN_OK;
-}
-
-Span rows_span(const void* p, int64_t rows, int64_t ld, int32_t H, int32_t d, int32_t io) {
-  return rows > 0 ? span(p, (rows - 1) * ld + (int64_t)H * d, dtype_bytes(io)) : Span{0, 0};
-}
-
-gdn_status check_rope(int32_t dim, int32_t mode, float factor, float eps, int32_t d) {
-  if (dim < 0 || dim > d || dim % 16 != 0) return GDN_ERR_INVALID_ARG;
-  if (mode != GDN_ROPE_HALF && mode != GDN_ROPE_INTERLEAVED) return GDN_ERR_INVALID_ARG;
-  if (!std::isfinite(factor) || !std::isfinite(eps) || eps < 0.f) return GDN_ERR_INVALID_ARG;
   return GDN_OK;
 }
 
@@ -91,18 +68,6 @@ gdn_status check_cache_ptrs(const CachePtrs& c) {
       !aligned(c.table, 4) || !aligned(c.lens, 8))
     return GDN_ERR_INVALID_ARG;
   return GDN_OK;
-}
-
-// No output overlaps an input or another output.
-template <size_t I, size_t O>
-bool apart(const Span (&ins)[I], const Span (&outs)[O]) {
-  for (size_t o = 0; o < O; ++o) {
-    for (const Span& in : ins)
-      if (overlaps(outs[o], in)) return false;
-    for (size_t i = 0; i < o; ++i)
-      if (overlaps(outs[o], outs[i])) return false;
-  }
-  return true;
 }
 
 gdn_status check_decode_desc(const gdn_attn_decode_desc* d) {

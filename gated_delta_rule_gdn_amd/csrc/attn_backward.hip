@@ -1,0 +1,707 @@
+// attn_backward.hip -- gradients of the causal softmax attention of
+// attn_prefill.hip on gfx950.  With c = scale, p_ts = exp(c q_t . k_s - m_t) / l_t
+// from the statistics that the forward left,
+//
+//   D_t = sum_s p_ts (d_o_t . v_s) = d_o_t . o_t
+//   ds_ts = p_ts (d_o_t . v_s - D_t)
+//   dq_t = c sum_s ds_ts k_s,   dk_s = c sum_t ds_ts q_t,   dv_s = sum_t p_ts d_o_t
+//
+// the last two over the query heads of the key head too.
+//
+// Two kernels form the probabilities again, each with the sums that it is after in
+// registers: one walks the keys of a query tile (dq, and D and the statistics packed
+// for the other), one the queries of a key tile (dk, dv).  That is 7 products of
+// d x keys x queries where one kernel with both sums would do 5; but its dq (or dk and
+// dv) would go through memory for every pair of tiles, as atomics, whose order changes
+// the result, or as partial sums of four times the products' operands.  Here every sum
+// has a fixed order.
+//
+// In both, what is summed over lies on the rows of the first products (S^T = K Q^T and
+// dP^T = V dO^T for dq; S = Q K^T and dP = dO V^T for dk and dv), so p and ds are, as
+// they lie in the accumulators, the k-values of the second products.
+#include "attn_tiles.hpp"
+
+#include "hybrid_kernels.hpp"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ TileArgs tile_args(const AttnBwdArgs& p, int G) {
+  return TileArgs{p.cu_seqlens, p.N, p.Tseq, p.total_T, p.window, p.Hk, G};
+}
+
+// The workspace: 16 bytes for each query and head, then the partial dk and dv.
+__device__ __forceinline__ uint4* aux_of(const AttnBwdArgs& p, int hq) {
+  return reinterpret_cast<uint4*>(p.ws) + hq * p.total_T;
+}
+__device__ __forceinline__ float* parts_of(const AttnBwdArgs& p) {
+  return p.ws + 4 * p.total_T * p.Hq;
+}
+
+// A key tile's number from its rank among the tiles of its sequence by cost: the first
+// keys are seen by the most queries.
+template <int BK>
+__device__ __forceinline__ int key_tile_start(const Tile& t) {
+  const int tiles = (int)((t.L + BK - 1) / BK);
+  return (tiles - 1 - (int)(t.q0 / BK)) * BK;
+}
+
+// What one workgroup of a key tile walks: steps [at, stop) of the query heads of its
+// key head, each going through the `each` query tiles that see the keys.
+struct Walk {
+  int each, at, stop;
+};
+template <int BK, int BQ>
+__device__ __forceinline__ Walk walk_of(int k0, int L, int window, int G, int part, int parts) {
+  int64_t end = window ? (int64_t)k0 + BK - 1 + window : L;
+  if (end > L) end = L;
+  Walk w;
+  w.each = (int)(end - k0 + BQ - 1) / BQ;
+  const int64_t all = (int64_t)w.each * G;
+  w.at = (int)(all * part / parts);
+  w.stop = (int)(all * (part + 1) / parts);
+  return w;
+}
+
+// ---------------------------------------------------------------------------
+// fp32: v_mfma_f32_16x16x4_f32, 32 queries (dq) or 32 keys (dk, dv) to a workgroup,
+// tiles of 32 rows of the other in LDS.  Waves 0 and 1 take 16 rows of their own over
+// the first 16 rows of each tile, waves 2 and 3 the same over the others, and their
+// sums are added at the end.
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attn_dq_f32_kernel(AttnBwdArgs p, uint32_t blocks) {
+  constexpr int BM = 32, BN = 32, LD = D + 4, KB = D / 32, MT = D / 16;
+  constexpr int NL = BN * D / 4 / kThreads;
+  __shared__ __align__(16) float s_kv[2 * BN * LD];
+  lds_nan_fill(s_kv, sizeof s_kv);
+  float *s_k = s_kv, *s_v = s_kv + BN * LD;
+  const int G = p.Hq / p.Hk;
+  const Tile tl = find_tile<BM>(tile_args(p, G), blocks);
+  if (!tl.valid) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wq = wave & 1, wk = wave >> 1;
+  const int g = lane >> 4, j = lane & 15;
+  const int hk = tl.hq / G, L = (int)tl.L;
+  const int q0 = (int)tl.q0 + 16 * wq, tq = q0 + j;
+  const float* kb_ = static_cast<const float*>(p.k) + tl.a * p.ld_k + hk * D;
+  const float* vb_ = static_cast<const float*>(p.v) + tl.a * p.ld_v + hk * D;
+  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
+  int lo = window ? (int)tl.q0 - window + 1 : 0;
+  lo = lo < 0 ? 0 : lo / BN * BN;
+  const int stop = (int)tl.q0 + BM < L ? (int)tl.q0 + BM : L;
+  float4 kr[NL], vr[NL];
+  auto load_tile = [&](int k0) {            // rows past the sequence are zero
+#pragma unroll
+    for (int e = 0; e < NL; ++e) {
+      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+      kr[e] = vr[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + row < L) {
+        kr[e] = *reinterpret_cast<const float4*>(kb_ + (int64_t)(k0 + row) * p.ld_k + c);
+        vr[e] = *reinterpret_cast<const float4*>(vb_ + (int64_t)(k0 + row) * p.ld_v + c);
+      }
+    }
+  };
+  load_tile(lo);
+  Frag8<float> q[KB], go[KB];
+  float m, rl, dl = 0.f;
+  {
+    const int64_t row = tl.a + (tq < L ? tq : L - 1);
+    const float* qp = static_cast<const float*>(p.q) + row * p.ld_q + tl.hq * D + 8 * g;
+    const float* gp = static_cast<const float*>(p.d_o) + (row * p.Hq + tl.hq) * D + 8 * g;
+    const float* op = static_cast<const float*>(p.o) + (row * p.Hq + tl.hq) * D + 8 * g;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      float o[8];
+      load_f32<8, float>(qp + 32 * kb, q[kb].v);
+      load_f32<8, float>(gp + 32 * kb, go[kb].v);
+      load_f32<8, float>(op + 32 * kb, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dl = __builtin_fmaf(go[kb].v[i], o[i], dl);
+    }
+    dl += __shfl_xor(dl, 16);
+    dl += __shfl_xor(dl, 32);
+    const float2 st = reinterpret_cast<const float2*>(p.stats)[row * p.Hq + tl.hq];
+    m = st.x;
+    rl = 1.f / st.y;
+    if (wk == 0 && g == 0 && tq < L)
+      reinterpret_cast<float4*>(aux_of(p, tl.hq))[row] = make_float4(m, rl, dl, 0.f);
+  }
+  const float c_scale = p.scale * kLog2e;
+  f32x4 dq[MT];
+#pragma unroll
+  for (int c = 0; c < MT; ++c) dq[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  for (int k0 = lo; k0 < stop; k0 += BN) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < NL; ++e) {
+      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+      lds_check(s_v + row * LD + c, 16);
+      *reinterpret_cast<float4*>(s_k + row * LD + c) = kr[e];
+      *reinterpret_cast<float4*>(s_v + row * LD + c) = vr[e];
+    }
+    __syncthreads();
+    if (k0 + BN < stop) load_tile(k0 + BN);
+    const int kw = k0 + 16 * wk;
+    if (kw > q0 + 15 || (window && kw + 15 <= q0 - window)) continue;   // nothing seen
+    f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      Frag8<float> a;
+      load_f32<8, float>(s_k + (16 * wk + j) * LD + 32 * kb + 8 * g, a.v);
+      mma32(s, a, q[kb]);
+      load_f32<8, float>(s_v + (16 * wk + j) * LD + 32 * kb + 8 * g, a.v);
+      mma32(dp, a, go[kb]);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int u = kw + 4 * g + r;
+      const bool seen = u <= tq && (!window || u > tq - window);
+      const float pr = seen ? weight_of(s[r] * c_scale, m) * rl : 0.f;
+      const float ds = pr * (dp[r] - dl);
+      const float* kl = s_k + (16 * wk + 4 * g + r) * LD + j;
+#pragma unroll
+      for (int c = 0; c < MT; ++c)
+        dq[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(kl[16 * c], ds, dq[c], 0, 0, 0);
+    }
+  }
+  __syncthreads();
+  if (wk == 1) {
+#pragma unroll
+    for (int c = 0; c < MT; ++c) {
+      float* dst = s_kv + (16 * wq + j) * LD + 16 * c + 4 * g;
+      lds_check(dst, 16);
+      *reinterpret_cast<float4*>(dst) = make_float4(dq[c][0], dq[c][1], dq[c][2], dq[c][3]);
+    }
+  }
+  __syncthreads();
+  if (wk == 1 || tq >= L) return;
+  float* to = static_cast<float*>(p.dq) + (tl.a + tq) * p.ld_dq + tl.hq * D + 4 * g;
+#pragma unroll
+  for (int c = 0; c < MT; ++c) {
+    const float4 u = *reinterpret_cast<const float4*>(s_kv + (16 * wq + j) * LD + 16 * c + 4 * g);
+    store4<float>(to + 16 * c, (dq[c][0] + u.x) * p.scale, (dq[c][1] + u.y) * p.scale,
+                  (dq[c][2] + u.z) * p.scale, (dq[c][3] + u.w) * p.scale);
+  }
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attn_dkv_f32_kernel(AttnBwdArgs p, uint32_t blocks, int parts) {
+  constexpr int BK = 32, BQ = 32, LD = D + 4, KB = D / 32, MT = D / 16;
+  constexpr int NL = BQ * D / 4 / kThreads;
+  __shared__ __align__(16) float s_qg[2 * BQ * LD];
+  __shared__ __align__(16) float4 s_aux[BQ];
+  lds_nan_fill(s_qg, sizeof s_qg);
+  float *s_q = s_qg, *s_g = s_qg + BQ * LD;
+  const int G = p.Hq / p.Hk;
+  const Tile tl = find_tile<BK>(tile_args(p, parts), blocks);
+  if (!tl.valid) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = wave & 1, wq = wave >> 1;
+  const int g = lane >> 4, j = lane & 15;
+  const int hk = tl.hq / parts, part = tl.hq - hk * parts, L = (int)tl.L;
+  const int k0 = key_tile_start<BK>(tl);
+  const int u0 = k0 + 16 * wk, tk = u0 + j;           // this lane's key
+  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
+  const Walk w = walk_of<BK, BQ>(k0, L, window, G, part, parts);
+  const float c_scale = p.scale * kLog2e;
+
+  Frag8<float> k[KB], v[KB];
+  {
+    const int64_t row = tl.a + (tk < L ? tk : L - 1);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      load_f32<8, float>(static_cast<const float*>(p.k) + row * p.ld_k + hk * D + 32 * kb + 8 * g, k[kb].v);
+      load_f32<8, float>(static_cast<const float*>(p.v) + row * p.ld_v + hk * D + 32 * kb + 8 * g, v[kb].v);
+    }
+  }
+  f32x4 dk[MT], dv[MT];
+#pragma unroll
+  for (int c = 0; c < MT; ++c) dk[c] = dv[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float4 qr[NL], gr[NL], ar;
+  auto load_tile = [&](int step) {          // rows past the sequence are zero
+    const int head = step / w.each, t0 = k0 + (step - head * w.each) * BQ;
+    const int hq = hk * G + head;
+#pragma unroll
+    for (int e = 0; e < NL; ++e) {
+      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+      qr[e] = gr[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t0 + row < L) {
+        qr[e] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + (tl.a + t0 + row) * p.ld_q + hq * D + c);
+        gr[e] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.d_o) + ((tl.a + t0 + row) * p.Hq + hq) * (int64_t)D + c);
+      }
+    }
+    ar = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < BQ && t0 + tid < L)
+      ar = reinterpret_cast<const float4*>(aux_of(p, hq))[tl.a + t0 + tid];
+  };
+  if (w.at < w.stop) load_tile(w.at);
+  for (int step = w.at; step < w.stop; ++step) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < NL; ++e) {
+      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+      lds_check(s_g + row * LD + c, 16);
+      *reinterpret_cast<float4*>(s_q + row * LD + c) = qr[e];
+      *reinterpret_cast<float4*>(s_g + row * LD + c) = gr[e];
+    }
+    if (tid < BQ) s_aux[tid] = ar;
+    __syncthreads();
+    if (step + 1 < w.stop) load_tile(step + 1);
+    const int t0 = k0 + step % w.each * BQ + 16 * wq;       // this wave's queries
+    if (t0 + 15 < u0 || t0 >= L || (window && t0 - window >= u0 + 15)) continue;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      Frag8<float> a;
+      load_f32<8, float>(s_q + (16 * wq + j) * LD + 32 * kb + 8 * g, a.v);
+      mma32(s, a, k[kb]);
+      load_f32<8, float>(s_g + (16 * wq + j) * LD + 32 * kb + 8 * g, a.v);
+      mma32(dp, a, v[kb]);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * wq + 4 * g + r, t = t0 + 4 * g + r;
+      const float4 st = s_aux[row];
+      const bool seen = tk <= t && t < L && (!window || tk > t - window);
+      const float pr = seen ? weight_of(s[r] * c_scale, st.x) * st.y : 0.f;
+      const float ds = pr * (dp[r] - st.z);
+      const float *ql = s_q + row * LD + j, *gl = s_g + row * LD + j;
+#pragma unroll
+      for (int c = 0; c < MT; ++c) {
+        dv[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(gl[16 * c], pr, dv[c], 0, 0, 0);
+        dk[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(ql[16 * c], ds, dk[c], 0, 0, 0);
+      }
+    }
+  }
+  __syncthreads();
+  if (wq == 1) {
+#pragma unroll
+    for (int c = 0; c < MT; ++c) {
+      float* dst = s_qg + (16 * wk + j) * LD + 16 * c + 4 * g;
+      lds_check(dst + BQ * LD, 16);
+      *reinterpret_cast<float4*>(dst) = make_float4(dk[c][0], dk[c][1], dk[c][2], dk[c][3]);
+      *reinterpret_cast<float4*>(dst + BQ * LD) = make_float4(dv[c][0], dv[c][1], dv[c][2], dv[c][3]);
+    }
+  }
+  __syncthreads();
+  if (wq == 1 || tk >= L) return;
+  float *tok, *tov;
+  if (parts == 1) {
+    tok = static_cast<float*>(p.dk) + (tl.a + tk) * p.ld_dk + hk * D;
+    tov = static_cast<float*>(p.dv) + (tl.a + tk) * p.ld_dv + hk * D;
+  } else {
+    tok = parts_of(p) + ((part * p.total_T + tl.a + tk) * p.Hk + hk) * (2 * D);
+    tov = tok + D;
+  }
+#pragma unroll
+  for (int c = 0; c < MT; ++c) {
+    const float* src = s_qg + (16 * wk + j) * LD + 16 * c + 4 * g;
+    const float4 a = *reinterpret_cast<const float4*>(src);
+    const float4 b = *reinterpret_cast<const float4*>(src + BQ * LD);
+    store4<float>(tok + 16 * c + 4 * g, (dk[c][0] + a.x) * p.scale, (dk[c][1] + a.y) * p.scale,
+                  (dk[c][2] + a.z) * p.scale, (dk[c][3] + a.w) * p.scale);
+    store4<float>(tov + 16 * c + 4 * g, dv[c][0] + b.x, dv[c][1] + b.y, dv[c][2] + b.z, dv[c][3] + b.w);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// bf16: v_mfma_f32_32x32x16_bf16, 32 queries (dq) or keys (dk, dv) to a wave, 128 to
+// a workgroup, tiles of 64 rows of the other, double-buffered in LDS.  p and ds are
+// rounded to bf16 for the second products, half a step of 2^-8 of each like the
+// outputs' own rounding.
+//
+// Lane 32 h + i holds, of a 32 x 32 product, column i and rows 8 a + 4 h + b
+// (a, b = 0..3), and supplies 8 k-values: rows 4 h + b and 8 + 4 h + b of a block of
+// 16, so the other operand of the second products is read with the same 8 rows, by two
+// transposing LDS reads of 4 rows each.
+//
+// Every tile is read by rows and transposed.  Its 16-byte chunks are permuted so
+// that both kinds of reads fall on different banks: 16 rows at one chunk go to 16
+// places, and 4 neighbouring rows at 4 neighbouring chunks too.
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ int chunk_at(int row, int c) {
+  return D == 128 ? c ^ ((row & 3) << 2 | ((row >> 2) & 3)) : c ^ (((row >> 1) & 1) << 2 | ((row >> 2) & 3));
+}
+
+// A tile of 64 rows of D elements, `rows` of them there (the last one repeats: what
+// it gives is masked), into LDS by a workgroup.
+template <int D>
+__device__ __forceinline__ void load_tile64(const bf16* base, uint32_t ld2, int rows, const bf16* dst, int tid) {
+  constexpr int CH = D / 8, RL = kThreads / CH, NL = 64 / RL;
+  const i32x4 rs = buffer_at(base);
+  const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(dst)) +
+                      1024 * __builtin_amdgcn_readfirstlane(tid >> 6);
+#pragma unroll
+  for (int e = 0; e < NL; ++e) {
+    const int r = e * RL + tid / CH;
+    load_lds16(at + e * 4096, rs, (uint32_t)(r < rows ? r : rows - 1) * ld2 + 16 * chunk_at<D>(r, tid % CH), 0);
+  }
+}
+
+// The rows [r0, r0 + 32) of a tile as the first operand of a product over d, and the
+// rows [r0, r0 + 16) transposed, columns [32 c, +32), as that of one over rows.
+template <int D>
+__device__ __forceinline__ bf16x8 read_rows(const bf16* tile, int r0, int kb, int lane) {
+  const int row = r0 + (lane & 31);
+  const bf16* src = tile + row * D + 8 * chunk_at<D>(row, 2 * kb + (lane >> 5));
+  lds_check(src, 16);
+  return *reinterpret_cast<const bf16x8*>(src);
+}
+template <int D>
+__device__ __forceinline__ bf16x8 read_columns(const bf16* tile, int r0, int c, int lane) {
+  bf16x8 f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int li = lane & 15;
+    const int row = r0 + 8 * half + 4 * (lane >> 5) + (li >> 2);
+    const int col = 32 * c + 16 * ((lane >> 4) & 1) + 4 * (li & 3);
+    const bf16x4 u = read_tr16(tile + row * D + 8 * chunk_at<D>(row, col / 8) + col % 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[4 * half + i] = u[i];
+  }
+  return f;
+}
+
+// x as three bf16 terms (24 bits).
+__device__ __forceinline__ uint2 three_terms(float x) {
+  const bf16 a = (bf16)x;
+  const float r = x - (float)a;
+  const bf16 b = (bf16)r;
+  const bf16x4 t = {a, b, (bf16)(r - (float)b), (bf16)0.f};
+  return __builtin_bit_cast(uint2, t);
+}
+
+template <int D, typename TG>
+__global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p, uint32_t blocks) {
+  constexpr int BM = 128, BN = 64, KB = D / 16, MT = D / 32;
+  __shared__ __align__(16) bf16 s_k[2][BN * D], s_v[2][BN * D];
+  lds_nan_fill(s_k, sizeof s_k);
+  lds_nan_fill(s_v, sizeof s_v);
+  const int G = p.Hq / p.Hk;
+  const Tile tl = find_tile<BM>(tile_args(p, G), blocks);
+  if (!tl.valid) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, i32 = lane & 31;
+  const int hk = tl.hq / G;
+  const int L = __builtin_amdgcn_readfirstlane((int)tl.L);
+  const int qt0 = __builtin_amdgcn_readfirstlane((int)tl.q0);
+  const int q0 = qt0 + 32 * wave, tq = q0 + i32;
+  const bf16* kb_ = static_cast<const bf16*>(p.k) + tl.a * p.ld_k + hk * D;
+  const bf16* vb_ = static_cast<const bf16*>(p.v) + tl.a * p.ld_v + hk * D;
+  const uint32_t lk2 = (uint32_t)p.ld_k * 2, lv2 = (uint32_t)p.ld_v * 2;
+  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
+  int lo = window ? qt0 - window + 1 : 0;
+  lo = lo < 0 ? 0 : lo / BN * BN;
+  const int stop = qt0 + BM < L ? qt0 + BM : L;
+  load_tile64<D>(kb_ + lo * p.ld_k, lk2, L - lo, s_k[0], tid);
+  load_tile64<D>(vb_ + lo * p.ld_v, lv2, L - lo, s_v[0], tid);
+
+  const float c_scale = p.scale * kLog2e;
+  bf16x8 q[KB], go[KB];
+  float lse, dl = 0.f;
+  {
+    const int64_t row = tl.a + (tq < L ? tq : L - 1);
+    const bf16* qp = static_cast<const bf16*>(p.q) + row * p.ld_q + tl.hq * D + 8 * h;
+    const bf16* gp = static_cast<const bf16*>(p.d_o) + (row * p.Hq + tl.hq) * D + 8 * h;
+    const bf16* op = static_cast<const bf16*>(p.o) + (row * p.Hq + tl.hq) * D + 8 * h;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      q[kb] = *reinterpret_cast<const bf16x8*>(qp + 16 * kb);
+      go[kb] = *reinterpret_cast<const bf16x8*>(gp + 16 * kb);
+      const bf16x8 o = *reinterpret_cast<const bf16x8*>(op + 16 * kb);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dl = __builtin_fmaf((float)go[kb][i], (float)o[i], dl);
+    }
+    dl += __shfl_xor(dl, 32);
+    const float2 st = reinterpret_cast<const float2*>(p.stats)[row * p.Hq + tl.hq];
+    lse = st.x + __builtin_amdgcn_logf(st.y);
+    if (h == 0 && tq < L) {
+      const uint2 a = three_terms(-lse / c_scale), b = three_terms(-dl);
+      aux_of(p, tl.hq)[row] = make_uint4(a.x, a.y, b.x, b.y);
+    }
+  }
+  f32x16 dq[MT];
+#pragma unroll
+  for (int c = 0; c < MT; ++c)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) dq[c][r] = 0.f;
+
+  int buf = 0;
+  for (int k0 = lo; k0 < stop; k0 += BN, buf ^= 1) {
+    wait_tiles();
+    if (k0 + BN < stop) {
+      load_tile64<D>(kb_ + (k0 + BN) * p.ld_k, lk2, L - k0 - BN, s_k[buf ^ 1], tid);
+      load_tile64<D>(vb_ + (k0 + BN) * p.ld_v, lv2, L - k0 - BN, s_v[buf ^ 1], tid);
+    }
+    if (q0 >= L) continue;
+#pragma unroll
+    for (int sub = 0; sub < BN; sub += 32) {
+      const int kw = k0 + sub;
+      if (kw > q0 + 31 || (window && kw + 31 <= q0 - window)) continue;   // nothing seen
+      f32x16 s, dp;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_rows<D>(s_k[buf], sub, kb, lane), q[kb], s, 0, 0, 0);
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_rows<D>(s_v[buf], sub, kb, lane), go[kb], dp, 0, 0, 0);
+      }
+      if (kw + 31 > q0 || (window && kw <= q0 + 31 - window)) {
+        const int last = tq - kw - 4 * h, before = window ? last - window : -1;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int u = 8 * (r / 4) + r % 4;
+          if (u > last || u <= before) s[r] = -__builtin_huge_valf() * c_scale;
+        }
+      }
+      bf16x8 ds[2];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float pr = exp2_fast(__builtin_fmaf(s[r], c_scale, -lse));
+        ds[r / 8][r % 8] = (bf16)(pr * (dp[r] - dl));
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int c = 0; c < MT; ++c)
+          dq[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_columns<D>(s_k[buf], sub + 16 * b, c, lane), ds[b], dq[c], 0, 0, 0);
+    }
+  }
+  if (tq >= L) return;
+  TG* to = static_cast<TG*>(p.dq) + (tl.a + tq) * p.ld_dq + tl.hq * D + 4 * h;
+#pragma unroll
+  for (int c = 0; c < MT; ++c)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+      store4<TG>(to + 32 * c + 2 * r, dq[c][r] * p.scale, dq[c][r + 1] * p.scale, dq[c][r + 2] * p.scale, dq[c][r + 3] * p.scale);
+}
+
+// The statistics enter the first products: a 17th block of 16 k-values holds, of each
+// query, -(m + log2 l) / (c log2 e) and -D in three bf16 terms each, and ones on the
+// side of the keys.  So the products give c q . k - m - log2 l (over c) and
+// d_o . v - D without a vector operation, and without the 8 LDS reads that would bring
+// them to the lanes, whose 16 rows are all different queries.
+template <int D, typename TG>
+__global__ __launch_bounds__(kThreads, 2) void attn_dkv_bf16_kernel(AttnBwdArgs p, uint32_t blocks, int parts) {
+  constexpr int BK = 128, BQ = 64, KB = D / 16, MT = D / 32;
+  __shared__ __align__(16) bf16 s_q[2][BQ * D], s_g[2][BQ * D];
+  __shared__ __align__(16) uint4 s_aux[2][BQ];
+  lds_nan_fill(s_q, sizeof s_q);
+  lds_nan_fill(s_g, sizeof s_g);
+  const int G = p.Hq / p.Hk;
+  const Tile tl = find_tile<BK>(tile_args(p, parts), blocks);
+  if (!tl.valid) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, i32 = lane & 31;
+  const int hk = __builtin_amdgcn_readfirstlane(tl.hq / parts);
+  const int part = __builtin_amdgcn_readfirstlane(tl.hq - hk * parts);
+  const int L = __builtin_amdgcn_readfirstlane((int)tl.L);
+  const int k0 = __builtin_amdgcn_readfirstlane(key_tile_start<BK>(tl));
+  const int u0 = k0 + 32 * wave, tk = u0 + i32;       // this lane's key
+  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
+  const Walk w = walk_of<BK, BQ>(k0, L, window, G, part, parts);
+  const float c_scale = p.scale * kLog2e;
+  const uint32_t lq2 = (uint32_t)p.ld_q * 2, lg2 = (uint32_t)p.Hq * D * 2;
+
+  int head = w.at / w.each, tile = w.at - head * w.each;   // of the step to load
+  auto load_step = [&](int buf) {
+    const int hq = hk * G + head, t0 = k0 + tile * BQ;
+    load_tile64<D>(static_cast<const bf16*>(p.q) + (tl.a + t0) * p.ld_q + hq * D, lq2, L - t0, s_q[buf], tid);
+    load_tile64<D>(static_cast<const bf16*>(p.d_o) + ((tl.a + t0) * p.Hq + hq) * (int64_t)D, lg2, L - t0, s_g[buf], tid);
+    if (wave == 0)
+      load_lds16(__builtin_amdgcn_readfirstlane(lds_address(s_aux[buf])), buffer_at(aux_of(p, hq) + tl.a + t0),
+                 16u * (uint32_t)(lane < L - t0 ? lane : L - t0 - 1), 0);
+    if (++tile == w.each) { tile = 0; ++head; }
+  };
+  if (w.at < w.stop) load_step(0);
+  bf16x8 k[KB], v[KB];
+  {
+    const int64_t row = tl.a + (tk < L ? tk : L - 1);
+    const bf16* kp = static_cast<const bf16*>(p.k) + row * p.ld_k + hk * D + 8 * h;
+    const bf16* vp = static_cast<const bf16*>(p.v) + row * p.ld_v + hk * D + 8 * h;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      k[kb] = *reinterpret_cast<const bf16x8*>(kp + 16 * kb);
+      v[kb] = *reinterpret_cast<const bf16x8*>(vp + 16 * kb);
+    }
+  }
+  // lanes 0..31 supply the terms of m and l, 32..63 those of D
+  const uint32_t one = 0x3f80;              // 1 in bf16
+  const uint32_t s1 = h == 0 ? one << 16 | one : 0, s2 = h == 0 ? one : 0;
+  const uint32_t d1 = h == 1 ? one << 16 | one : 0, d2 = h == 1 ? one : 0;
+  f32x16 dk[MT], dv[MT];
+#pragma unroll
+  for (int c = 0; c < MT; ++c)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) dk[c][r] = dv[c][r] = 0.f;
+
+  int now = w.each > 0 ? w.at % w.each : 0;
+  for (int step = w.at; step < w.stop; ++step) {
+    const int buf = (step - w.at) & 1;
+    wait_tiles();
+    if (step + 1 < w.stop) load_step(buf ^ 1);
+    const int tt = k0 + now * BQ;
+    if (++now == w.each) now = 0;
+    if (u0 >= L) continue;
+#pragma unroll
+    for (int sub = 0; sub < BQ; sub += 32) {
+      const int t0 = tt + sub;
+      if (t0 + 31 < u0 || t0 >= L || (window && t0 - window >= u0 + 31)) continue;   // no pair
+      f32x16 s, dp;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
+      {
+        const uint2 a = reinterpret_cast<const uint2*>(&s_aux[buf][sub + i32])[h];
+        const bf16x8 x = __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, 0, 0));
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, __builtin_bit_cast(bf16x8, make_uint4(s1, s2, 0, 0)), s, 0, 0, 0);
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, __builtin_bit_cast(bf16x8, make_uint4(d1, d2, 0, 0)), dp, 0, 0, 0);
+      }
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_rows<D>(s_q[buf], sub, kb, lane), k[kb], s, 0, 0, 0);
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_rows<D>(s_g[buf], sub, kb, lane), v[kb], dp, 0, 0, 0);
+      }
+      if (t0 < u0 + 31 || t0 + 31 >= L || (window && t0 + 31 - window >= u0)) {
+        // element r is query t0 + 4 h + at: seen where it is at the key or behind it,
+        // before the end, and less than the window behind it
+        const int first = tk - t0 - 4 * h;
+        int end = L - t0 - 4 * h;
+        if (window && first + window < end) end = first + window;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int at = 8 * (r / 4) + r % 4;
+          if (at < first || at >= end) s[r] = -__builtin_huge_valf() * c_scale;
+        }
+      }
+      bf16x8 pw[2], dw[2];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float pr = exp2_fast(s[r] * c_scale);
+        pw[r / 8][r % 8] = (bf16)pr;
+        dw[r / 8][r % 8] = (bf16)(pr * dp[r]);
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int c = 0; c < MT; ++c) {
+          dv[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_columns<D>(s_g[buf], sub + 16 * b, c, lane), pw[b], dv[c], 0, 0, 0);
+          dk[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_columns<D>(s_q[buf], sub + 16 * b, c, lane), dw[b], dk[c], 0, 0, 0);
+        }
+    }
+  }
+  if (tk >= L) return;
+  if (parts == 1) {
+    TG* tok = static_cast<TG*>(p.dk) + (tl.a + tk) * p.ld_dk + hk * D + 4 * h;
+    TG* tov = static_cast<TG*>(p.dv) + (tl.a + tk) * p.ld_dv + hk * D + 4 * h;
+#pragma unroll
+    for (int c = 0; c < MT; ++c)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        store4<TG>(tok + 32 * c + 2 * r, dk[c][r] * p.scale, dk[c][r + 1] * p.scale, dk[c][r + 2] * p.scale, dk[c][r + 3] * p.scale);
+        store4<TG>(tov + 32 * c + 2 * r, dv[c][r], dv[c][r + 1], dv[c][r + 2], dv[c][r + 3]);
+      }
+  } else {
+    float* tok = parts_of(p) + ((part * p.total_T + tl.a + tk) * p.Hk + hk) * (2 * D) + 4 * h;
+#pragma unroll
+    for (int c = 0; c < MT; ++c)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        store4<float>(tok + 32 * c + 2 * r, dk[c][r] * p.scale, dk[c][r + 1] * p.scale, dk[c][r + 2] * p.scale, dk[c][r + 3] * p.scale);
+        store4<float>(tok + D + 32 * c + 2 * r, dv[c][r], dv[c][r + 1], dv[c][r + 2], dv[c][r + 3]);
+      }
+  }
+}
+
+// The parts of dk and dv added in order: a wave to a row of a tile and head.
+template <typename TG, int D, int BK>
+__global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(AttnBwdArgs p, uint32_t blocks, int parts) {
+  const Tile tl = find_tile<BK>(tile_args(p, 1), blocks);
+  if (!tl.valid) return;
+  constexpr int LR = 2 * D / 4;             // lanes of a row of dk and dv
+  const int k0 = key_tile_start<BK>(tl), c = 4 * (threadIdx.x % LR);
+  for (int r = threadIdx.x / LR; r < BK && k0 + r < tl.L; r += kThreads / LR) {
+    const int64_t row = tl.a + k0 + r;
+    const float* src = parts_of(p) + (row * p.Hk + tl.hq) * (2 * D) + c;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < parts; ++i) {
+      const float4 u = *reinterpret_cast<const float4*>(src + i * p.total_T * p.Hk * (2 * D));
+      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    }
+    if (c < D) store4<TG>(static_cast<TG*>(p.dk) + row * p.ld_dk + tl.hq * D + c, v.x, v.y, v.z, v.w);
+    else store4<TG>(static_cast<TG*>(p.dv) + row * p.ld_dv + tl.hq * D + c - D, v.x, v.y, v.z, v.w);
+  }
+}
+
+int64_t tiles_of(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int64_t rows) {
+  return packed ? total_T / rows + N : N * ((Tseq + rows - 1) / rows);
+}
+
+template <typename TG, int D>
+hipError_t launch_bf16(const AttnBwdArgs& a, int parts, hipStream_t stream) {
+  const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, 128);
+  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = (uint32_t)(tiles * a.Hk * parts), nj = (uint32_t)(tiles * a.Hk);
+  attn_dq_bf16_kernel<D, TG><<<dim3(nq), kThreads, 0, stream>>>(a, nq);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  attn_dkv_bf16_kernel<D, TG><<<dim3(nk), kThreads, 0, stream>>>(a, nk, parts);
+  e = hipGetLastError();
+  if (e != hipSuccess || parts == 1) return e;
+  attn_dkv_join_kernel<TG, D, 128><<<dim3(nj), kThreads, 0, stream>>>(a, nj, parts);
+  return hipGetLastError();
+}
+template <int D>
+hipError_t launch_f32(const AttnBwdArgs& a, int parts, hipStream_t stream) {
+  const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, 32);
+  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = (uint32_t)(tiles * a.Hk * parts), nj = (uint32_t)(tiles * a.Hk);
+  attn_dq_f32_kernel<D><<<dim3(nq), kThreads, 0, stream>>>(a, nq);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  attn_dkv_f32_kernel<D><<<dim3(nk), kThreads, 0, stream>>>(a, nk, parts);
+  e = hipGetLastError();
+  if (e != hipSuccess || parts == 1) return e;
+  attn_dkv_join_kernel<float, D, 32><<<dim3(nj), kThreads, 0, stream>>>(a, nj, parts);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+AttnBwdPlan attn_bwd_plan(int64_t N, int64_t total_T, int64_t window, int Hq, int Hk, int d, DType io) {
+  const int64_t tiles = (total_T + (io == DType::F32 ? 31 : 127)) / (io == DType::F32 ? 32 : 128) * Hk;
+  int64_t parts = tiles > 0 ? 2048 / tiles : 1;
+  const int64_t most = Hq / Hk * 2;
+  parts = parts < most ? parts : most;
+  if (parts < 1) parts = 1;
+  AttnBwdPlan r;
+  r.parts = (int)parts;
+  r.ws_floats = 4 * total_T * Hq + (parts > 1 ? parts * total_T * Hk * 2 * d : 0);
+  return r;
+}
+
+int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, int Hk, int parts, DType io) {
+  const int64_t tiles = tiles_of(N, total_T, Tseq, packed, io == DType::F32 ? 32 : 128);
+  const int64_t a = tiles * Hq, b = tiles * Hk * parts;
+  return a > b ? a : b;
+}
+
+hipError_t launch_attn_bwd(const AttnBwdArgs& a, const AttnBwdPlan& plan, hipStream_t stream) {
+  if (a.io == DType::F32)
+    return a.d == 128 ? launch_f32<128>(a, plan.parts, stream) : launch_f32<64>(a, plan.parts, stream);
+  if (a.grad == DType::F32)
+    return a.d == 128 ? launch_bf16<float, 128>(a, plan.parts, stream) : launch_bf16<float, 64>(a, plan.parts, stream);
+  return a.d == 128 ? launch_bf16<bf16, 128>(a, plan.parts, stream) : launch_bf16<bf16, 64>(a, plan.parts, stream);
+}
+
+#ifdef GDN_CHECK
+unsigned check_violations_attn_bwd() { return take_check_violations(); }
+#endif
+
+}  // namespace gdn

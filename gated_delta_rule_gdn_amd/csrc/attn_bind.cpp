@@ -1,6 +1,7 @@
 // attn_bind.cpp -- Python extension module _attn_native: checks the tensors of
-// an attention call, fills its descriptor and calls the C ABI
-// (include/gdn_attn.h).  Argument marshalling only.
+// an attention call or of one of a hybrid's other operators, fills its descriptor
+// and calls the C ABI (include/gdn_attn.h, include/gdn_hybrid.h).  Argument
+// marshalling only.
 //
 // A decode step's calls are so short that the host's share decides how fast
 // they follow each other; the same checks made from Python cost 5 us a call.
@@ -20,7 +21,7 @@
 #include <initializer_list>
 #include <string>
 
-#include "gdn_attn.h"
+#include "gdn_hybrid.h"
 
 namespace {
 
@@ -390,6 +391,260 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (fn, q, k, v, cu_seqlens, N, window, scale, o, stats, stream)
+PyObject* attn_prefill_save(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    const Tensor& q = first(a[1], "q");
+    const int dev = (int)q.get_device();
+    const ScalarType io = q.scalar_type();
+    const int64_t T = q.size(0), d = q.size(2);
+    gdn_attn_prefill_desc desc{};
+    desc.total_T = T;
+    desc.H_q = narrow(q.size(1), "H_q");
+    desc.H_k = narrow(first(a[2], "k").size(1), "H_k");
+    desc.d = narrow(d, "d");
+    desc.io_dtype = io_of(io);
+    const void* q_in = heads(a[1], "q", dev, T, desc.H_q, d, io, &desc.ld_q);
+    const void* k_in = heads(a[2], "k", dev, T, desc.H_k, d, io, &desc.ld_k);
+    const void* v_in = heads(a[3], "v", dev, T, desc.H_k, d, io, &desc.ld_v);
+    const int64_t* cu;
+    desc.N = packed(a[4], a[5], dev, &cu);
+    desc.window = integer(a[6], "window");
+    desc.scale = scale_of(a[7], d);
+    void* o = dense(a[8], "o", dev, {T, desc.H_q, d}, io);
+    void* stats = dense(a[9], "stats", dev, {T, desc.H_q, 2}, ScalarType::Float);
+    const auto fn = function<decltype(&gdn_attn_prefill_save)>(a[0]);
+    void* stream = handle(a[10]);
+    return on_device(dev, [&] {
+      return fn(&desc, cu, q_in, k_in, v_in, o, static_cast<float*>(stats), stream);
+    });
+  });
+}
+
+// The workspace's address and bytes where `need` is not 0; false: it is not given.
+bool workspace_of(PyObject* o, int dev, size_t need, void** ws, size_t* bytes) {
+  *ws = nullptr;
+  *bytes = 0;
+  if (!need) return true;
+  if (o == Py_None) return false;
+  const Tensor& t = tensor(o, "workspace");
+  if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
+    throw Refused("workspace must be a contiguous tensor on the device of the others");
+  *ws = t.data_ptr();
+  *bytes = t.nbytes();
+  return true;
+}
+
+// The type of an operand that may be fp32 beside bf16.
+ScalarType second_type(const Tensor& t, const char* name) {
+  const ScalarType s = t.scalar_type();
+  if (s != ScalarType::Float && s != ScalarType::BFloat16)
+    throw Refused(std::string(name) + " must be float32 or bfloat16");
+  return s;
+}
+
+// (fn, size_fn, q, k, v, o, d_o, stats, cu_seqlens, N, window, scale, dq, dk, dv, workspace, stream); a workspace
+// that is needed and not given: minus its bytes
+PyObject* attn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    const Tensor& q = first(a[2], "q");
+    const int dev = (int)q.get_device();
+    const ScalarType io = q.scalar_type();
+    const int64_t T = q.size(0), d = q.size(2);
+    gdn_attn_bwd_desc desc{};
+    desc.total_T = T;
+    desc.H_q = narrow(q.size(1), "H_q");
+    desc.H_k = narrow(first(a[3], "k").size(1), "H_k");
+    desc.d = narrow(d, "d");
+    desc.io_dtype = io_of(io);
+    const void* q_in = heads(a[2], "q", dev, T, desc.H_q, d, io, &desc.ld_q);
+    const void* k_in = heads(a[3], "k", dev, T, desc.H_k, d, io, &desc.ld_k);
+    const void* v_in = heads(a[4], "v", dev, T, desc.H_k, d, io, &desc.ld_v);
+    const void* o = dense(a[5], "o", dev, {T, desc.H_q, d}, io);
+    const void* d_o = dense(a[6], "d_o", dev, {T, desc.H_q, d}, io);
+    const void* stats = dense(a[7], "stats", dev, {T, desc.H_q, 2}, ScalarType::Float);
+    const int64_t* cu;
+    desc.N = packed(a[8], a[9], dev, &cu);
+    desc.window = integer(a[10], "window");
+    desc.scale = scale_of(a[11], d);
+    const ScalarType grad = second_type(tensor(a[12], "dq"), "dq");
+    desc.grad_dtype = io_of(grad);
+    void* dq = heads(a[12], "dq", dev, T, desc.H_q, d, grad, &desc.ld_dq);
+    void* dk = heads(a[13], "dk", dev, T, desc.H_k, d, grad, &desc.ld_dk);
+    void* dv = heads(a[14], "dv", dev, T, desc.H_k, d, grad, &desc.ld_dv);
+    const size_t need = function<decltype(&gdn_attn_backward_workspace_size)>(a[1])(&desc);
+    void* ws;
+    size_t bytes;
+    if (!workspace_of(a[15], dev, need, &ws, &bytes)) return PyLong_FromLongLong(-(long long)need);
+    const auto fn = function<decltype(&gdn_attn_backward)>(a[0]);
+    void* stream = handle(a[16]);
+    return on_device(dev, [&] {
+      return fn(&desc, cu, q_in, k_in, v_in, o, d_o, static_cast<const float*>(stats), ws, bytes,
+                dq, dk, dv, stream);
+    });
+  });
+}
+
+// (fn, size_fn, dq, dk, q_raw, k_raw, positions, inv_freq, q_weight, k_weight, interleaved, rope_scale, eps, dq_raw,
+//  dk_raw, dq_weight, dk_weight, workspace, stream); a workspace that is needed and not given: minus its bytes
+PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 19, [&]() -> PyObject* {
+    const bool has_q = a[2] != Py_None, has_k = a[3] != Py_None;
+    if (!has_q && !has_k) throw Refused("dq or dk must be given");
+    const Tensor& one = has_q ? first(a[2], "dq") : first(a[3], "dk");
+    const int dev = (int)one.get_device();
+    const ScalarType grad = one.scalar_type();
+    const int64_t rows = one.size(0), d = one.size(2);
+    gdn_qk_bwd_desc desc{};
+    desc.rows = rows;
+    desc.d = narrow(d, "d");
+    desc.grad_dtype = desc.io_dtype = io_of(grad);
+    ScalarType io = grad;
+    if (has_q && a[4] != Py_None) io = second_type(tensor(a[4], "q_raw"), "q_raw");
+    else if (has_k && a[5] != Py_None) io = second_type(tensor(a[5], "k_raw"), "k_raw");
+    desc.io_dtype = io_of(io);
+    const void* up[2] = {nullptr, nullptr};
+    const void* raw[2] = {nullptr, nullptr};
+    void* out[2] = {nullptr, nullptr};
+    const char* names[2][3] = {{"dq", "q_raw", "dq_raw"}, {"dk", "k_raw", "dk_raw"}};
+    for (int i = 0; i < 2; ++i) {
+      int32_t& H = i ? desc.H_k : desc.H_q;
+      int64_t &ld = i ? desc.ld_k : desc.ld_q, &ldo = i ? desc.ld_dk : desc.ld_dq;
+      if (a[2 + i] == Py_None) {
+        if (a[4 + i] != Py_None || a[13 + i] != Py_None)
+          throw Refused(std::string(names[i][1]) + " or " + names[i][2] + " without " + names[i][0]);
+        continue;
+      }
+      H = narrow(first(a[2 + i], names[i][0]).size(1), "H");
+      up[i] = dense(a[2 + i], names[i][0], dev, {rows, H, d}, grad);
+      ld = (int64_t)H * d;
+      if (a[4 + i] != Py_None) raw[i] = heads(a[4 + i], names[i][1], dev, rows, H, d, io, &ld);
+      out[i] = heads(a[13 + i], names[i][2], dev, rows, H, d, grad, &ldo);
+    }
+    if (a[7] != Py_None && a[6] == Py_None) throw Refused("rotation needs positions");
+    const float* freqs;
+    desc.rope_dim = rope_of(a[7], dev, &freqs);
+    const void* pos = dense(a[6], "positions", dev, {rows}, ScalarType::Long);
+    const void* qw = dense(a[8], "q_weight", dev, {d}, ScalarType::Float);
+    const void* kw = dense(a[9], "k_weight", dev, {d}, ScalarType::Float);
+    desc.rope_mode = truth(a[10], "interleaved") ? GDN_ROPE_INTERLEAVED : GDN_ROPE_HALF;
+    desc.rope_scale = (float)number(a[11], "rope_scale");
+    desc.eps = (float)number(a[12], "eps");
+    void* dqw = dense(a[15], "dq_weight", dev, {d}, ScalarType::Float);
+    void* dkw = dense(a[16], "dk_weight", dev, {d}, ScalarType::Float);
+    const size_t need = dqw || dkw
+        ? function<decltype(&gdn_qk_norm_rope_backward_workspace_size)>(a[1])(&desc) : 0;
+    void* ws;
+    size_t bytes;
+    if (!workspace_of(a[17], dev, need, &ws, &bytes)) return PyLong_FromLongLong(-(long long)need);
+    const auto fn = function<decltype(&gdn_qk_norm_rope_backward)>(a[0]);
+    void* stream = handle(a[18]);
+    return on_device(dev, [&] {
+      return fn(&desc, up[0], up[1], raw[0], raw[1], static_cast<const float*>(qw),
+                static_cast<const float*>(kw),
+                desc.rope_dim ? static_cast<const int64_t*>(pos) : nullptr, freqs, ws, bytes, out[0],
+                out[1], static_cast<float*>(dqw), static_cast<float*>(dkw), stream);
+    });
+  });
+}
+
+// The [rows, C] tensor `name` on device dev (any if < 0) with dense rows, its type and row stride.
+void* rows_of(PyObject* o, const char* name, int dev, int64_t rows, int64_t C, ScalarType type,
+              int64_t* ld) {
+  const Tensor& t = like(o, name, dev, {rows, C}, type);
+  if (t.stride(1) != 1 && rows * C > 0 && C > 1)
+    throw Refused(std::string(name) + " must have dense rows of " + std::to_string(C) + " elements");
+  *ld = rows > 1 ? t.stride(0) : C;
+  return t.data_ptr();
+}
+const Tensor& first_rows(PyObject* o, const char* name) {
+  const Tensor& t = tensor(o, name);
+  if (!t.is_cuda()) throw Refused(std::string(name) + " must be a device tensor");
+  second_type(t, name);
+  if (t.dim() != 2) throw Refused(std::string(name) + " must have 2 dimensions (rows, channels)");
+  return t;
+}
+
+// (fn, x, res, weight, eps, group (None: y like x), res_out, y, y_scale, stream)
+PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject* {
+    const Tensor& x = first_rows(a[1], "x");
+    const int dev = (int)x.get_device();
+    const ScalarType io = x.scalar_type();
+    const int64_t rows = x.size(0), C = x.size(1);
+    gdn_add_norm_desc desc{};
+    desc.rows = rows;
+    desc.C = narrow(C, "C");
+    desc.io_dtype = desc.res_dtype = io_of(io);
+    desc.eps = (float)number(a[4], "eps");
+    desc.group = -1;
+    if (a[5] != Py_None) {
+      const int64_t g = integer(a[5], "group");
+      if (g < 0 || (g > 0 && C % g != 0))
+        throw Refused("group must be None, 0 or a divisor of the row's channels");
+      desc.group = narrow(g, "group");
+    }
+    const void* x_in = rows_of(a[1], "x", dev, rows, C, io, &desc.ld_x);
+    ScalarType rt = io;
+    if (a[2] != Py_None) rt = second_type(tensor(a[2], "res"), "res");
+    else if (a[6] != Py_None) rt = second_type(tensor(a[6], "res_out"), "res_out");
+    desc.res_dtype = io_of(rt);
+    const void* res = dense(a[2], "res", dev, {rows, C}, rt);
+    const void* weight = dense(a[3], "weight", dev, {C}, ScalarType::Float);
+    void* res_out = dense(a[6], "res_out", dev, {rows, C}, rt);
+    const bool codes = desc.group >= 0;
+    void* y = dense(a[7], "y", dev, {rows, C}, codes ? ScalarType::Float8_e4m3fn : io);
+    void* scale = nullptr;
+    if (codes) {
+      scale = dense(a[8], "y_scale", dev, {rows, desc.group ? C / desc.group : 1}, ScalarType::Float);
+    } else if (a[8] != Py_None) {
+      throw Refused("y_scale without group");
+    }
+    const auto fn = function<decltype(&gdn_add_norm)>(a[0]);
+    void* stream = handle(a[9]);
+    return on_device(dev, [&] {
+      return fn(&desc, x_in, res, static_cast<const float*>(weight), res_out, y,
+                static_cast<float*>(scale), stream);
+    });
+  });
+}
+
+// (fn, size_fn, dy, r, weight, d_res_out, eps, dx, d_res, d_weight, workspace, stream); a workspace that is needed and
+// not given: minus its bytes
+PyObject* add_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const Tensor& dy = first_rows(a[2], "dy");
+    const int dev = (int)dy.get_device();
+    const ScalarType io = dy.scalar_type();
+    const int64_t rows = dy.size(0), C = dy.size(1);
+    const ScalarType rt = second_type(tensor(a[3], "r"), "r");
+    gdn_add_norm_bwd_desc desc{};
+    desc.rows = rows;
+    desc.C = narrow(C, "C");
+    desc.ld_dx = C;
+    desc.io_dtype = io_of(io);
+    desc.res_dtype = io_of(rt);
+    desc.eps = (float)number(a[6], "eps");
+    const void* up = dense(a[2], "dy", dev, {rows, C}, io);
+    const void* r = dense(a[3], "r", dev, {rows, C}, rt);
+    const void* weight = dense(a[4], "weight", dev, {C}, ScalarType::Float);
+    const void* dro = dense(a[5], "d_res_out", dev, {rows, C}, rt);
+    void* dx = a[7] == Py_None ? nullptr : rows_of(a[7], "dx", dev, rows, C, io, &desc.ld_dx);
+    void* d_res = dense(a[8], "d_res", dev, {rows, C}, rt);
+    void* dw = dense(a[9], "d_weight", dev, {C}, ScalarType::Float);
+    const size_t need = dw ? function<decltype(&gdn_add_norm_backward_workspace_size)>(a[1])(&desc) : 0;
+    void* ws;
+    size_t bytes;
+    if (!workspace_of(a[10], dev, need, &ws, &bytes)) return PyLong_FromLongLong(-(long long)need);
+    const auto fn = function<decltype(&gdn_add_norm_backward)>(a[0]);
+    void* stream = handle(a[11]);
+    return on_device(dev, [&] {
+      return fn(&desc, up, r, static_cast<const float*>(weight), dro, ws, bytes, dx, d_res,
+                static_cast<float*>(dw), stream);
+    });
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return PyMethodDef{name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)),
@@ -397,7 +652,12 @@ PyMethodDef method(const char* name) {
 }
 PyMethodDef g_methods[] = {method<qk_norm_rope>("qk_norm_rope"), method<kv_append>("kv_append"),
                            method<attn_prefill>("attn_prefill"),
-                           method<attn_decode>("attn_decode"), {nullptr, nullptr, 0, nullptr}};
+                           method<attn_decode>("attn_decode"),
+                           method<attn_prefill_save>("attn_prefill_save"),
+                           method<attn_backward>("attn_backward"),
+                           method<qk_norm_rope_backward>("qk_norm_rope_backward"),
+                           method<add_norm>("add_norm"),
+                           method<add_norm_backward>("add_norm_backward"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_attn_native", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 

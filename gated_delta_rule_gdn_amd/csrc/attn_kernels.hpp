@@ -59,6 +59,7 @@ struct PrefillArgs {
   float scale;
   const void *q, *k, *v;
   void* o;
+  float* stats = nullptr;             // [total_T, Hq, 2] or NULL
 };
 
 struct AttnDecodeArgs {

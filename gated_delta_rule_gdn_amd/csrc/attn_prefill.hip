@@ -5,6 +5,9 @@
 //
 // in one pass over the keys with a running maximum m and sum for each query.
 //
+// Where asked, each query leaves m (times log2 e) and l, the sum of its p_ts, for the
+// backward pass (attn_backward.hip).
+//
 // Both kernels put the queries on the columns of the products,
 //   S^T [tokens x queries] = K Q^T,    O^T [d x queries] += V^T P^T,
 // so that a lane holds scores of one query only: the maximum and the sum are
@@ -23,103 +26,15 @@
 // TFLOP/s; 16 prompts, 32768 tokens in all, a window of 2048, 337 to 361 us, 954 to
 // 1022 TFLOP/s.  Short prompts wait for memory at both ends of a tile (about 6 us
 // of each workgroup).
-#include "attn_device.hpp"
+#include "attn_tiles.hpp"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
 
-// One workgroup's query tile: queries [q0, q0 + BM) of the sequence that is
-// rows [a, a + L) of the packed tensors, and a query head.
-struct Tile {
-  int64_t a, L, q0;
-  int hq;
-  bool valid;
-};
-
-// Workgroup blk runs on XCD blk % 8, and each XCD has an L2 of its own, so the
-// workgroups that follow each other on an XCD should read the same keys and
-// values; and a query tile costs as many key tiles as lie before it, so the
-// late tiles should start first.  The query heads of a key head always follow
-// each other.  (All counts fit in 32 bits: the host bounds the grid.)
-//
-// Equal lengths, key heads of all sequences a multiple of 8: an XCD keeps its
-// share of them, in groups of 4 query heads or more, and goes through each
-// group's tiles from the last to the first.  64 workgroups
-// of an XCD then walk the keys of 4 heads together (B 8, T 4096, 16 heads:
-// 78 % of the L2 reads hit against 48 % with heads dealt round the XCDs).
-// Otherwise tiles are dealt round the XCDs, the last tiles of all sequences
-// first.
-//
-// Packed lengths: the tiles are dealt round the XCDs, the dear ones first
-// (rank_tile_by): found by counting, so nothing is sorted.  (16 prompts, 32768
-// tokens, a window of 2048: 367 us; in the order of the tokens 383 us.)
-constexpr uint32_t kXcds = 8;
-constexpr int64_t kMaxRanked = 1024;      // sequences that are ranked; more keep their order
-
-template <int BM>
-__device__ __forceinline__ Tile find_tile(const PrefillArgs& p, uint32_t blocks) {
-  Tile t;
-  const uint32_t blk = blockIdx.x;
-  const uint32_t G = (uint32_t)(p.Hq / p.Hk), Hk = (uint32_t)p.Hk, N = (uint32_t)p.N;
-  const uint32_t per = blocks / kXcds;                    // full rounds over the XCDs
-  const uint32_t xcd = blk % kXcds, i = blk / kXcds;
-  t.valid = true;
-  if (!p.cu_seqlens) {
-    const uint32_t tiles = ((uint32_t)p.Tseq + BM - 1) / BM, pairs = N * Hk;
-    const uint32_t mine = pairs / kXcds;                  // pairs of an XCD
-    uint32_t pair, tile, head;
-    if (pairs % kXcds == 0) {
-      const uint32_t gp = G >= 4 ? 1 : 4 / G;             // pairs of a group
-      const uint32_t grp = i / (gp * tiles * G), w = i - grp * (gp * tiles * G);
-      const uint32_t here = mine - grp * gp < gp ? mine - grp * gp : gp;
-      const uint32_t level = w / (here * G), x = w - level * (here * G);
-      tile = tiles - 1 - level;
-      pair = xcd + kXcds * (grp * gp + x / G);
-      head = x % G;
-    } else {
-      // unit = (tile from the last, pair); the last partial round is dealt plainly
-      uint32_t unit;
-      const uint32_t rounds = per / G;
-      if (i < rounds * G) { unit = i / G * kXcds + xcd; head = i % G; }
-      else { const uint32_t r = blk - rounds * G * kXcds; unit = rounds * kXcds + r / G; head = r % G; }
-      tile = tiles - 1 - unit / pairs;
-      pair = unit % pairs;
-    }
-    const uint32_t n = pair / Hk, hk = pair - n * Hk;
-    t.a = n * p.Tseq;
-    t.L = p.Tseq;
-    t.q0 = (int64_t)tile * BM;
-    t.hq = (int)(hk * G + head);
-    return t;
-  }
-  uint32_t unit, head;
-  const uint32_t rounds = per / G;
-  if (i < rounds * G) {
-    unit = i / G * kXcds + xcd;
-    head = i % G;
-  } else {
-    const uint32_t r = blk - rounds * G * kXcds;
-    unit = rounds * kXcds + r / G;
-    head = r % G;
-  }
-  const uint32_t rank = unit / Hk;
-  t.hq = (int)((unit - rank * Hk) * G + head);
-  PackedItem it;
-  // tiles from this number on see a whole window
-  const int level = (int)((p.window > 0 && p.window < p.total_T ? p.window : p.total_T) + BM - 1) / BM;
-  if (p.N <= 64)
-    it = rank_tile<1>(p.cu_seqlens, (int)p.N, p.total_T, BM, level, (int)rank);
-  else if (p.N <= kMaxRanked)
-    it = rank_tile<kMaxRanked / 64>(p.cu_seqlens, (int)p.N, p.total_T, BM, level, (int)rank);
-  else
-    it = find_packed(p.cu_seqlens, p.N, p.total_T, BM, 1, (int64_t)rank);
-  t.a = it.start;
-  t.L = it.end - it.start;
-  t.q0 = it.item * BM;
-  t.valid = t.q0 >= 0 && t.q0 < t.L;
-  return t;
+__device__ __forceinline__ TileArgs tile_args(const PrefillArgs& p) {
+  return TileArgs{p.cu_seqlens, p.N, p.Tseq, p.total_T, p.window, p.Hk, p.Hq / p.Hk};
 }
 
 // The products give unseen tokens a weight of zero, and zero times an infinite or
@@ -147,6 +62,13 @@ __device__ __forceinline__ bool unseen_not_finite(const T* __restrict__ v, int64
   scan(q0 + 1, q0 + 160);
   if (window) scan(q0 - window - 160, q0 + rows - window);
   return __any(z != z);
+}
+
+// A query's running maximum and sum, as they are at its end.
+__device__ __forceinline__ void leave_stats(const PrefillArgs& p, const Tile& tl, int t, float m,
+                                            float l) {
+  float2* to = reinterpret_cast<float2*>(p.stats) + (tl.a + t) * p.Hq + tl.hq;
+  *to = make_float2(m, l);
 }
 
 // Says that x points to global memory, as a kernel's own arguments do.
@@ -218,6 +140,7 @@ __device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl,
     T* op = static_cast<T*>(p.o) + ((tl.a + t) * p.Hq + tl.hq) * (int64_t)D + lane;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) op[64 * c] = (T)(o[c] / l);
+    if (p.stats && lane == 0) leave_stats(p, tl, t, m, l);
   }
 }
 
@@ -262,7 +185,7 @@ __global__ __launch_bounds__(128 * KW, KW == 4 ? 2 : D == 64 ? 4 : 3) void prefi
   __shared__ float s_m[KW - 1][32], s_l[KW - 1][32];
   lds_nan_fill(s_kv, sizeof s_kv);
   float *s_k = s_kv, *s_v = s_kv + BN * LD;
-  const Tile tl = find_tile<BM>(p, blocks);
+  const Tile tl = find_tile<BM>(tile_args(p), blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -400,6 +323,7 @@ __global__ __launch_bounds__(128 * KW, KW == 4 ? 2 : D == 64 ? 4 : 3) void prefi
 #pragma unroll
     for (int r = 0; r < 4; ++r) z = __builtin_fmaf(o[c][r], 0.f, z);
   if (__any(z != z) && rows_again<float, D>(tl, hk, window, q0, 16, false)) return;
+  if (p.stats && g == 0 && tq < L) leave_stats(p, tl, tq, m, l);
   float* op = static_cast<float*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * g;
 #pragma unroll
   for (int c = 0; c < MT; ++c)
@@ -428,52 +352,6 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
   return D == 128 ? c ^ ((row & 3) << 2) : c ^ (((row >> 1) & 1) << 2);
 }
 
-__device__ __forceinline__ bf16x4 read_tr16(const bf16* p) {
-  lds_check(p, 8);
-  typedef short v4s __attribute__((ext_vector_type(4)));
-  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (__attribute__((address_space(3))) v4s*)(p)));
-}
-
-// 16 bytes for each lane from base + voff + soff straight into LDS at
-// lds + 16 * lane (lds is the same for the wave).  The load is counted by
-// vmcnt like any other; the compiler does not know of it, so wait_tiles()
-// stands before the barrier behind which the bytes are read.  m0 is set in the same
-// block and named as clobbered; the compiler warns that it is a reserved register,
-// which it sets before each use of its own.  (As an operand "{m0}" its writes are
-// merged across the blocks, and tiles land in the wrong place.)
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ void load_lds16(uint32_t lds, i32x4 base, uint32_t voff, uint32_t soff) {
-#if __HIP_DEVICE_COMPILE__
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %1, %2, %3 offen lds"
-      ::"s"(lds), "v"(voff), "s"(base), "s"(soff) : "memory", "m0");
-#pragma clang diagnostic pop
-#endif
-}
-// This wave's loads have landed and its LDS reads are done; then all waves'.
-__device__ __forceinline__ void wait_tiles() {
-#if __HIP_DEVICE_COMPILE__
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-#endif
-}
-__device__ __forceinline__ i32x4 buffer_at(const void* p) {
-  const uint64_t u = reinterpret_cast<uint64_t>(p);
-  i32x4 r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
-  r[1] = __builtin_amdgcn_readfirstlane((int)((u >> 32) & 0xffff));
-  r[2] = -1;                              // offsets are kept in range by the caller
-  r[3] = 0x00027000;
-  return r;
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
-}
-
 // WIN: with the code of a window's mask (calls without a window are 1 to 2 % faster
 // without it: 8 prompts of 4096 tokens 546 / 540 us, 4 short ones 11.0 / 10.7).
 // SPLIT 2: 64 queries to a workgroup; waves 0 and 1 take the even key tiles, 2
@@ -495,7 +373,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
   __shared__ __align__(16) bf16 s_k[2][STEP * D], s_v[2][STEP * D];
   lds_nan_fill(s_k, sizeof s_k);
   lds_nan_fill(s_v, sizeof s_v);
-  const Tile tl = find_tile<BM>(p, blocks);
+  const Tile tl = find_tile<BM>(tile_args(p), blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -790,6 +668,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
     huge |= s_huge[wq] != 0;
     const float m1 = sm[0], mm = fmaxf(m, m1);
     const float f0 = exp2_fast(m - mm), f1 = exp2_fast(m1 - mm);
+    m = mm;
     l = l * f0 + sm[64] * f1;
 #pragma unroll
     for (int c = 0; c < MT; ++c)
@@ -809,6 +688,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
     for (int r = 0; r < 16; ++r) z[r % 4] = __builtin_fmaf(o[c][r], 0.f, z[r % 4]);
   z[0] += z[1] + (z[2] + z[3]);
   if ((huge || __any(z[0] != z[0])) && rows_again<bf16, D>(tl, hk, window, q0, 32, huge)) return;
+  if (p.stats && h == 0 && tq < L) leave_stats(p, tl, tq, m, l);
   bf16* so = &s_k[0][0] + wq * 32 * D;
 #pragma unroll
   for (int c = 0; c < MT; ++c)
