@@ -36,10 +36,12 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-I", INCLUDE, "-I", CSRC, "-Wall", "-Wno-unused-function"]
 
 
-# Flags of single sources.  attn_prefill.hip: products take and leave their sums
-# in vector registers; otherwise kernels that fill a CU's LDS with one workgroup
-# keep them in accumulation registers and move them there and back in every tile.
-SOURCE_FLAGS = {"attn_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# Flags of single sources.  attn_prefill.hip, attn_backward.hip: products take and
+# leave their sums in vector registers; otherwise kernels that fill a CU's LDS with
+# one workgroup keep them in accumulation registers and move them there and back in
+# every tile.
+SOURCE_FLAGS = {"attn_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+                "attn_backward.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 # The product library and its debug twin (-DGDN_CHECK: LDS filled with NaN
 # at kernel start, LDS accesses and block indices checked, every call waits

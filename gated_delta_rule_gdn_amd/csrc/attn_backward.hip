@@ -484,18 +484,131 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p
       store4<TG>(to + 32 * c + 2 * r, dq[c][r] * p.scale, dq[c][r + 1] * p.scale, dq[c][r + 2] * p.scale, dq[c][r + 3] * p.scale);
 }
 
+// Where a lane reads from a tile in LDS.  Rows: row i32, its 16-byte chunk 2 kb + h, is
+// at rows ^ 32 kb; a tile's rows are 2 D bytes and its base a multiple of that, so the
+// permutation's exclusive or goes through the whole address.  Columns [32 c, +32) of the
+// rows [16 b, +16), transposed: at (cols ^ 64 c ^ 32 half) + (16 b + 8 half) 2 D.
+struct LaneReads {
+  uint32_t rows, cols;
+};
+template <int D>
+__device__ __forceinline__ LaneReads lane_reads(uint32_t base, int lane) {
+  const int h = lane >> 5, i32 = lane & 31, li = lane & 15;
+  const int row = 4 * h + (li >> 2), chunk = 2 * ((lane >> 4) & 1) + ((li & 3) >> 1);
+  return LaneReads{base + i32 * 2 * D + 16 * chunk_at<D>(i32, h),
+                   base + row * 2 * D + 16 * chunk_at<D>(row, chunk) + 8 * (li & 1)};
+}
+template <typename T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+  T x{};
+#if __HIP_DEVICE_COMPILE__
+#ifdef GDN_CHECK
+  check_true(at + sizeof(T) <= __builtin_amdgcn_groupstaticsize());
+#endif
+  x = *(const __attribute__((address_space(3))) T*)at;
+#endif
+  return x;
+}
+template <int D>
+__device__ __forceinline__ bf16x8 rows_at(uint32_t rows, int kb, int offset) {
+  return lds_read<bf16x8>((rows ^ (32 * kb)) + offset);
+}
+template <int D>
+__device__ __forceinline__ bf16x8 columns_at(uint32_t cols, int b, int c, int offset) {
+  bf16x8 f{};
+#if __HIP_DEVICE_COMPILE__
+  typedef short v4s __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t at = (cols ^ (64 * c + 32 * half)) + (16 * b + 8 * half) * 2 * D + offset;
+#ifdef GDN_CHECK
+    check_true(at + 8 <= __builtin_amdgcn_groupstaticsize());
+#endif
+    const bf16x4 u = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) v4s*)at));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[4 * half + i] = u[i];
+  }
+#endif
+  return f;
+}
+
 // The statistics enter the first products: a 17th block of 16 k-values holds, of each
 // query, -(m + log2 l) / (c log2 e) and -D in three bf16 terms each, and ones on the
 // side of the keys.  So the products give c q . k - m - log2 l (over c) and
 // d_o . v - D without a vector operation, and without the 8 LDS reads that would bring
 // them to the lanes, whose 16 rows are all different queries.
+//
+// Products with their registers chosen: sums that stay, and keys and values, in accumulation
+// registers, which the vector unit does not see (the compiler would move them there and
+// back for every product), scores in vector registers.  The compiler knows nothing of what
+// a product takes, so:
+//  - operands that the vector unit wrote go through settle() first (2 wait states);
+//  - results are read by it behind 8 further products or more, or behind products_done()
+//    (11 wait states); all these are volatile, so they keep their order, and in between
+//    results are operands of nothing else;
+//  - a sum comes around again 2 products later at the earliest, which needs no wait.
+__device__ __forceinline__ void product_v0(f32x16& acc, const bf16x8& a, const bf16x8& b) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(acc) : "v"(a), "a"(b));
+#endif
+}
+__device__ __forceinline__ void product_v(f32x16& acc, const bf16x8& a, const bf16x8& b) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(a), "a"(b));
+#endif
+}
+__device__ __forceinline__ void product_a(f32x16& acc, const bf16x8& a, const bf16x8& b) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+#endif
+}
+__device__ __forceinline__ void settle(bf16x8& a) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("s_nop 1" : "+v"(a));
+#endif
+}
+// Behind it the sums can be read, or copied by the compiler: it stands at the end of each
+// loop that adds to them, since copies may be made anywhere behind that.
+template <int N>
+__device__ __forceinline__ void products_done(f32x16* a, f32x16* b) {
+#if __HIP_DEVICE_COMPILE__
+  if constexpr (N == 4)
+    asm volatile("s_nop 11" : "+a"(a[0]), "+a"(a[1]), "+a"(a[2]), "+a"(a[3]), "+a"(b[0]), "+a"(b[1]), "+a"(b[2]), "+a"(b[3]));
+  else
+    asm volatile("s_nop 11" : "+a"(a[0]), "+a"(a[1]), "+a"(b[0]), "+a"(b[1]));
+#endif
+}
+__device__ __forceinline__ void products_done(f32x16& a, f32x16& b) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("s_nop 11" : "+v"(a), "+v"(b));
+#endif
+}
+// What is behind reads x where it stands now.
+__device__ __forceinline__ void behind_v(f32x16& x) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("" : "+v"(x));
+#endif
+}
+__device__ __forceinline__ void keep_a(bf16x8& x) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("" : "+a"(x));
+#endif
+}
+
+// One wave to a SIMD: two sums of 32 keys x D and the keys and values themselves take
+// 192 registers.  What hides latencies instead is a pipeline by hand over blocks of 32
+// queries: the first products of the next block, with the weights of this one formed
+// between them, then this one's second products; every LDS read some products ahead of its
+// use; tiles three deep in LDS.
 template <int D, typename TG>
-__global__ __launch_bounds__(kThreads, 2) void attn_dkv_bf16_kernel(AttnBwdArgs p, uint32_t blocks, int parts) {
+__global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs p, uint32_t blocks, int parts) {
   constexpr int BK = 128, BQ = 64, KB = D / 16, MT = D / 32;
-  __shared__ __align__(16) bf16 s_q[2][BQ * D], s_g[2][BQ * D];
-  __shared__ __align__(16) uint4 s_aux[2][BQ];
-  lds_nan_fill(s_q, sizeof s_q);
-  lds_nan_fill(s_g, sizeof s_g);
+  constexpr int GO = BQ * D * 2;            // d_o behind q in a buffer
+  constexpr int BUF = 2 * GO;
+  __shared__ __align__(1024) bf16 s_t[3][2 * BQ * D];
+  __shared__ __align__(1024) uint4 s_aux[3][BQ];
+  lds_nan_fill(s_t, sizeof s_t);
   const int G = p.Hq / p.Hk;
   const Tile tl = find_tile<BK>(tile_args(p, parts), blocks);
   if (!tl.valid) return;
@@ -513,16 +626,19 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dkv_bf16_kernel(AttnBwdArgs 
   const uint32_t lq2 = (uint32_t)p.ld_q * 2, lg2 = (uint32_t)p.Hq * D * 2;
 
   int head = w.at / w.each, tile = w.at - head * w.each;   // of the step to load
+  int now = tile;                                          // of the step at hand
   auto load_step = [&](int buf) {
     const int hq = hk * G + head, t0 = k0 + tile * BQ;
-    load_tile64<D>(static_cast<const bf16*>(p.q) + (tl.a + t0) * p.ld_q + hq * D, lq2, L - t0, s_q[buf], tid);
-    load_tile64<D>(static_cast<const bf16*>(p.d_o) + ((tl.a + t0) * p.Hq + hq) * (int64_t)D, lg2, L - t0, s_g[buf], tid);
+    load_tile64<D>(static_cast<const bf16*>(p.q) + (tl.a + t0) * p.ld_q + hq * D, lq2, L - t0, s_t[buf], tid);
+    load_tile64<D>(static_cast<const bf16*>(p.d_o) + ((tl.a + t0) * p.Hq + hq) * (int64_t)D, lg2, L - t0,
+                   s_t[buf] + BQ * D, tid);
     if (wave == 0)
       load_lds16(__builtin_amdgcn_readfirstlane(lds_address(s_aux[buf])), buffer_at(aux_of(p, hq) + tl.a + t0),
                  16u * (uint32_t)(lane < L - t0 ? lane : L - t0 - 1), 0);
     if (++tile == w.each) { tile = 0; ++head; }
   };
   if (w.at < w.stop) load_step(0);
+  if (w.at + 1 < w.stop) load_step(1);
   bf16x8 k[KB], v[KB];
   {
     const int64_t row = tl.a + (tk < L ? tk : L - 1);
@@ -536,67 +652,131 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dkv_bf16_kernel(AttnBwdArgs 
   }
   // lanes 0..31 supply the terms of m and l, 32..63 those of D
   const uint32_t one = 0x3f80;              // 1 in bf16
-  const uint32_t s1 = h == 0 ? one << 16 | one : 0, s2 = h == 0 ? one : 0;
-  const uint32_t d1 = h == 1 ? one << 16 | one : 0, d2 = h == 1 ? one : 0;
-  f32x16 dk[MT], dv[MT];
+  bf16x8 ones_s = __builtin_bit_cast(bf16x8, make_uint4(h == 0 ? one << 16 | one : 0, h == 0 ? one : 0, 0, 0));
+  bf16x8 ones_d = __builtin_bit_cast(bf16x8, make_uint4(h == 1 ? one << 16 | one : 0, h == 1 ? one : 0, 0, 0));
+  f32x16 zero, dk[MT], dv[MT];
 #pragma unroll
-  for (int c = 0; c < MT; ++c)
+  for (int r = 0; r < 16; ++r) zero[r] = 0.f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) dk[c][r] = dv[c][r] = 0.f;
+  for (int c = 0; c < MT; ++c) dk[c] = dv[c] = zero;
+  const LaneReads at = lane_reads<D>(lds_address(s_t), lane);
+  const uint32_t at_aux = lds_address(s_aux) + 16 * i32 + 8 * h;
 
-  int now = w.each > 0 ? w.at % w.each : 0;
-  for (int step = w.at; step < w.stop; ++step) {
-    const int buf = (step - w.at) & 1;
-    wait_tiles();
-    if (step + 1 < w.stop) load_step(buf ^ 1);
-    const int tt = k0 + now * BQ;
-    if (++now == w.each) now = 0;
-    if (u0 >= L) continue;
-#pragma unroll
-    for (int sub = 0; sub < BQ; sub += 32) {
-      const int t0 = tt + sub;
-      if (t0 + 31 < u0 || t0 >= L || (window && t0 - window >= u0 + 31)) continue;   // no pair
-      f32x16 s, dp;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
-      {
-        const uint2 a = reinterpret_cast<const uint2*>(&s_aux[buf][sub + i32])[h];
-        const bf16x8 x = __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, 0, 0));
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, __builtin_bit_cast(bf16x8, make_uint4(s1, s2, 0, 0)), s, 0, 0, 0);
-        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, __builtin_bit_cast(bf16x8, make_uint4(d1, d2, 0, 0)), dp, 0, 0, 0);
-      }
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_rows<D>(s_q[buf], sub, kb, lane), k[kb], s, 0, 0, 0);
-        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_rows<D>(s_g[buf], sub, kb, lane), v[kb], dp, 0, 0, 0);
-      }
-      if (t0 < u0 + 31 || t0 + 31 >= L || (window && t0 + 31 - window >= u0)) {
-        // element r is query t0 + 4 h + at: seen where it is at the key or behind it,
-        // before the end, and less than the window behind it
-        const int first = tk - t0 - 4 * h;
-        int end = L - t0 - 4 * h;
-        if (window && first + window < end) end = first + window;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int at = 8 * (r / 4) + r % 4;
-          if (at < first || at >= end) s[r] = -__builtin_huge_valf() * c_scale;
-        }
-      }
-      bf16x8 pw[2], dw[2];
+  auto statistics = [&](uint32_t block) {   // of a block of 32 queries, at BUF-relative byte `block`
+    const uint2 a = lds_read<uint2>(at_aux + block);
+    return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, 0, 0));
+  };
+  constexpr int NF = 2 * KB, NS = 4 * MT;   // first and second products of a block
+  constexpr int AF = 4, AS = 4;             // reads ahead
+  constexpr int EW = 16 / NF;               // weights to a first product
+  // A block's statistics and the rows of its first AF products, read ahead of it.
+  bf16x8 x, ahead[AF];
+  auto read_first = [&](uint32_t block, int i) { return rows_at<D>(at.rows + block, i / 2, i % 2 ? GO : 0); };
+
+  // One block: its scores are in s and dp; leaves those of the block at `next` in sn, dpn,
+  // and reads ahead of the one at `after`.
+  auto step = [&](uint32_t cur, int t0, uint32_t next, uint32_t after, uint32_t after_aux, f32x16& s, f32x16& dp,
+                  f32x16& sn, f32x16& dpn) {
+    if (t0 < u0 + 31 || t0 + 31 >= L || (window && t0 + 31 - window >= u0)) {
+      // element r is query t0 + 4 h + at: seen where it is at the key or behind it,
+      // before the end, and less than the window behind it
+      const int first = tk - t0 - 4 * h;
+      int end = L - t0 - 4 * h;
+      if (window && first + window < end) end = first + window;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float pr = exp2_fast(s[r] * c_scale);
-        pw[r / 8][r % 8] = (bf16)pr;
-        dw[r / 8][r % 8] = (bf16)(pr * dp[r]);
+        const int e = 8 * (r / 4) + r % 4;
+        if (e < first || e >= end) s[r] = -__builtin_huge_valf() * c_scale;
       }
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int c = 0; c < MT; ++c) {
-          dv[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_columns<D>(s_g[buf], sub + 16 * b, c, lane), pw[b], dv[c], 0, 0, 0);
-          dk[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_columns<D>(s_q[buf], sub + 16 * b, c, lane), dw[b], dk[c], 0, 0, 0);
-        }
     }
+    const uint32_t cols = at.cols + cur;
+    bf16x8 f[NF], g[NS], pw[2], dw[2];
+    auto read_second = [&](int j) { g[j] = columns_at<D>(cols, j / (2 * MT), j / 2 % MT, j % 2 ? 0 : GO); };
+#pragma unroll
+    for (int i = 0; i < AF; ++i) f[i] = ahead[i];
+    __builtin_amdgcn_sched_barrier(0);
+    settle(x);
+    product_v0(sn, x, ones_s);
+    product_v0(dpn, x, ones_d);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + AF < NF) f[i + AF] = read_first(next, i + AF);
+      if (i >= NF - AS) read_second(i - (NF - AS));
+      if (i % 2 == 0) product_v(sn, f[i], k[i / 2]);
+      else product_v(dpn, f[i], v[i / 2]);
+#pragma unroll
+      for (int e = EW * i; e < EW * i + EW; ++e) {
+        const float pr = exp2_fast(s[e] * c_scale);
+        pw[e / 8][e % 8] = (bf16)pr;
+        dw[e / 8][e % 8] = (bf16)(pr * dp[e]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) { settle(pw[b]); settle(dw[b]); }
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (j + AS < NS) read_second(j + AS);
+      else if (j + AS - NS < AF) ahead[j + AS - NS] = read_first(after, j + AS - NS);
+      if (j == NS - 1) x = statistics(after_aux);
+      const int b = j / (2 * MT), c = j / 2 % MT;
+      if (j % 2 == 0) product_a(dv[c], g[j], pw[b]);
+      else product_a(dk[c], g[j], dw[b]);
+    }
+    static_assert(AS >= AF && NS >= 8, "every read has its line; products behind the scores");
+    __builtin_amdgcn_sched_barrier(0);
+    behind_v(sn);
+    behind_v(dpn);
+  };
+
+  f32x16 s, dp, s1, dp1;
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    keep_a(k[kb]);
+    keep_a(v[kb]);
+  }
+  keep_a(ones_s);
+  keep_a(ones_d);
+  wait_tiles();
+  int buf = 0;
+  auto next_buf = [](int i) { return i == 2 ? 0 : i + 1; };
+  auto next_tile = [&](int i) {             // the next tile is there, and the last one free
+    wait_tiles();
+    if (i + 2 < w.stop) load_step(next_buf(next_buf(buf)));
+  };
+  if (u0 >= L) {                            // no key: this wave's share of the loads is all it does
+    for (int i = w.at; i < w.stop; ++i) {
+      next_tile(i);
+      buf = next_buf(buf);
+    }
+    return;
+  }
+  constexpr uint32_t HALF = 64 * D, HALF_AUX = 512;   // the second block of a buffer
+  {
+    x = statistics(0);
+    settle(x);
+    product_v0(s, x, ones_s);
+    product_v0(dp, x, ones_d);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      if (i % 2 == 0) product_v(s, read_first(0, i), k[i / 2]);
+      else product_v(dp, read_first(0, i), v[i / 2]);
+    }
+    products_done(s, dp);
+    x = statistics(HALF_AUX);
+#pragma unroll
+    for (int i = 0; i < AF; ++i) ahead[i] = read_first(HALF, i);
+  }
+  for (int i = w.at; i < w.stop; ++i) {
+    next_tile(i);
+    const int t0 = k0 + now * BQ, nb = next_buf(buf);
+    if (++now == w.each) now = 0;
+    const uint32_t cur = buf * BUF, then = nb * BUF, then_aux = nb * (BQ * 16);
+    step(cur, t0, cur + HALF, then, then_aux, s, dp, s1, dp1);
+    step(cur + HALF, t0 + 32, then, then + HALF, then_aux + HALF_AUX, s1, dp1, s, dp);
+    products_done<MT>(dk, dv);
+    buf = nb;
   }
   if (tk >= L) return;
   if (parts == 1) {
