@@ -378,6 +378,31 @@ __device__ __forceinline__ uint2 three_terms(float x) {
   return __builtin_bit_cast(uint2, t);
 }
 
+// 32 rows of a wave, row i32 in the lanes i32 and 32 + i32 as the products leave it, times
+// f to memory by way of 64 D bytes (fp32: 128 D) of LDS of its own.
+template <int D, typename TG>
+__device__ __forceinline__ void rows_out(bf16* lds, const f32x16* acc, float f, TG* to, int64_t ld, int rows, int lane) {
+  constexpr int N = 16 / sizeof(TG), CH = D / N;      // elements of a chunk, chunks of a row
+  TG* so = reinterpret_cast<TG*>(lds);
+  const int h = lane >> 5, i32 = lane & 31;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const int at = 32 * c + 2 * r + 4 * h;
+      TG* dst = so + i32 * D + N * ((at / N) ^ (i32 & 7)) + at % N;
+      lds_check(dst, 4 * sizeof(TG));
+      store4<TG>(dst, acc[c][r] * f, acc[c][r + 1] * f, acc[c][r + 2] * f, acc[c][r + 3] * f);
+    }
+#pragma unroll
+  for (int e = 0; e < 32 * CH / 64; ++e) {
+    const int row = (e * 64 + lane) / CH, c = (e * 64 + lane) % CH;
+    const TG* src = so + row * D + N * (c ^ (row & 7));
+    lds_check(src, 16);
+    if (row < rows) *reinterpret_cast<uint4*>(to + row * ld + N * c) = *reinterpret_cast<const uint4*>(src);
+  }
+}
+
 template <int D, typename TG>
 __global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p, uint32_t blocks) {
   constexpr int BM = 128, BN = 64, KB = D / 16, MT = D / 32;
@@ -475,13 +500,11 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p
           dq[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_columns<D>(s_k[buf], sub + 16 * b, c, lane), ds[b], dq[c], 0, 0, 0);
     }
   }
-  if (tq >= L) return;
-  TG* to = static_cast<TG*>(p.dq) + (tl.a + tq) * p.ld_dq + tl.hq * D + 4 * h;
-#pragma unroll
-  for (int c = 0; c < MT; ++c)
-#pragma unroll
-    for (int r = 0; r < 16; r += 4)
-      store4<TG>(to + 32 * c + 2 * r, dq[c][r] * p.scale, dq[c][r + 1] * p.scale, dq[c][r + 2] * p.scale, dq[c][r + 3] * p.scale);
+  wait_tiles();                             // the key tiles are free
+  if (q0 >= L) return;
+  static_assert(sizeof s_k + sizeof s_v >= 128 * D * sizeof(TG), "the rows fit");
+  bf16* mine = (wave < 2 ? s_k[0] : s_v[0]) + (wave & 1) * BN * D;
+  rows_out<D>(mine, dq, p.scale, static_cast<TG*>(p.dq) + (tl.a + q0) * p.ld_dq + tl.hq * D, p.ld_dq, L - q0, lane);
 }
 
 // Where a lane reads from a tile in LDS.  Rows: row i32, its 16-byte chunk 2 kb + h, is
@@ -606,8 +629,10 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
   constexpr int BK = 128, BQ = 64, KB = D / 16, MT = D / 32;
   constexpr int GO = BQ * D * 2;            // d_o behind q in a buffer
   constexpr int BUF = 2 * GO;
-  __shared__ __align__(1024) bf16 s_t[3][2 * BQ * D];
-  __shared__ __align__(1024) uint4 s_aux[3][BQ];
+  constexpr int NB = 4;                     // buffers
+  constexpr int LOADS = 2 * BQ * D / 8 / kThreads + 1;   // of a wave and tile
+  __shared__ __align__(1024) bf16 s_t[NB][2 * BQ * D];
+  __shared__ __align__(1024) uint4 s_aux[NB][BQ];
   lds_nan_fill(s_t, sizeof s_t);
   const int G = p.Hq / p.Hk;
   const Tile tl = find_tile<BK>(tile_args(p, parts), blocks);
@@ -632,13 +657,16 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
     load_tile64<D>(static_cast<const bf16*>(p.q) + (tl.a + t0) * p.ld_q + hq * D, lq2, L - t0, s_t[buf], tid);
     load_tile64<D>(static_cast<const bf16*>(p.d_o) + ((tl.a + t0) * p.Hq + hq) * (int64_t)D, lg2, L - t0,
                    s_t[buf] + BQ * D, tid);
-    if (wave == 0)
-      load_lds16(__builtin_amdgcn_readfirstlane(lds_address(s_aux[buf])), buffer_at(aux_of(p, hq) + tl.a + t0),
-                 16u * (uint32_t)(lane < L - t0 ? lane : L - t0 - 1), 0);
+    if (lane < BQ / 4) {                    // a quarter of the statistics to a wave
+      const int r = BQ / 4 * wave + lane;
+      load_lds16(__builtin_amdgcn_readfirstlane(lds_address(s_aux[buf]) + BQ * 4 * wave),
+                 buffer_at(aux_of(p, hq) + tl.a + t0), 16u * (uint32_t)(r < L - t0 ? r : L - t0 - 1), 0);
+    }
     if (++tile == w.each) { tile = 0; ++head; }
   };
-  if (w.at < w.stop) load_step(0);
-  if (w.at + 1 < w.stop) load_step(1);
+#pragma unroll
+  for (int i = 0; i < NB - 1; ++i)
+    if (w.at + i < w.stop) load_step(i);
   bf16x8 k[KB], v[KB];
   {
     const int64_t row = tl.a + (tk < L ? tk : L - 1);
@@ -668,7 +696,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
   };
   constexpr int NF = 2 * KB, NS = 4 * MT;   // first and second products of a block
   constexpr int AF = 4, AS = 4;             // reads ahead
-  constexpr int EW = 16 / NF;               // weights to a first product
+  constexpr int E1 = 10;                    // weights formed between first products; the others behind them
   // A block's statistics and the rows of its first AF products, read ahead of it.
   bf16x8 x, ahead[AF];
   auto read_first = [&](uint32_t block, int i) { return rows_at<D>(at.rows + block, i / 2, i % 2 ? GO : 0); };
@@ -692,6 +720,14 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
     const uint32_t cols = at.cols + cur;
     bf16x8 f[NF], g[NS], pw[2], dw[2];
     auto read_second = [&](int j) { g[j] = columns_at<D>(cols, j / (2 * MT), j / 2 % MT, j % 2 ? 0 : GO); };
+    auto weights = [&](int from, int to) {
+#pragma unroll
+      for (int e = from; e < to; ++e) {
+        const float pr = exp2_fast(s[e] * c_scale);
+        pw[e / 8][e % 8] = (bf16)pr;
+        dw[e / 8][e % 8] = (bf16)(pr * dp[e]);
+      }
+    };
 #pragma unroll
     for (int i = 0; i < AF; ++i) f[i] = ahead[i];
     __builtin_amdgcn_sched_barrier(0);
@@ -701,28 +737,38 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
       __builtin_amdgcn_sched_barrier(0);
-      if (i + AF < NF) f[i + AF] = read_first(next, i + AF);
-      if (i >= NF - AS) read_second(i - (NF - AS));
+      if (i % 2 == 0) {
+#pragma unroll
+        for (int n = i; n < i + 2; ++n) {
+          if (n + AF < NF) f[n + AF] = read_first(next, n + AF);
+          if (n >= NF - AS) read_second(n - (NF - AS));
+        }
+      }
       if (i % 2 == 0) product_v(sn, f[i], k[i / 2]);
       else product_v(dpn, f[i], v[i / 2]);
-#pragma unroll
-      for (int e = EW * i; e < EW * i + EW; ++e) {
-        const float pr = exp2_fast(s[e] * c_scale);
-        pw[e / 8][e % 8] = (bf16)pr;
-        dw[e / 8][e % 8] = (bf16)(pr * dp[e]);
-      }
+      weights(E1 * i / NF, E1 * (i + 1) / NF);
     }
-#pragma unroll
-    for (int b = 0; b < 2; ++b) { settle(pw[b]); settle(dw[b]); }
+    settle(pw[0]);
+    settle(dw[0]);
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
       __builtin_amdgcn_sched_barrier(0);
-      if (j + AS < NS) read_second(j + AS);
-      else if (j + AS - NS < AF) ahead[j + AS - NS] = read_first(after, j + AS - NS);
+      if (j % 2 == 0) {
+#pragma unroll
+        for (int n = j; n < j + 2; ++n) {
+          if (n + AS < NS) read_second(n + AS);
+          else if (n + AS - NS < AF) ahead[n + AS - NS] = read_first(after, n + AS - NS);
+        }
+      }
+      if (j == NS / 2) {
+        settle(pw[1]);
+        settle(dw[1]);
+      }
       if (j == NS - 1) x = statistics(after_aux);
       const int b = j / (2 * MT), c = j / 2 % MT;
       if (j % 2 == 0) product_a(dv[c], g[j], pw[b]);
       else product_a(dk[c], g[j], dw[b]);
+      if (j < NS / 2) weights(E1 + (16 - E1) * j / (NS / 2), E1 + (16 - E1) * (j + 1) / (NS / 2));
     }
     static_assert(AS >= AF && NS >= 8, "every read has its line; products behind the scores");
     __builtin_amdgcn_sched_barrier(0);
@@ -740,10 +786,12 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
   keep_a(ones_d);
   wait_tiles();
   int buf = 0;
-  auto next_buf = [](int i) { return i == 2 ? 0 : i + 1; };
-  auto next_tile = [&](int i) {             // the next tile is there, and the last one free
-    wait_tiles();
-    if (i + 2 < w.stop) load_step(next_buf(next_buf(buf)));
+  auto next_buf = [](int i) { return (i + 1) % NB; };
+  // The next tile is there, with the one behind it perhaps still on its way, and the last one free.
+  auto next_tile = [&](int i) {
+    if (i + 2 < w.stop) wait_tiles_but<LOADS>();
+    else wait_tiles();
+    if (i + NB - 1 < w.stop) load_step((buf + NB - 1) % NB);
   };
   if (u0 >= L) {                            // no key: this wave's share of the loads is all it does
     for (int i = w.at; i < w.stop; ++i) {
@@ -778,26 +826,18 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
     products_done<MT>(dk, dv);
     buf = nb;
   }
-  if (tk >= L) return;
+  // Rows leave through LDS, so that a store covers whole rows.  The last two buffers but
+  // one are read by no wave any more: a quarter of them to a wave.
+  bf16* mine = s_t[(buf + 1 + (wave >> 1)) % NB] + (wave & 1) * BQ * D;
+  const int64_t row0 = tl.a + u0;
+  const int rows = L - u0 < 32 ? L - u0 : 32;
   if (parts == 1) {
-    TG* tok = static_cast<TG*>(p.dk) + (tl.a + tk) * p.ld_dk + hk * D + 4 * h;
-    TG* tov = static_cast<TG*>(p.dv) + (tl.a + tk) * p.ld_dv + hk * D + 4 * h;
-#pragma unroll
-    for (int c = 0; c < MT; ++c)
-#pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        store4<TG>(tok + 32 * c + 2 * r, dk[c][r] * p.scale, dk[c][r + 1] * p.scale, dk[c][r + 2] * p.scale, dk[c][r + 3] * p.scale);
-        store4<TG>(tov + 32 * c + 2 * r, dv[c][r], dv[c][r + 1], dv[c][r + 2], dv[c][r + 3]);
-      }
+    rows_out<D>(mine, dk, p.scale, static_cast<TG*>(p.dk) + row0 * p.ld_dk + hk * D, p.ld_dk, rows, lane);
+    rows_out<D>(mine, dv, 1.f, static_cast<TG*>(p.dv) + row0 * p.ld_dv + hk * D, p.ld_dv, rows, lane);
   } else {
-    float* tok = parts_of(p) + ((part * p.total_T + tl.a + tk) * p.Hk + hk) * (2 * D) + 4 * h;
-#pragma unroll
-    for (int c = 0; c < MT; ++c)
-#pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        store4<float>(tok + 32 * c + 2 * r, dk[c][r] * p.scale, dk[c][r + 1] * p.scale, dk[c][r + 2] * p.scale, dk[c][r + 3] * p.scale);
-        store4<float>(tok + D + 32 * c + 2 * r, dv[c][r], dv[c][r + 1], dv[c][r + 2], dv[c][r + 3]);
-      }
+    float* to = parts_of(p) + ((part * p.total_T + row0) * p.Hk + hk) * (2 * D);
+    rows_out<D>(mine, dk, p.scale, to, (int64_t)p.Hk * (2 * D), rows, lane);
+    rows_out<D>(mine, dv, 1.f, to + D, (int64_t)p.Hk * (2 * D), rows, lane);
   }
 }
 

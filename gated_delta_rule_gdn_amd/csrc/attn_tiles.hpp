@@ -138,6 +138,13 @@ __device__ __forceinline__ void wait_tiles() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #endif
 }
+// The same, but for this wave's last N loads.
+template <int N>
+__device__ __forceinline__ void wait_tiles_but() {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+#endif
+}
 __device__ __forceinline__ i32x4 buffer_at(const void* p) {
   const uint64_t u = reinterpret_cast<uint64_t>(p);
   i32x4 r;
