@@ -841,64 +841,79 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
   }
 }
 
-// The parts of dk and dv added in order: a wave to a row of a tile and head.
-template <typename TG, int D, int BK>
-__global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(AttnBwdArgs p, uint32_t blocks, int parts) {
-  const Tile tl = find_tile<BK>(tile_args(p, 1), blocks);
-  if (!tl.valid) return;
-  constexpr int LR = 2 * D / 4;             // lanes of a row of dk and dv
-  const int k0 = key_tile_start<BK>(tl), c = 4 * (threadIdx.x % LR);
-  for (int r = threadIdx.x / LR; r < BK && k0 + r < tl.L; r += kThreads / LR) {
-    const int64_t row = tl.a + k0 + r;
-    const float* src = parts_of(p) + (row * p.Hk + tl.hq) * (2 * D) + c;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < parts; ++i) {
-      const float4 u = *reinterpret_cast<const float4*>(src + i * p.total_T * p.Hk * (2 * D));
-      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-    }
-    if (c < D) store4<TG>(static_cast<TG*>(p.dk) + row * p.ld_dk + tl.hq * D + c, v.x, v.y, v.z, v.w);
-    else store4<TG>(static_cast<TG*>(p.dv) + row * p.ld_dv + tl.hq * D + c - D, v.x, v.y, v.z, v.w);
+// The parts of dk and dv added in order, 4 elements to a thread.  Well-formed offsets cover
+// the rows from their first to their last; the others are kept.
+template <typename TG, int D>
+__global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(AttnBwdArgs p, int parts) {
+  constexpr int LR = 2 * D / 4;             // threads of a row of dk and dv
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, x = i / LR;
+  const int64_t row = x / p.Hk;
+  const int hk = (int)(x - row * p.Hk), c = 4 * (int)(i - x * LR);
+  if (row >= p.total_T) return;
+  if (p.cu_seqlens && (row < clamp_i64(p.cu_seqlens[0], 0, p.total_T) ||
+                       row >= clamp_i64(p.cu_seqlens[p.N], 0, p.total_T)))
+    return;
+  const float* src = parts_of(p) + x * (2 * D) + c;
+  const int64_t step = p.total_T * p.Hk * (2 * D);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int n = 0; n < parts; ++n) {
+    const float4 u = *reinterpret_cast<const float4*>(src + n * step);
+    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
   }
+  if (c < D) store4<TG>(static_cast<TG*>(p.dk) + row * p.ld_dk + hk * D + c, v.x, v.y, v.z, v.w);
+  else store4<TG>(static_cast<TG*>(p.dv) + row * p.ld_dv + hk * D + c - D, v.x, v.y, v.z, v.w);
 }
 
 int64_t tiles_of(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int64_t rows) {
   return packed ? total_T / rows + N : N * ((Tseq + rows - 1) / rows);
 }
 
+int64_t join_blocks(int64_t total_T, int Hk, int d) { return (total_T * Hk * (d / 2) + kThreads - 1) / kThreads; }
+template <typename TG, int D>
+hipError_t launch_join(const AttnBwdArgs& a, int parts, hipStream_t stream) {
+  attn_dkv_join_kernel<TG, D><<<dim3((unsigned)join_blocks(a.total_T, a.Hk, D)), kThreads, 0, stream>>>(a, parts);
+  return hipGetLastError();
+}
+
 template <typename TG, int D>
 hipError_t launch_bf16(const AttnBwdArgs& a, int parts, hipStream_t stream) {
   const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, 128);
-  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = (uint32_t)(tiles * a.Hk * parts), nj = (uint32_t)(tiles * a.Hk);
+  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = (uint32_t)(tiles * a.Hk * parts);
   attn_dq_bf16_kernel<D, TG><<<dim3(nq), kThreads, 0, stream>>>(a, nq);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   attn_dkv_bf16_kernel<D, TG><<<dim3(nk), kThreads, 0, stream>>>(a, nk, parts);
   e = hipGetLastError();
   if (e != hipSuccess || parts == 1) return e;
-  attn_dkv_join_kernel<TG, D, 128><<<dim3(nj), kThreads, 0, stream>>>(a, nj, parts);
-  return hipGetLastError();
+  return launch_join<TG, D>(a, parts, stream);
 }
 template <int D>
 hipError_t launch_f32(const AttnBwdArgs& a, int parts, hipStream_t stream) {
   const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, 32);
-  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = (uint32_t)(tiles * a.Hk * parts), nj = (uint32_t)(tiles * a.Hk);
+  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = (uint32_t)(tiles * a.Hk * parts);
   attn_dq_f32_kernel<D><<<dim3(nq), kThreads, 0, stream>>>(a, nq);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   attn_dkv_f32_kernel<D><<<dim3(nk), kThreads, 0, stream>>>(a, nk, parts);
   e = hipGetLastError();
   if (e != hipSuccess || parts == 1) return e;
-  attn_dkv_join_kernel<float, D, 32><<<dim3(nj), kThreads, 0, stream>>>(a, nj, parts);
-  return hipGetLastError();
+  return launch_join<float, D>(a, parts, stream);
 }
 
 }  // namespace
 
+// A key tile is walked by several workgroups where there are few tiles: 1024 workgroups
+// keep the CUs evenly busy to the end, but each part's fp32 sums go through memory, and a
+// workgroup takes as long as some 4 steps before and behind its walk, so not below 8
+// steps to a part.
 AttnBwdPlan attn_bwd_plan(int64_t N, int64_t total_T, int64_t window, int Hq, int Hk, int d, DType io) {
-  const int64_t tiles = (total_T + (io == DType::F32 ? 31 : 127)) / (io == DType::F32 ? 32 : 128) * Hk;
-  int64_t parts = tiles > 0 ? 2048 / tiles : 1;
-  const int64_t most = Hq / Hk * 2;
-  parts = parts < most ? parts : most;
+  const int64_t rows = io == DType::F32 ? 32 : 128, step = io == DType::F32 ? 32 : 64;
+  const int64_t len = N > 0 ? total_T / N : 0;
+  const int64_t tiles = total_T / rows + N, seen = window > 0 && window < len ? 2 * window : len;
+  const int64_t steps = (seen / (2 * step) + 1) * (Hq / Hk);          // of a tile, about
+  int64_t parts = (1024 + tiles * Hk - 1) / (tiles * Hk);
+  if (parts > steps / 8) parts = steps / 8;
   if (parts < 1) parts = 1;
   AttnBwdPlan r;
   r.parts = (int)parts;
@@ -906,10 +921,13 @@ AttnBwdPlan attn_bwd_plan(int64_t N, int64_t total_T, int64_t window, int Hq, in
   return r;
 }
 
-int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, int Hk, int parts, DType io) {
+int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, int Hk, int d,
+                        int parts, DType io) {
   const int64_t tiles = tiles_of(N, total_T, Tseq, packed, io == DType::F32 ? 32 : 128);
-  const int64_t a = tiles * Hq, b = tiles * Hk * parts;
-  return a > b ? a : b;
+  int64_t most = tiles * Hq;
+  if (most < tiles * Hk * parts) most = tiles * Hk * parts;
+  if (parts > 1 && most < join_blocks(total_T, Hk, d)) most = join_blocks(total_T, Hk, d);
+  return most;
 }
 
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, const AttnBwdPlan& plan, hipStream_t stream) {

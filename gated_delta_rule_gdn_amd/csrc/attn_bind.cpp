@@ -10,6 +10,7 @@
 // what cannot be marshalled raises ValueError.
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
@@ -391,7 +392,42 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (fn, q, k, v, cu_seqlens, N, window, scale, o, stats, stream)
+// Outputs and workspaces that are not given are allocated here, for the current stream of
+// the device: from Python that costs as much again as the rest of a call.
+Tensor make(int dev, at::IntArrayRef shape, ScalarType type) {
+  return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)dev)));
+}
+// A contiguous output: the one given, or a new one in `made`.
+void* out_dense(PyObject* o, const char* name, int dev, at::IntArrayRef shape, ScalarType type, Tensor* made) {
+  if (o != Py_None) return dense(o, name, dev, shape, type);
+  *made = make(dev, shape, type);
+  return made->data_ptr();
+}
+void* out_heads(PyObject* o, const char* name, int dev, int64_t rows, int64_t H, int64_t d, ScalarType type,
+                int64_t* ld, Tensor* made) {
+  if (o != Py_None) return heads(o, name, dev, rows, H, d, type, ld);
+  *made = make(dev, {rows, H, d}, type);
+  *ld = H * d;
+  return made->data_ptr();
+}
+// A new reference to what stands for an output: given, made or None.
+PyObject* given_or(PyObject* o, const Tensor& made) {
+  if (made.defined()) return THPVariable_Wrap(made);
+  Py_INCREF(o);
+  return o;
+}
+// (status, outputs ...)
+template <size_t N>
+PyObject* answer(PyObject* status, PyObject* const (&given)[N], const Tensor (&made)[N]) {
+  if (!status) return nullptr;
+  PyObject* r = PyTuple_New(N + 1);
+  if (!r) { Py_DECREF(status); return nullptr; }
+  PyTuple_SET_ITEM(r, 0, status);
+  for (size_t i = 0; i < N; ++i) PyTuple_SET_ITEM(r, i + 1, given_or(given[i], made[i]));
+  return r;
+}
+
+// (fn, q, k, v, cu_seqlens, N, window, scale, o, stats, stream) -> (status, o, stats)
 PyObject* attn_prefill_save(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&]() -> PyObject* {
     const Tensor& q = first(a[1], "q");
@@ -411,28 +447,32 @@ PyObject* attn_prefill_save(PyObject*, PyObject* const* a, Py_ssize_t n) {
     desc.N = packed(a[4], a[5], dev, &cu);
     desc.window = integer(a[6], "window");
     desc.scale = scale_of(a[7], d);
-    void* o = dense(a[8], "o", dev, {T, desc.H_q, d}, io);
-    void* stats = dense(a[9], "stats", dev, {T, desc.H_q, 2}, ScalarType::Float);
+    Tensor made[2];
+    void* o = out_dense(a[8], "o", dev, {T, desc.H_q, d}, io, &made[0]);
+    void* stats = out_dense(a[9], "stats", dev, {T, desc.H_q, 2}, ScalarType::Float, &made[1]);
     const auto fn = function<decltype(&gdn_attn_prefill_save)>(a[0]);
     void* stream = handle(a[10]);
-    return on_device(dev, [&] {
+    PyObject* const given[2] = {a[8], a[9]};
+    return answer(on_device(dev, [&] {
       return fn(&desc, cu, q_in, k_in, v_in, o, static_cast<float*>(stats), stream);
-    });
+    }), given, made);
   });
 }
 
-// The workspace's address and bytes where `need` is not 0; false: it is not given.
-bool workspace_of(PyObject* o, int dev, size_t need, void** ws, size_t* bytes) {
-  *ws = nullptr;
+// The workspace's address and bytes where `need` is not 0.
+void* workspace_of(PyObject* o, int dev, size_t need, size_t* bytes, Tensor* made) {
   *bytes = 0;
-  if (!need) return true;
-  if (o == Py_None) return false;
+  if (!need) return nullptr;
+  if (o == Py_None) {
+    *made = make(dev, {(int64_t)need}, ScalarType::Byte);
+    *bytes = need;
+    return made->data_ptr();
+  }
   const Tensor& t = tensor(o, "workspace");
   if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
     throw Refused("workspace must be a contiguous tensor on the device of the others");
-  *ws = t.data_ptr();
   *bytes = t.nbytes();
-  return true;
+  return t.data_ptr();
 }
 
 // The type of an operand that may be fp32 beside bf16.
@@ -443,10 +483,10 @@ ScalarType second_type(const Tensor& t, const char* name) {
   return s;
 }
 
-// (fn, size_fn, q, k, v, o, d_o, stats, cu_seqlens, N, window, scale, dq, dk, dv, workspace, stream); a workspace
-// that is needed and not given: minus its bytes
+// (fn, size_fn, q, k, v, o, d_o, stats, cu_seqlens, N, window, scale, dq, dk, dv, grad_dtype is float32, workspace,
+//  stream) -> (status, dq, dk, dv)
 PyObject* attn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 17, [&]() -> PyObject* {
+  return guarded(n, 18, [&]() -> PyObject* {
     const Tensor& q = first(a[2], "q");
     const int dev = (int)q.get_device();
     const ScalarType io = q.scalar_type();
@@ -467,26 +507,27 @@ PyObject* attn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     desc.N = packed(a[8], a[9], dev, &cu);
     desc.window = integer(a[10], "window");
     desc.scale = scale_of(a[11], d);
-    const ScalarType grad = second_type(tensor(a[12], "dq"), "dq");
+    const ScalarType grad = truth(a[15], "grad_dtype") ? ScalarType::Float : ScalarType::BFloat16;
     desc.grad_dtype = io_of(grad);
-    void* dq = heads(a[12], "dq", dev, T, desc.H_q, d, grad, &desc.ld_dq);
-    void* dk = heads(a[13], "dk", dev, T, desc.H_k, d, grad, &desc.ld_dk);
-    void* dv = heads(a[14], "dv", dev, T, desc.H_k, d, grad, &desc.ld_dv);
+    Tensor made[3], scratch;
+    void* dq = out_heads(a[12], "dq", dev, T, desc.H_q, d, grad, &desc.ld_dq, &made[0]);
+    void* dk = out_heads(a[13], "dk", dev, T, desc.H_k, d, grad, &desc.ld_dk, &made[1]);
+    void* dv = out_heads(a[14], "dv", dev, T, desc.H_k, d, grad, &desc.ld_dv, &made[2]);
     const size_t need = function<decltype(&gdn_attn_backward_workspace_size)>(a[1])(&desc);
-    void* ws;
     size_t bytes;
-    if (!workspace_of(a[15], dev, need, &ws, &bytes)) return PyLong_FromLongLong(-(long long)need);
+    void* ws = workspace_of(a[16], dev, need, &bytes, &scratch);
     const auto fn = function<decltype(&gdn_attn_backward)>(a[0]);
-    void* stream = handle(a[16]);
-    return on_device(dev, [&] {
+    void* stream = handle(a[17]);
+    PyObject* const given[3] = {a[12], a[13], a[14]};
+    return answer(on_device(dev, [&] {
       return fn(&desc, cu, q_in, k_in, v_in, o, d_o, static_cast<const float*>(stats), ws, bytes,
                 dq, dk, dv, stream);
-    });
+    }), given, made);
   });
 }
 
 // (fn, size_fn, dq, dk, q_raw, k_raw, positions, inv_freq, q_weight, k_weight, interleaved, rope_scale, eps, dq_raw,
-//  dk_raw, dq_weight, dk_weight, workspace, stream); a workspace that is needed and not given: minus its bytes
+//  dk_raw, dq_weight, dk_weight, workspace, stream) -> (status, dq_raw, dk_raw, dq_weight, dk_weight)
 PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 19, [&]() -> PyObject* {
     const bool has_q = a[2] != Py_None, has_k = a[3] != Py_None;
@@ -507,6 +548,7 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* raw[2] = {nullptr, nullptr};
     void* out[2] = {nullptr, nullptr};
     const char* names[2][3] = {{"dq", "q_raw", "dq_raw"}, {"dk", "k_raw", "dk_raw"}};
+    Tensor made[4], scratch;
     for (int i = 0; i < 2; ++i) {
       int32_t& H = i ? desc.H_k : desc.H_q;
       int64_t &ld = i ? desc.ld_k : desc.ld_q, &ldo = i ? desc.ld_dk : desc.ld_dq;
@@ -519,7 +561,7 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       up[i] = dense(a[2 + i], names[i][0], dev, {rows, H, d}, grad);
       ld = (int64_t)H * d;
       if (a[4 + i] != Py_None) raw[i] = heads(a[4 + i], names[i][1], dev, rows, H, d, io, &ld);
-      out[i] = heads(a[13 + i], names[i][2], dev, rows, H, d, grad, &ldo);
+      out[i] = out_heads(a[13 + i], names[i][2], dev, rows, H, d, grad, &ldo, &made[i]);
     }
     if (a[7] != Py_None && a[6] == Py_None) throw Refused("rotation needs positions");
     const float* freqs;
@@ -530,21 +572,23 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     desc.rope_mode = truth(a[10], "interleaved") ? GDN_ROPE_INTERLEAVED : GDN_ROPE_HALF;
     desc.rope_scale = (float)number(a[11], "rope_scale");
     desc.eps = (float)number(a[12], "eps");
-    void* dqw = dense(a[15], "dq_weight", dev, {d}, ScalarType::Float);
-    void* dkw = dense(a[16], "dk_weight", dev, {d}, ScalarType::Float);
+    void* dqw = qw ? out_dense(a[15], "dq_weight", dev, {d}, ScalarType::Float, &made[2])
+                   : dense(a[15], "dq_weight", dev, {d}, ScalarType::Float);
+    void* dkw = kw ? out_dense(a[16], "dk_weight", dev, {d}, ScalarType::Float, &made[3])
+                   : dense(a[16], "dk_weight", dev, {d}, ScalarType::Float);
     const size_t need = dqw || dkw
         ? function<decltype(&gdn_qk_norm_rope_backward_workspace_size)>(a[1])(&desc) : 0;
-    void* ws;
     size_t bytes;
-    if (!workspace_of(a[17], dev, need, &ws, &bytes)) return PyLong_FromLongLong(-(long long)need);
+    void* ws = workspace_of(a[17], dev, need, &bytes, &scratch);
     const auto fn = function<decltype(&gdn_qk_norm_rope_backward)>(a[0]);
     void* stream = handle(a[18]);
-    return on_device(dev, [&] {
+    PyObject* const given[4] = {a[13], a[14], a[15], a[16]};
+    return answer(on_device(dev, [&] {
       return fn(&desc, up[0], up[1], raw[0], raw[1], static_cast<const float*>(qw),
                 static_cast<const float*>(kw),
                 desc.rope_dim ? static_cast<const int64_t*>(pos) : nullptr, freqs, ws, bytes, out[0],
                 out[1], static_cast<float*>(dqw), static_cast<float*>(dkw), stream);
-    });
+    }), given, made);
   });
 }
 
@@ -565,7 +609,7 @@ const Tensor& first_rows(PyObject* o, const char* name) {
   return t;
 }
 
-// (fn, x, res, weight, eps, group (None: y like x), res_out, y, y_scale, stream)
+// (fn, x, res, weight, eps, group (None: y like x), res_out, y, y_scale, stream) -> (status, y, y_scale, res_out)
 PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject* {
     const Tensor& x = first_rows(a[1], "x");
@@ -591,26 +635,29 @@ PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     desc.res_dtype = io_of(rt);
     const void* res = dense(a[2], "res", dev, {rows, C}, rt);
     const void* weight = dense(a[3], "weight", dev, {C}, ScalarType::Float);
-    void* res_out = dense(a[6], "res_out", dev, {rows, C}, rt);
+    Tensor made[3];
+    void* res_out = res ? out_dense(a[6], "res_out", dev, {rows, C}, rt, &made[2])
+                        : dense(a[6], "res_out", dev, {rows, C}, rt);
     const bool codes = desc.group >= 0;
-    void* y = dense(a[7], "y", dev, {rows, C}, codes ? ScalarType::Float8_e4m3fn : io);
+    void* y = out_dense(a[7], "y", dev, {rows, C}, codes ? ScalarType::Float8_e4m3fn : io, &made[0]);
     void* scale = nullptr;
     if (codes) {
-      scale = dense(a[8], "y_scale", dev, {rows, desc.group ? C / desc.group : 1}, ScalarType::Float);
+      scale = out_dense(a[8], "y_scale", dev, {rows, desc.group ? C / desc.group : 1}, ScalarType::Float, &made[1]);
     } else if (a[8] != Py_None) {
       throw Refused("y_scale without group");
     }
     const auto fn = function<decltype(&gdn_add_norm)>(a[0]);
     void* stream = handle(a[9]);
-    return on_device(dev, [&] {
+    PyObject* const given[3] = {a[7], a[8], a[6]};
+    return answer(on_device(dev, [&] {
       return fn(&desc, x_in, res, static_cast<const float*>(weight), res_out, y,
                 static_cast<float*>(scale), stream);
-    });
+    }), given, made);
   });
 }
 
-// (fn, size_fn, dy, r, weight, d_res_out, eps, dx, d_res, d_weight, workspace, stream); a workspace that is needed and
-// not given: minus its bytes
+// (fn, size_fn, dy, r, weight, d_res_out, eps, dx, d_res, d_weight, workspace, stream) -> (status, dx, d_res,
+//  d_weight); dx is d_res where it is not given and the types are one
 PyObject* add_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> PyObject* {
     const Tensor& dy = first_rows(a[2], "dy");
@@ -629,19 +676,26 @@ PyObject* add_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* r = dense(a[3], "r", dev, {rows, C}, rt);
     const void* weight = dense(a[4], "weight", dev, {C}, ScalarType::Float);
     const void* dro = dense(a[5], "d_res_out", dev, {rows, C}, rt);
-    void* dx = a[7] == Py_None ? nullptr : rows_of(a[7], "dx", dev, rows, C, io, &desc.ld_dx);
-    void* d_res = dense(a[8], "d_res", dev, {rows, C}, rt);
-    void* dw = dense(a[9], "d_weight", dev, {C}, ScalarType::Float);
+    Tensor made[3], scratch;
+    const bool one = a[7] == Py_None && io == rt;
+    void* d_res = out_dense(a[8], "d_res", dev, {rows, C}, rt, &made[1]);
+    void* dx = nullptr;
+    if (!one)
+      dx = a[7] == Py_None ? out_dense(a[7], "dx", dev, {rows, C}, io, &made[0])
+                           : rows_of(a[7], "dx", dev, rows, C, io, &desc.ld_dx);
+    void* dw = weight ? out_dense(a[9], "d_weight", dev, {C}, ScalarType::Float, &made[2])
+                      : dense(a[9], "d_weight", dev, {C}, ScalarType::Float);
     const size_t need = dw ? function<decltype(&gdn_add_norm_backward_workspace_size)>(a[1])(&desc) : 0;
-    void* ws;
     size_t bytes;
-    if (!workspace_of(a[10], dev, need, &ws, &bytes)) return PyLong_FromLongLong(-(long long)need);
+    void* ws = workspace_of(a[10], dev, need, &bytes, &scratch);
     const auto fn = function<decltype(&gdn_add_norm_backward)>(a[0]);
     void* stream = handle(a[11]);
-    return on_device(dev, [&] {
+    PyObject* const given[3] = {one ? a[8] : a[7], a[8], a[9]};
+    if (one) made[0] = made[1];
+    return answer(on_device(dev, [&] {
       return fn(&desc, up, r, static_cast<const float*>(weight), dro, ws, bytes, dx, d_res,
                 static_cast<float*>(dw), stream);
-    });
+    }), given, made);
   });
 }
 

@@ -130,33 +130,36 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(QkNormRopeBw
     for (int e = 0; e < 16; ++e) s_w[wave][(e < 8 ? m.c0 : m.c1 - 8) + e] = acc[e];
   }
   __syncthreads();
+  // the parts of an operand follow each other: q's, then k's
+  const int64_t part = is_q ? tb * sp.gq + grp : sp.tb * sp.gq + tb * sp.gk + (grp - sp.gq);
   if (threadIdx.x < D)
-    p.ws[blockIdx.x * (int64_t)D + threadIdx.x] = (s_w[0][threadIdx.x] + s_w[1][threadIdx.x]) +
+    p.ws[part * D + threadIdx.x] = (s_w[0][threadIdx.x] + s_w[1][threadIdx.x]) +
                                                   (s_w[2][threadIdx.x] + s_w[3][threadIdx.x]);
 }
 
 // Sum of the workgroups' partial weight gradients: one workgroup for 16 channels of an operand,
-// 16 threads to a channel.
+// 64 threads to a channel, each with several loads on their way (1816 parts of 128
+// channels: 42 us with 16 threads and one load at a time, XX us so).
+constexpr int kJoin = 64;
 template <int D>
-__global__ __launch_bounds__(kThreads) void qk_weight_join_kernel(QkNormRopeBwdArgs p) {
-  __shared__ float s[16][17];
+__global__ __launch_bounds__(16 * kJoin) void qk_weight_join_kernel(QkNormRopeBwdArgs p) {
+  __shared__ float s[kJoin][17];
   lds_nan_fill(s, sizeof s);
   const bool is_q = blockIdx.y == 0;
   float* to = is_q ? p.dq_weight : p.dk_weight;
   if (!to) return;
   const Split sp = split_of(p.rows, p.Hq, p.Hk, D);
-  const int all = sp.gq + sp.gk, first = is_q ? 0 : sp.gq, n = is_q ? sp.gq : sp.gk;
+  const int n = (int)sp.tb * (is_q ? sp.gq : sp.gk);
   const int col = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const float* src = p.ws + (is_q ? 0 : sp.tb * sp.gq * D) + 16 * blockIdx.x + col;
   float v = 0.f;
-  for (int64_t i = part; i < sp.tb * n; i += 16) {
-    const int64_t blk = i / n * all + first + i % n;
-    v += p.ws[blk * D + 16 * blockIdx.x + col];
-  }
+#pragma unroll 8
+  for (int i = part; i < n; i += kJoin) v += src[(int64_t)i * D];
   s[part][col] = v;
   __syncthreads();
   if (part == 0) {
-    v = s[0][col];
-    for (int i = 1; i < 16; ++i) v += s[i][col];
+#pragma unroll 8
+    for (int i = 1; i < kJoin; ++i) v += s[i][col];
     to[16 * blockIdx.x + col] = v;
   }
 }
@@ -172,7 +175,7 @@ hipError_t launch_d(const QkNormRopeBwdArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (!a.dq_weight && !a.dk_weight) return hipSuccess;
-  qk_weight_join_kernel<D><<<dim3(D / 16, 2), kThreads, 0, stream>>>(a);
+  qk_weight_join_kernel<D><<<dim3(D / 16, 2), 16 * kJoin, 0, stream>>>(a);
   return hipGetLastError();
 }
 template <typename T, typename G>

@@ -30,7 +30,7 @@ struct AttnBwdPlan {
 AttnBwdPlan attn_bwd_plan(int64_t N, int64_t total_T, int64_t window, int Hq, int Hk, int d,
                           DType io);
 // The most workgroups of any launch (checked against the grid limit by the caller).
-int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, int Hk,
+int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, int Hk, int d,
                         int parts, DType io);
 
 struct QkNormRopeBwdArgs {

@@ -75,13 +75,15 @@ def hybrid_abi_version() -> int:
     return lib.gdn_hybrid_abi_version()
 
 
-def _with_workspace(name, call, workspace, like, stream):
-    """call(workspace), with one of the size that it asks for where none is given."""
-    st = call(workspace)
-    if st < 0:                              # a workspace of so many bytes is needed
-        st = call(_empty((-st,), torch.uint8, like, stream))
-    if st != GDN_OK:
-        raise GdnError(st, name)
+def _done(r, name):
+    """The outputs of a call that answers (status, outputs ...)."""
+    if r[0] != GDN_OK:
+        raise GdnError(r[0], name)
+    return r[1:]
+
+
+# The extension module allocates what is not given for the device's current stream; on another stream it is
+# allocated here first.
 
 
 def gdn_attn_prefill_save(q, k, v, cu_seqlens=None, N=None, window: int = 0, scale=None, o=None,
@@ -92,15 +94,11 @@ def gdn_attn_prefill_save(q, k, v, cu_seqlens=None, N=None, window: int = 0, sca
     Arguments as gdn_attn_prefill; stats fp32 [total_T, H_q, 2] is allocated
     when not given, as o is.
     """
-    if o is None:
-        o = _empty(q.shape, q.dtype, q, stream)
-    if stats is None:
-        stats = _empty((*q.shape[:2], 2), torch.float32, q, stream)
-    st = _native.attn_prefill_save(_fn["gdn_attn_prefill_save"], q, k, v, cu_seqlens, N, window,
-                                   scale, o, stats, _raw_stream(stream, q))
-    if st != GDN_OK:
-        raise GdnError(st, "gdn_attn_prefill_save")
-    return o, stats
+    if stream is not None:
+        o = _empty(q.shape, q.dtype, q, stream) if o is None else o
+        stats = _empty((*q.shape[:2], 2), torch.float32, q, stream) if stats is None else stats
+    return _done(_native.attn_prefill_save(_fn["gdn_attn_prefill_save"], q, k, v, cu_seqlens, N, window,
+                                           scale, o, stats, _raw_stream(stream, q)), "gdn_attn_prefill_save")
 
 
 def gdn_attn_backward_workspace_size(q, k, N: int = 1, window: int = 0) -> int:
@@ -127,17 +125,18 @@ def gdn_attn_backward(q, k, v, o, d_o, stats, cu_seqlens=None, N=None, window: i
     """
     if grad_dtype is None:
         grad_dtype = next((t.dtype for t in (dq, dk, dv) if t is not None), q.dtype)
-    if dq is None:
-        dq = _empty(q.shape, grad_dtype, q, stream)
-    if dk is None:
-        dk = _empty(k.shape, grad_dtype, q, stream)
-    if dv is None:
-        dv = _empty(v.shape, grad_dtype, q, stream)
-    raw = _raw_stream(stream, q)
-    _with_workspace("gdn_attn_backward", lambda ws: _native.attn_backward(
-        _fn["gdn_attn_backward"], _fn["gdn_attn_backward_workspace_size"], q, k, v, o, d_o, stats,
-        cu_seqlens, N, window, scale, dq, dk, dv, ws, raw), workspace, q, stream)
-    return dq, dk, dv
+    if grad_dtype not in _DT:
+        raise ValueError("gradients must be float32 or bfloat16")
+    if stream is not None:
+        dq, dk, dv = (_empty(x.shape, grad_dtype, q, stream) if t is None else t
+                      for t, x in ((dq, q), (dk, k), (dv, v)))
+        if workspace is None:
+            need = gdn_attn_backward_workspace_size(q, k, len(cu_seqlens) - 1 if cu_seqlens is not None else N or 1, window)
+            workspace = _empty((need,), torch.uint8, q, stream)
+    return _done(_native.attn_backward(_fn["gdn_attn_backward"], _fn["gdn_attn_backward_workspace_size"],
+                                       q, k, v, o, d_o, stats, cu_seqlens, N, window, scale, dq, dk, dv,
+                                       grad_dtype == torch.float32, workspace, _raw_stream(stream, q)),
+                 "gdn_attn_backward")
 
 
 def gdn_qk_norm_rope_backward_workspace_size(dq=None, dk=None) -> int:
@@ -168,20 +167,17 @@ def gdn_qk_norm_rope_backward(dq, dk, q_raw=None, k_raw=None, positions=None, in
     one = dk if dq is None else dq
     if one is None:
         raise ValueError("dq or dk must be given")
-    if dq_raw is None and dq is not None:
-        dq_raw = _empty(dq.shape, dq.dtype, dq, stream)
-    if dk_raw is None and dk is not None:
-        dk_raw = _empty(dk.shape, dk.dtype, dk, stream)
-    if dq_weight is None and q_weight is not None:
-        dq_weight = _empty(q_weight.shape, torch.float32, one, stream)
-    if dk_weight is None and k_weight is not None:
-        dk_weight = _empty(k_weight.shape, torch.float32, one, stream)
-    raw = _raw_stream(stream, one)
-    _with_workspace("gdn_qk_norm_rope_backward", lambda ws: _native.qk_norm_rope_backward(
-        _fn["gdn_qk_norm_rope_backward"], _fn["gdn_qk_norm_rope_backward_workspace_size"], dq, dk,
-        q_raw, k_raw, positions, inv_freq, q_weight, k_weight, interleaved, rope_scale, eps, dq_raw,
-        dk_raw, dq_weight, dk_weight, ws, raw), workspace, one, stream)
-    return dq_raw, dk_raw, dq_weight, dk_weight
+    if stream is not None:
+        dq_raw, dk_raw = (_empty(x.shape, x.dtype, x, stream) if t is None and x is not None else t
+                          for t, x in ((dq_raw, dq), (dk_raw, dk)))
+        dq_weight, dk_weight = (_empty(w.shape, torch.float32, one, stream) if t is None and w is not None else t
+                                for t, w in ((dq_weight, q_weight), (dk_weight, k_weight)))
+        if workspace is None:
+            workspace = _empty((gdn_qk_norm_rope_backward_workspace_size(dq, dk),), torch.uint8, one, stream)
+    return _done(_native.qk_norm_rope_backward(
+        _fn["gdn_qk_norm_rope_backward"], _fn["gdn_qk_norm_rope_backward_workspace_size"], dq, dk, q_raw, k_raw,
+        positions, inv_freq, q_weight, k_weight, interleaved, rope_scale, eps, dq_raw, dk_raw, dq_weight,
+        dk_weight, workspace, _raw_stream(stream, one)), "gdn_qk_norm_rope_backward")
 
 
 def gdn_add_norm(x, res=None, weight=None, eps: float = 1e-6, group=None, res_out=None, y=None,
@@ -196,17 +192,15 @@ def gdn_add_norm(x, res=None, weight=None, eps: float = 1e-6, group=None, res_ou
     and, with a res, res_out are allocated when not given; res_out may be res, and
     y may be a dense x.
     """
-    if y is None:
-        y = _empty(x.shape, x.dtype if group is None else torch.float8_e4m3fn, x, stream)
-    if y_scale is None and group is not None:
-        y_scale = _empty((x.shape[0], x.shape[1] // group if group else 1), torch.float32, x, stream)
-    if res_out is None and res is not None:
-        res_out = _empty(res.shape, res.dtype, x, stream)
-    st = _native.add_norm(_fn["gdn_add_norm"], x, res, weight, eps, group, res_out, y, y_scale,
-                          _raw_stream(stream, x))
-    if st != GDN_OK:
-        raise GdnError(st, "gdn_add_norm")
-    return y, y_scale, res_out
+    if stream is not None:
+        if y is None:
+            y = _empty(x.shape, x.dtype if group is None else torch.float8_e4m3fn, x, stream)
+        if y_scale is None and group is not None:
+            y_scale = _empty((x.shape[0], x.shape[1] // group if group else 1), torch.float32, x, stream)
+        if res_out is None and res is not None:
+            res_out = _empty(res.shape, res.dtype, x, stream)
+    return _done(_native.add_norm(_fn["gdn_add_norm"], x, res, weight, eps, group, res_out, y, y_scale,
+                                  _raw_stream(stream, x)), "gdn_add_norm")
 
 
 def gdn_add_norm_backward_workspace_size(dy) -> int:
@@ -229,15 +223,15 @@ def gdn_add_norm_backward(dy, r, weight=None, d_res_out=None, eps: float = 1e-6,
     where the types are one and dx is not given, dx is d_res.  What is not given
     is allocated (d_weight only with a weight); dx may be dy, d_res may be d_res_out.
     """
-    if d_res is None:
-        d_res = _empty(r.shape, r.dtype, dy, stream)
-    if d_weight is None and weight is not None:
-        d_weight = _empty(weight.shape, torch.float32, dy, stream)
-    both = dx is None and dy.dtype == r.dtype
-    if dx is None and not both:
-        dx = _empty(dy.shape, dy.dtype, dy, stream)
-    raw = _raw_stream(stream, dy)
-    _with_workspace("gdn_add_norm_backward", lambda ws: _native.add_norm_backward(
-        _fn["gdn_add_norm_backward"], _fn["gdn_add_norm_backward_workspace_size"], dy, r, weight,
-        d_res_out, eps, dx, d_res, d_weight, ws, raw), workspace, dy, stream)
-    return d_res if both else dx, d_res, d_weight
+    if stream is not None:
+        if d_res is None:
+            d_res = _empty(r.shape, r.dtype, dy, stream)
+        if d_weight is None and weight is not None:
+            d_weight = _empty(weight.shape, torch.float32, dy, stream)
+        if dx is None and dy.dtype != r.dtype:
+            dx = _empty(dy.shape, dy.dtype, dy, stream)
+        if workspace is None:
+            workspace = _empty((gdn_add_norm_backward_workspace_size(dy),), torch.uint8, dy, stream)
+    return _done(_native.add_norm_backward(
+        _fn["gdn_add_norm_backward"], _fn["gdn_add_norm_backward_workspace_size"], dy, r, weight, d_res_out, eps,
+        dx, d_res, d_weight, workspace, _raw_stream(stream, dy)), "gdn_add_norm_backward")

@@ -91,8 +91,9 @@ size_t gdn_attn_backward_workspace_size(const gdn_attn_bwd_desc* desc);
  *              outside the arguments)
  *   workspace  >= gdn_attn_backward_workspace_size(desc) bytes, 16-byte aligned
  *   dq [total_T, H_q, d], dk, dv [total_T, H_k, d] grad_dtype, row strides
- *              (outputs); may be column blocks of one buffer.  Rows that no range
- *              covers are kept.
+ *              (outputs); may be column blocks of one buffer.  Rows before the
+ *              first range and behind the last are kept; offsets that fall give
+ *              unspecified gradients, never an access outside the arguments.
  */
 gdn_status gdn_attn_backward(const gdn_attn_bwd_desc* desc, const int64_t* cu_seqlens,
                              const void* q, const void* k, const void* v, const void* o,
