@@ -19,6 +19,7 @@
 // In both, what is summed over lies on the rows of the first products (S^T = K Q^T and
 // dP^T = V dO^T for dq; S = Q K^T and dP = dO V^T for dk and dv), so p and ds are, as
 // they lie in the accumulators, the k-values of the second products.
+#include "attn_shares.hpp"
 #include "attn_tiles.hpp"
 
 #include "hybrid_kernels.hpp"
@@ -32,38 +33,208 @@ __device__ __forceinline__ TileArgs tile_args(const AttnBwdArgs& p, int G) {
   return TileArgs{p.cu_seqlens, p.N, p.Tseq, p.total_T, p.window, p.Hk, G};
 }
 
-// The workspace: 16 bytes for each query and head, then the partial dk and dv.
+// One walk of a key tile: [k0, k0 + BK) of the sequence [a, a + L), steps [at, stop) of the
+// `each` steps of each query head of the key head hk; its sums go to the outputs (slot -1)
+// or to a slot of the workspace.
+struct Walk {
+  int64_t a;
+  int L, k0, hk, each, at, stop, slot, pad;
+};
+// A worker's walks, and the tile that it begins and `behind` workers behind it go on with.
+struct Worker {
+  int first, count;
+  int64_t row0;
+  int rows, hk, behind, pad;
+};
+static_assert(sizeof(Walk) == 40 && sizeof(Worker) == 32, "10 and 8 floats");
+
+// The workspace: 16 bytes for each query and head, the workers, their walks, and two
+// partial tiles of dk and dv for each worker.
+__host__ __device__ inline int64_t tiles_of(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int64_t rows) {
+  return packed ? total_T / rows + N : N * ((Tseq + rows - 1) / rows);
+}
 __device__ __forceinline__ uint4* aux_of(const AttnBwdArgs& p, int hq) {
   return reinterpret_cast<uint4*>(p.ws) + hq * p.total_T;
 }
-__device__ __forceinline__ float* parts_of(const AttnBwdArgs& p) {
-  return p.ws + 4 * p.total_T * p.Hq;
+__device__ __forceinline__ Worker* workers_of(const AttnBwdArgs& p) {
+  return reinterpret_cast<Worker*>(p.ws + 4 * p.total_T * p.Hq);
+}
+__device__ __forceinline__ Walk* walks_of(const AttnBwdArgs& p, int workers) {
+  return reinterpret_cast<Walk*>(p.ws + 4 * p.total_T * p.Hq + 8 * workers);
+}
+__host__ __device__ inline int64_t walk_floats(int64_t tiles, int Hk, int workers) {
+  return (10 * (tiles * Hk + workers) + 3) / 4 * 4;   // slots begin at 16 bytes
+}
+template <int D, int BK>
+__device__ __forceinline__ float* slot_of(const AttnBwdArgs& p, int workers, int slot) {
+  const int64_t tiles = tiles_of(p.N, p.total_T, p.Tseq, p.cu_seqlens != nullptr, BK);
+  return p.ws + 4 * p.total_T * p.Hq + 8 * workers + walk_floats(tiles, p.Hk, workers) +
+         (int64_t)slot * (BK * 2 * D);
 }
 
-// A key tile's number from its rank among the tiles of its sequence by cost: the first
-// keys are seen by the most queries.
-template <int BK>
-__device__ __forceinline__ int key_tile_start(const Tile& t) {
-  const int tiles = (int)((t.L + BK - 1) / BK);
-  return (tiles - 1 - (int)(t.q0 / BK)) * BK;
+// ---------------------------------------------------------------------------
+// Who walks what.  A workgroup of the dk and dv kernel has either one key tile (`workers`
+// 0: many tiles, the dear ones first) or an equal share of all tiles' walks, in the order
+// of sequence, key head and tile: then the first and the last walk of a share may be parts
+// of one, whose sums go to the workspace and are joined in order by another kernel.  Shares
+// that follow each other are on one XCD.  The shares are counted out by the first
+// workgroups of the dq kernel, a wave to a worker.
+// ---------------------------------------------------------------------------
+constexpr int kLead = 4;                    // steps that a walk's beginning and end are worth
+constexpr int64_t kLeast = 8;               // units of a share
+constexpr int plan_blocks(int workers) { return (workers + 8 * 4 - 1) / (8 * 4) * 8; }   // whole rounds of the XCDs
+
+__device__ __forceinline__ int64_t length_of(const AttnBwdArgs& p, int64_t i) {
+  const int64_t l = clamp_i64(p.cu_seqlens[i + 1], 0, p.total_T) - clamp_i64(p.cu_seqlens[i], 0, p.total_T);
+  return l > 0 ? l : 0;
 }
 
-// What one workgroup of a key tile walks: steps [at, stop) of the query heads of its
-// key head, each going through the `each` query tiles that see the keys.
-struct Walk {
-  int each, at, stop;
-};
 template <int BK, int BQ>
-__device__ __forceinline__ Walk walk_of(int k0, int L, int window, int G, int part, int parts) {
-  int64_t end = window ? (int64_t)k0 + BK - 1 + window : L;
-  if (end > L) end = L;
-  Walk w;
-  w.each = (int)(end - k0 + BQ - 1) / BQ;
-  const int64_t all = (int64_t)w.each * G;
-  w.at = (int)(all * part / parts);
-  w.stop = (int)(all * (part + 1) / parts);
-  return w;
+__device__ __forceinline__ void plan_worker(const AttnBwdArgs& p, int workers, int worker) {
+  if (worker >= workers) return;
+  const int lane = threadIdx.x & 63;
+  const WalkUnits u{p.window, BK, BQ, p.Hq / p.Hk, kLead};
+  int64_t total;
+  if (!p.cu_seqlens) {
+    total = p.N * p.Hk * u.units(p.Tseq);
+  } else {
+    int64_t sum = 0;
+    for (int64_t i = lane; i < p.N; i += 64) sum += u.units(length_of(p, i));
+#pragma unroll
+    for (int off = 32; off; off >>= 1) sum += __shfl_xor((long long)sum, off);
+    total = sum * p.Hk;
+  }
+  const Shares s = shares_of(total, workers, kLeast);
+  Worker me{0, 0, 0, 0, 0, 0, 0};
+  int64_t x = 0, end = 0;
+  if (worker < s.workers) {
+    x = s.begin(worker);
+    end = s.begin(worker + 1);
+  }
+  if (x < end) {
+    // sequence n with its units [base, base + Hk per), its tile j of head hk from unit `from`
+    // on; `tiles` before the sequence
+    int64_t n = 0, base = 0, per = 1, a = 0, L = 0, tiles = 0;
+    if (!p.cu_seqlens) {
+      per = u.units(p.Tseq);
+      n = x / (per * p.Hk);
+      base = n * per * p.Hk;
+      a = n * p.Tseq;
+      L = p.Tseq;
+      tiles = n * u.tiles(L);
+    } else {
+      for (int64_t i0 = 0; i0 < p.N; i0 += 64) {
+        const int64_t l = i0 + lane < p.N ? length_of(p, i0 + lane) : 0;
+        const int64_t mine = u.units(l) * p.Hk;
+        int64_t upto = mine, tiles_to = u.tiles(l);
+#pragma unroll
+        for (int off = 1; off < 64; off *= 2) {
+          const int64_t v = __shfl_up((long long)upto, off), t = __shfl_up((long long)tiles_to, off);
+          if (lane >= off) { upto += v; tiles_to += t; }
+        }
+        const uint64_t m = __ballot(base + upto > x);
+        if (m) {
+          const int k = __ffsll((unsigned long long)m) - 1;
+          n = i0 + k;
+          L = read_lane(l, k);
+          per = read_lane(mine, k) / p.Hk;
+          base += read_lane(upto, k) - per * p.Hk;
+          tiles += read_lane(tiles_to, k) - u.tiles(L);
+          break;
+        }
+        base += read_lane(upto, 63);
+        tiles += read_lane(tiles_to, 63);
+      }
+      a = clamp_i64(p.cu_seqlens[n], 0, p.total_T);
+    }
+    const int64_t r = x - base;
+    int hk = (int)(r / per);
+    int64_t j = u.tile_at(L, r - hk * per);
+    int64_t from = base + hk * per + u.before(L, j);
+    // each tile has a place of its own in the list, and each worker one more
+    me.first = (int)(tiles * p.Hk + hk * u.tiles(L) + j + worker);
+    Walk* to = walks_of(p, workers) + me.first;
+    while (x < end) {
+      const WalkPart w = part_of(u, L, j, from, x, end);
+      if (w.s1 > w.s0) {
+        const Walk t{a, (int)L, (int)(j * BK), hk, (int)(w.all / u.G), (int)w.s0, (int)w.s1,
+                     w.whole() ? -1 : 2 * worker + (w.s0 == 0), 0};
+        if (lane == 0) to[me.count] = t;
+        ++me.count;
+        if (w.s0 == 0 && !w.whole()) {
+          me.behind = s.owner(from + u.lead + w.all - 1) - worker;
+          me.row0 = a + j * BK;
+          me.rows = (int)(L - j * BK < BK ? L - j * BK : BK);
+          me.hk = hk;
+        }
+      }
+      x = w.next;
+      from += u.lead + w.all;
+      if (x < end && ++j == u.tiles(L)) {
+        j = 0;
+        if (++hk == p.Hk) {
+          hk = 0;
+          ++n;
+          if (p.cu_seqlens) {
+            while (n < p.N && length_of(p, n) == 0) ++n;
+            if (n >= p.N) break;            // (offsets that changed under the call)
+            a = clamp_i64(p.cu_seqlens[n], 0, p.total_T);
+            L = length_of(p, n);
+          } else {
+            a += p.Tseq;
+          }
+        }
+      }
+    }
+  }
+  if (lane == 0) workers_of(p)[worker] = me;
 }
+
+// x, but what is computed from it is not taken out of a loop over walks: addresses kept
+// through a walk would spill its sums.
+__device__ __forceinline__ int each_walk(int x) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("" : "+v"(x));
+#endif
+  return x;
+}
+
+// The walks of a workgroup: those of its worker, or its tile's.
+template <int BK, int BQ>
+struct Walks {
+  int first, count;
+  __device__ __forceinline__ Walks(const AttnBwdArgs& p, int workers) : first(0), count(1) {
+    if (workers) {
+      const int worker = blockIdx.x % kXcds * (workers / kXcds) + blockIdx.x / kXcds;   // (a multiple of kXcds)
+      first = __builtin_amdgcn_readfirstlane(workers_of(p)[worker].first);
+      count = __builtin_amdgcn_readfirstlane(workers_of(p)[worker].count);
+    }
+  }
+  __device__ __forceinline__ Walk walk(const AttnBwdArgs& p, uint32_t blocks, int workers, int i) const {
+    Walk w;
+    if (workers) {
+      w = walks_of(p, workers)[first + i];
+      w.a = (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)w.a) |
+            (int64_t)__builtin_amdgcn_readfirstlane((int)(w.a >> 32)) << 32;
+    } else {
+      const Tile t = find_tile<BK>(tile_args(p, 1), blockIdx.x, blocks);
+      const WalkUnits u{p.window, BK, BQ, p.Hq / p.Hk, 0};
+      // the first keys are seen by the most queries
+      const int64_t j = t.valid ? (t.L + BK - 1) / BK - 1 - t.q0 / BK : 0;
+      w.a = t.a; w.L = (int)t.L; w.k0 = (int)(j * BK); w.hk = t.hq;
+      w.each = t.valid ? (int)u.steps(t.L, j) : 0;
+      w.at = 0; w.stop = w.each * u.G; w.slot = -1;
+    }
+    w.L = __builtin_amdgcn_readfirstlane(w.L);
+    w.k0 = __builtin_amdgcn_readfirstlane(w.k0);
+    w.hk = __builtin_amdgcn_readfirstlane(w.hk);
+    w.each = __builtin_amdgcn_readfirstlane(w.each);
+    w.at = __builtin_amdgcn_readfirstlane(w.at);
+    w.stop = __builtin_amdgcn_readfirstlane(w.stop);
+    w.slot = __builtin_amdgcn_readfirstlane(w.slot);
+    return w;
+  }
+};
 
 // ---------------------------------------------------------------------------
 // fp32: v_mfma_f32_16x16x4_f32, 32 queries (dq) or 32 keys (dk, dv) to a workgroup,
@@ -72,14 +243,19 @@ __device__ __forceinline__ Walk walk_of(int k0, int L, int window, int G, int pa
 // sums are added at the end.
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attn_dq_f32_kernel(AttnBwdArgs p, uint32_t blocks) {
+__global__ __launch_bounds__(kThreads, 2) void attn_dq_f32_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
   constexpr int BM = 32, BN = 32, LD = D + 4, KB = D / 32, MT = D / 16;
+  constexpr int KEYS = 32, STEP = 32;       // of the dk and dv kernel
   constexpr int NL = BN * D / 4 / kThreads;
   __shared__ __align__(16) float s_kv[2 * BN * LD];
   lds_nan_fill(s_kv, sizeof s_kv);
   float *s_k = s_kv, *s_v = s_kv + BN * LD;
-  const int G = p.Hq / p.Hk;
-  const Tile tl = find_tile<BM>(tile_args(p, G), blocks);
+  const int G = p.Hq / p.Hk, plan = plan_blocks(workers);
+  if ((int)blockIdx.x < plan) {
+    plan_worker<KEYS, STEP>(p, workers, 4 * blockIdx.x + (threadIdx.x >> 6));
+    return;
+  }
+  const Tile tl = find_tile<BM>(tile_args(p, G), blockIdx.x - plan, blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -190,7 +366,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_f32_kernel(AttnBwdArgs p,
 }
 
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attn_dkv_f32_kernel(AttnBwdArgs p, uint32_t blocks, int parts) {
+__global__ __launch_bounds__(kThreads, 2) void attn_dkv_f32_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
   constexpr int BK = 32, BQ = 32, LD = D + 4, KB = D / 32, MT = D / 16;
   constexpr int NL = BQ * D / 4 / kThreads;
   __shared__ __align__(16) float s_qg[2 * BQ * LD];
@@ -198,115 +374,118 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dkv_f32_kernel(AttnBwdArgs p
   lds_nan_fill(s_qg, sizeof s_qg);
   float *s_q = s_qg, *s_g = s_qg + BQ * LD;
   const int G = p.Hq / p.Hk;
-  const Tile tl = find_tile<BK>(tile_args(p, parts), blocks);
-  if (!tl.valid) return;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wave & 1, wq = wave >> 1;
-  const int g = lane >> 4, j = lane & 15;
-  const int hk = tl.hq / parts, part = tl.hq - hk * parts, L = (int)tl.L;
-  const int k0 = key_tile_start<BK>(tl);
-  const int u0 = k0 + 16 * wk, tk = u0 + j;           // this lane's key
-  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
-  const Walk w = walk_of<BK, BQ>(k0, L, window, G, part, parts);
   const float c_scale = p.scale * kLog2e;
-
-  Frag8<float> k[KB], v[KB];
-  {
-    const int64_t row = tl.a + (tk < L ? tk : L - 1);
+  const Walks<BK, BQ> walks(p, workers);
+  for (int nth = 0; nth < walks.count; ++nth) {
+    const Walk w = walks.walk(p, blocks, workers, nth);
+    if (w.at >= w.stop) continue;
+    const int tid = each_walk(threadIdx.x), lane = tid & 63, g = lane >> 4, j = lane & 15;
+    const int hk = w.hk, L = w.L, k0 = w.k0;
+    const int u0 = k0 + 16 * wk, tk = u0 + j;         // this lane's key
+    const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
+    Frag8<float> k[KB], v[KB];
+    {
+      const int64_t row = w.a + (tk < L ? tk : L - 1);
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      load_f32<8, float>(static_cast<const float*>(p.k) + row * p.ld_k + hk * D + 32 * kb + 8 * g, k[kb].v);
-      load_f32<8, float>(static_cast<const float*>(p.v) + row * p.ld_v + hk * D + 32 * kb + 8 * g, v[kb].v);
-    }
-  }
-  f32x4 dk[MT], dv[MT];
-#pragma unroll
-  for (int c = 0; c < MT; ++c) dk[c] = dv[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float4 qr[NL], gr[NL], ar;
-  auto load_tile = [&](int step) {          // rows past the sequence are zero
-    const int head = step / w.each, t0 = k0 + (step - head * w.each) * BQ;
-    const int hq = hk * G + head;
-#pragma unroll
-    for (int e = 0; e < NL; ++e) {
-      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
-      qr[e] = gr[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t0 + row < L) {
-        qr[e] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + (tl.a + t0 + row) * p.ld_q + hq * D + c);
-        gr[e] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.d_o) + ((tl.a + t0 + row) * p.Hq + hq) * (int64_t)D + c);
+      for (int kb = 0; kb < KB; ++kb) {
+        load_f32<8, float>(static_cast<const float*>(p.k) + row * p.ld_k + hk * D + 32 * kb + 8 * g, k[kb].v);
+        load_f32<8, float>(static_cast<const float*>(p.v) + row * p.ld_v + hk * D + 32 * kb + 8 * g, v[kb].v);
       }
     }
-    ar = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tid < BQ && t0 + tid < L)
-      ar = reinterpret_cast<const float4*>(aux_of(p, hq))[tl.a + t0 + tid];
-  };
-  if (w.at < w.stop) load_tile(w.at);
-  for (int step = w.at; step < w.stop; ++step) {
-    __syncthreads();
+    f32x4 dk[MT], dv[MT];
 #pragma unroll
-    for (int e = 0; e < NL; ++e) {
-      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
-      lds_check(s_g + row * LD + c, 16);
-      *reinterpret_cast<float4*>(s_q + row * LD + c) = qr[e];
-      *reinterpret_cast<float4*>(s_g + row * LD + c) = gr[e];
+    for (int c = 0; c < MT; ++c) dk[c] = dv[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float4 qr[NL], gr[NL], ar;
+    int head = w.at / w.each, tile = w.at - head * w.each;  // of the step to load
+    int now = tile;                                         // of the step at hand
+    auto load_tile = [&]() {                // rows past the sequence are zero
+      const int t0 = k0 + tile * BQ, hq = hk * G + head;
+#pragma unroll
+      for (int e = 0; e < NL; ++e) {
+        const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+        qr[e] = gr[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t0 + row < L) {
+          qr[e] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + (w.a + t0 + row) * p.ld_q + hq * D + c);
+          gr[e] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.d_o) + ((w.a + t0 + row) * p.Hq + hq) * (int64_t)D + c);
+        }
+      }
+      ar = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (tid < BQ && t0 + tid < L)
+        ar = reinterpret_cast<const float4*>(aux_of(p, hq))[w.a + t0 + tid];
+      if (++tile == w.each) { tile = 0; ++head; }
+    };
+    load_tile();
+    for (int step = w.at; step < w.stop; ++step) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < NL; ++e) {
+        const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+        lds_check(s_g + row * LD + c, 16);
+        *reinterpret_cast<float4*>(s_q + row * LD + c) = qr[e];
+        *reinterpret_cast<float4*>(s_g + row * LD + c) = gr[e];
+      }
+      if (tid < BQ) s_aux[tid] = ar;
+      __syncthreads();
+      if (step + 1 < w.stop) load_tile();
+      const int t0 = k0 + now * BQ + 16 * wq;         // this wave's queries
+      if (++now == w.each) now = 0;
+      if (t0 + 15 < u0 || t0 >= L || (window && t0 - window >= u0 + 15)) continue;
+      f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        Frag8<float> a;
+        load_f32<8, float>(s_q + (16 * wq + j) * LD + 32 * kb + 8 * g, a.v);
+        mma32(s, a, k[kb]);
+        load_f32<8, float>(s_g + (16 * wq + j) * LD + 32 * kb + 8 * g, a.v);
+        mma32(dp, a, v[kb]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * wq + 4 * g + r, t = t0 + 4 * g + r;
+        const float4 st = s_aux[row];
+        const bool seen = tk <= t && t < L && (!window || tk > t - window);
+        const float pr = seen ? weight_of(s[r] * c_scale, st.x) * st.y : 0.f;
+        const float ds = pr * (dp[r] - st.z);
+        const float *ql = s_q + row * LD + j, *gl = s_g + row * LD + j;
+#pragma unroll
+        for (int c = 0; c < MT; ++c) {
+          dv[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(gl[16 * c], pr, dv[c], 0, 0, 0);
+          dk[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(ql[16 * c], ds, dk[c], 0, 0, 0);
+        }
+      }
     }
-    if (tid < BQ) s_aux[tid] = ar;
     __syncthreads();
-    if (step + 1 < w.stop) load_tile(step + 1);
-    const int t0 = k0 + step % w.each * BQ + 16 * wq;       // this wave's queries
-    if (t0 + 15 < u0 || t0 >= L || (window && t0 - window >= u0 + 15)) continue;
-    f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      Frag8<float> a;
-      load_f32<8, float>(s_q + (16 * wq + j) * LD + 32 * kb + 8 * g, a.v);
-      mma32(s, a, k[kb]);
-      load_f32<8, float>(s_g + (16 * wq + j) * LD + 32 * kb + 8 * g, a.v);
-      mma32(dp, a, v[kb]);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * wq + 4 * g + r, t = t0 + 4 * g + r;
-      const float4 st = s_aux[row];
-      const bool seen = tk <= t && t < L && (!window || tk > t - window);
-      const float pr = seen ? weight_of(s[r] * c_scale, st.x) * st.y : 0.f;
-      const float ds = pr * (dp[r] - st.z);
-      const float *ql = s_q + row * LD + j, *gl = s_g + row * LD + j;
+    if (wq == 1) {
 #pragma unroll
       for (int c = 0; c < MT; ++c) {
-        dv[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(gl[16 * c], pr, dv[c], 0, 0, 0);
-        dk[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(ql[16 * c], ds, dk[c], 0, 0, 0);
+        float* dst = s_qg + (16 * wk + j) * LD + 16 * c + 4 * g;
+        lds_check(dst + BQ * LD, 16);
+        *reinterpret_cast<float4*>(dst) = make_float4(dk[c][0], dk[c][1], dk[c][2], dk[c][3]);
+        *reinterpret_cast<float4*>(dst + BQ * LD) = make_float4(dv[c][0], dv[c][1], dv[c][2], dv[c][3]);
       }
     }
-  }
-  __syncthreads();
-  if (wq == 1) {
+    __syncthreads();
+    if (wq == 0 && tk < L) {
+      float *tok, *tov;
+      if (w.slot < 0) {
+        tok = static_cast<float*>(p.dk) + (w.a + tk) * p.ld_dk + hk * D;
+        tov = static_cast<float*>(p.dv) + (w.a + tk) * p.ld_dv + hk * D;
+      } else {
+        tok = slot_of<D, BK>(p, workers, w.slot) + (tk - k0) * (2 * D);
+        tov = tok + D;
+      }
 #pragma unroll
-    for (int c = 0; c < MT; ++c) {
-      float* dst = s_qg + (16 * wk + j) * LD + 16 * c + 4 * g;
-      lds_check(dst + BQ * LD, 16);
-      *reinterpret_cast<float4*>(dst) = make_float4(dk[c][0], dk[c][1], dk[c][2], dk[c][3]);
-      *reinterpret_cast<float4*>(dst + BQ * LD) = make_float4(dv[c][0], dv[c][1], dv[c][2], dv[c][3]);
+      for (int c = 0; c < MT; ++c) {
+        const float* src = s_qg + (16 * wk + j) * LD + 16 * c + 4 * g;
+        const float4 a = *reinterpret_cast<const float4*>(src);
+        const float4 b = *reinterpret_cast<const float4*>(src + BQ * LD);
+        store4<float>(tok + 16 * c + 4 * g, (dk[c][0] + a.x) * p.scale, (dk[c][1] + a.y) * p.scale,
+                      (dk[c][2] + a.z) * p.scale, (dk[c][3] + a.w) * p.scale);
+        store4<float>(tov + 16 * c + 4 * g, dv[c][0] + b.x, dv[c][1] + b.y, dv[c][2] + b.z, dv[c][3] + b.w);
+      }
     }
-  }
-  __syncthreads();
-  if (wq == 1 || tk >= L) return;
-  float *tok, *tov;
-  if (parts == 1) {
-    tok = static_cast<float*>(p.dk) + (tl.a + tk) * p.ld_dk + hk * D;
-    tov = static_cast<float*>(p.dv) + (tl.a + tk) * p.ld_dv + hk * D;
-  } else {
-    tok = parts_of(p) + ((part * p.total_T + tl.a + tk) * p.Hk + hk) * (2 * D);
-    tov = tok + D;
-  }
-#pragma unroll
-  for (int c = 0; c < MT; ++c) {
-    const float* src = s_qg + (16 * wk + j) * LD + 16 * c + 4 * g;
-    const float4 a = *reinterpret_cast<const float4*>(src);
-    const float4 b = *reinterpret_cast<const float4*>(src + BQ * LD);
-    store4<float>(tok + 16 * c + 4 * g, (dk[c][0] + a.x) * p.scale, (dk[c][1] + a.y) * p.scale,
-                  (dk[c][2] + a.z) * p.scale, (dk[c][3] + a.w) * p.scale);
-    store4<float>(tov + 16 * c + 4 * g, dv[c][0] + b.x, dv[c][1] + b.y, dv[c][2] + b.z, dv[c][3] + b.w);
   }
 }
 
@@ -404,13 +583,18 @@ __device__ __forceinline__ void rows_out(bf16* lds, const f32x16* acc, float f, 
 }
 
 template <int D, typename TG>
-__global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p, uint32_t blocks) {
+__global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
   constexpr int BM = 128, BN = 64, KB = D / 16, MT = D / 32;
+  constexpr int KEYS = 128, STEP = 64;      // of the dk and dv kernel
   __shared__ __align__(16) bf16 s_k[2][BN * D], s_v[2][BN * D];
   lds_nan_fill(s_k, sizeof s_k);
   lds_nan_fill(s_v, sizeof s_v);
-  const int G = p.Hq / p.Hk;
-  const Tile tl = find_tile<BM>(tile_args(p, G), blocks);
+  const int G = p.Hq / p.Hk, plan = plan_blocks(workers);
+  if ((int)blockIdx.x < plan) {
+    plan_worker<KEYS, STEP>(p, workers, 4 * blockIdx.x + (threadIdx.x >> 6));
+    return;
+  }
+  const Tile tl = find_tile<BM>(tile_args(p, G), blockIdx.x - plan, blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -625,7 +809,7 @@ __device__ __forceinline__ void keep_a(bf16x8& x) {
 // between them, then this one's second products; every LDS read some products ahead of its
 // use; tiles three deep in LDS.
 template <int D, typename TG>
-__global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs p, uint32_t blocks, int parts) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
   constexpr int BK = 128, BQ = 64, KB = D / 16, MT = D / 32;
   constexpr int GO = BQ * D * 2;            // d_o behind q in a buffer
   constexpr int BUF = 2 * GO;
@@ -635,32 +819,48 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
   __shared__ __align__(1024) uint4 s_aux[NB][BQ];
   lds_nan_fill(s_t, sizeof s_t);
   const int G = p.Hq / p.Hk;
-  const Tile tl = find_tile<BK>(tile_args(p, parts), blocks);
-  if (!tl.valid) return;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int h = lane >> 5, i32 = lane & 31;
-  const int hk = __builtin_amdgcn_readfirstlane(tl.hq / parts);
-  const int part = __builtin_amdgcn_readfirstlane(tl.hq - hk * parts);
-  const int L = __builtin_amdgcn_readfirstlane((int)tl.L);
-  const int k0 = __builtin_amdgcn_readfirstlane(key_tile_start<BK>(tl));
-  const int u0 = k0 + 32 * wave, tk = u0 + i32;       // this lane's key
-  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
-  const Walk w = walk_of<BK, BQ>(k0, L, window, G, part, parts);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float c_scale = p.scale * kLog2e;
   const uint32_t lq2 = (uint32_t)p.ld_q * 2, lg2 = (uint32_t)p.Hq * D * 2;
 
+  // lanes 0..31 supply the terms of m and l, 32..63 those of D
+  const uint32_t one = 0x3f80;              // 1 in bf16
+  const bool low = (threadIdx.x & 32) == 0;
+  bf16x8 ones_s = __builtin_bit_cast(bf16x8, make_uint4(low ? one << 16 | one : 0, low ? one : 0, 0, 0));
+  bf16x8 ones_d = __builtin_bit_cast(bf16x8, make_uint4(low ? 0 : one << 16 | one, low ? 0 : one, 0, 0));
+  const LaneReads at = lane_reads<D>(lds_address(s_t), threadIdx.x & 63);
+  const uint32_t at_aux = lds_address(s_aux) + 16 * (threadIdx.x & 31) + (low ? 0 : 8);
+
+  auto statistics = [&](uint32_t block) {   // of a block of 32 queries, at BUF-relative byte `block`
+    const uint2 a = lds_read<uint2>(at_aux + block);
+    return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, 0, 0));
+  };
+  keep_a(ones_s);
+  keep_a(ones_d);
+  constexpr int NF = 2 * KB, NS = 4 * MT;   // first and second products of a block
+  constexpr int AF = 4, AS = 4;             // reads ahead
+  constexpr int E1 = 10;                    // weights formed between first products; the others behind them
+  constexpr uint32_t HALF = 64 * D, HALF_AUX = 512;   // the second block of a buffer
+  const Walks<BK, BQ> walks(p, workers);
+  for (int nth = 0; nth < walks.count; ++nth) {
+  const Walk w = walks.walk(p, blocks, workers, nth);
+  if (w.at >= w.stop) continue;
+  const int tid = each_walk(threadIdx.x), lane = tid & 63, h = lane >> 5, i32 = lane & 31;
+  const int hk = w.hk, L = w.L, k0 = w.k0;
+  const int u0 = k0 + 32 * wave, tk = u0 + i32;       // this lane's key
+  const int window = p.window > 0 && p.window < L ? (int)p.window : 0;
+  if (nth > 0) wait_tiles();                // no wave reads a buffer any more
   int head = w.at / w.each, tile = w.at - head * w.each;   // of the step to load
   int now = tile;                                          // of the step at hand
   auto load_step = [&](int buf) {
     const int hq = hk * G + head, t0 = k0 + tile * BQ;
-    load_tile64<D>(static_cast<const bf16*>(p.q) + (tl.a + t0) * p.ld_q + hq * D, lq2, L - t0, s_t[buf], tid);
-    load_tile64<D>(static_cast<const bf16*>(p.d_o) + ((tl.a + t0) * p.Hq + hq) * (int64_t)D, lg2, L - t0,
+    load_tile64<D>(static_cast<const bf16*>(p.q) + (w.a + t0) * p.ld_q + hq * D, lq2, L - t0, s_t[buf], tid);
+    load_tile64<D>(static_cast<const bf16*>(p.d_o) + ((w.a + t0) * p.Hq + hq) * (int64_t)D, lg2, L - t0,
                    s_t[buf] + BQ * D, tid);
     if (lane < BQ / 4) {                    // a quarter of the statistics to a wave
       const int r = BQ / 4 * wave + lane;
       load_lds16(__builtin_amdgcn_readfirstlane(lds_address(s_aux[buf]) + BQ * 4 * wave),
-                 buffer_at(aux_of(p, hq) + tl.a + t0), 16u * (uint32_t)(r < L - t0 ? r : L - t0 - 1), 0);
+                 buffer_at(aux_of(p, hq) + w.a + t0), 16u * (uint32_t)(r < L - t0 ? r : L - t0 - 1), 0);
     }
     if (++tile == w.each) { tile = 0; ++head; }
   };
@@ -669,7 +869,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
     if (w.at + i < w.stop) load_step(i);
   bf16x8 k[KB], v[KB];
   {
-    const int64_t row = tl.a + (tk < L ? tk : L - 1);
+    const int64_t row = w.a + (tk < L ? tk : L - 1);
     const bf16* kp = static_cast<const bf16*>(p.k) + row * p.ld_k + hk * D + 8 * h;
     const bf16* vp = static_cast<const bf16*>(p.v) + row * p.ld_v + hk * D + 8 * h;
 #pragma unroll
@@ -678,25 +878,12 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
       v[kb] = *reinterpret_cast<const bf16x8*>(vp + 16 * kb);
     }
   }
-  // lanes 0..31 supply the terms of m and l, 32..63 those of D
-  const uint32_t one = 0x3f80;              // 1 in bf16
-  bf16x8 ones_s = __builtin_bit_cast(bf16x8, make_uint4(h == 0 ? one << 16 | one : 0, h == 0 ? one : 0, 0, 0));
-  bf16x8 ones_d = __builtin_bit_cast(bf16x8, make_uint4(h == 1 ? one << 16 | one : 0, h == 1 ? one : 0, 0, 0));
   f32x16 zero, dk[MT], dv[MT];
 #pragma unroll
   for (int r = 0; r < 16; ++r) zero[r] = 0.f;
 #pragma unroll
   for (int c = 0; c < MT; ++c) dk[c] = dv[c] = zero;
-  const LaneReads at = lane_reads<D>(lds_address(s_t), lane);
-  const uint32_t at_aux = lds_address(s_aux) + 16 * i32 + 8 * h;
 
-  auto statistics = [&](uint32_t block) {   // of a block of 32 queries, at BUF-relative byte `block`
-    const uint2 a = lds_read<uint2>(at_aux + block);
-    return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, 0, 0));
-  };
-  constexpr int NF = 2 * KB, NS = 4 * MT;   // first and second products of a block
-  constexpr int AF = 4, AS = 4;             // reads ahead
-  constexpr int E1 = 10;                    // weights formed between first products; the others behind them
   // A block's statistics and the rows of its first AF products, read ahead of it.
   bf16x8 x, ahead[AF];
   auto read_first = [&](uint32_t block, int i) { return rows_at<D>(at.rows + block, i / 2, i % 2 ? GO : 0); };
@@ -782,8 +969,6 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
     keep_a(k[kb]);
     keep_a(v[kb]);
   }
-  keep_a(ones_s);
-  keep_a(ones_d);
   wait_tiles();
   int buf = 0;
   auto next_buf = [](int i) { return (i + 1) % NB; };
@@ -798,9 +983,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
       next_tile(i);
       buf = next_buf(buf);
     }
-    return;
+    continue;
   }
-  constexpr uint32_t HALF = 64 * D, HALF_AUX = 512;   // the second block of a buffer
   {
     x = statistics(0);
     settle(x);
@@ -829,113 +1013,100 @@ __global__ __launch_bounds__(kThreads, 1) void attn_dkv_bf16_kernel(AttnBwdArgs 
   // Rows leave through LDS, so that a store covers whole rows.  The last two buffers but
   // one are read by no wave any more: a quarter of them to a wave.
   bf16* mine = s_t[(buf + 1 + (wave >> 1)) % NB] + (wave & 1) * BQ * D;
-  const int64_t row0 = tl.a + u0;
   const int rows = L - u0 < 32 ? L - u0 : 32;
-  if (parts == 1) {
+  if (w.slot < 0) {
+    const int64_t row0 = w.a + u0;
     rows_out<D>(mine, dk, p.scale, static_cast<TG*>(p.dk) + row0 * p.ld_dk + hk * D, p.ld_dk, rows, lane);
     rows_out<D>(mine, dv, 1.f, static_cast<TG*>(p.dv) + row0 * p.ld_dv + hk * D, p.ld_dv, rows, lane);
   } else {
-    float* to = parts_of(p) + ((part * p.total_T + row0) * p.Hk + hk) * (2 * D);
-    rows_out<D>(mine, dk, p.scale, to, (int64_t)p.Hk * (2 * D), rows, lane);
-    rows_out<D>(mine, dv, 1.f, to + D, (int64_t)p.Hk * (2 * D), rows, lane);
+    float* to = slot_of<D, BK>(p, workers, w.slot) + (int64_t)(32 * wave) * (2 * D);
+    rows_out<D>(mine, dk, p.scale, to, 2 * D, rows, lane);
+    rows_out<D>(mine, dv, 1.f, to + D, 2 * D, rows, lane);
+  }
   }
 }
 
-// The parts of dk and dv added in order, 4 elements to a thread.  Well-formed offsets cover
-// the rows from their first to their last; the others are kept.
-template <typename TG, int D>
-__global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(AttnBwdArgs p, int parts) {
+// The parts of the tiles that several workers share, added in order: 32 rows of the tile
+// that a worker begins to a workgroup.
+template <typename TG, int D, int BK>
+__global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(AttnBwdArgs p, int workers) {
   constexpr int LR = 2 * D / 4;             // threads of a row of dk and dv
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, x = i / LR;
-  const int64_t row = x / p.Hk;
-  const int hk = (int)(x - row * p.Hk), c = 4 * (int)(i - x * LR);
-  if (row >= p.total_T) return;
-  if (p.cu_seqlens && (row < clamp_i64(p.cu_seqlens[0], 0, p.total_T) ||
-                       row >= clamp_i64(p.cu_seqlens[p.N], 0, p.total_T)))
-    return;
-  const float* src = parts_of(p) + x * (2 * D) + c;
-  const int64_t step = p.total_T * p.Hk * (2 * D);
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int worker = blockIdx.x;
+  const Worker t = workers_of(p)[worker];
+  if (t.behind <= 0) return;
+  const int c = 4 * (threadIdx.x % LR), r0 = 32 * blockIdx.y;
+  for (int r = r0 + threadIdx.x / LR; r < r0 + 32 && r < t.rows; r += kThreads / LR) {
+    float4 v = *reinterpret_cast<const float4*>(slot_of<D, BK>(p, workers, 2 * worker + 1) + r * (2 * D) + c);
 #pragma unroll 4
-  for (int n = 0; n < parts; ++n) {
-    const float4 u = *reinterpret_cast<const float4*>(src + n * step);
-    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    for (int i = 1; i <= t.behind; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(slot_of<D, BK>(p, workers, 2 * (worker + i)) + r * (2 * D) + c);
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    const int64_t row = t.row0 + r;
+    if (c < D) store4<TG>(static_cast<TG*>(p.dk) + row * p.ld_dk + t.hk * D + c, v.x, v.y, v.z, v.w);
+    else store4<TG>(static_cast<TG*>(p.dv) + row * p.ld_dv + t.hk * D + c - D, v.x, v.y, v.z, v.w);
   }
-  if (c < D) store4<TG>(static_cast<TG*>(p.dk) + row * p.ld_dk + hk * D + c, v.x, v.y, v.z, v.w);
-  else store4<TG>(static_cast<TG*>(p.dv) + row * p.ld_dv + hk * D + c - D, v.x, v.y, v.z, v.w);
 }
 
-int64_t tiles_of(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int64_t rows) {
-  return packed ? total_T / rows + N : N * ((Tseq + rows - 1) / rows);
-}
-
-int64_t join_blocks(int64_t total_T, int Hk, int d) { return (total_T * Hk * (d / 2) + kThreads - 1) / kThreads; }
 template <typename TG, int D>
-hipError_t launch_join(const AttnBwdArgs& a, int parts, hipStream_t stream) {
-  attn_dkv_join_kernel<TG, D><<<dim3((unsigned)join_blocks(a.total_T, a.Hk, D)), kThreads, 0, stream>>>(a, parts);
+hipError_t launch_bf16(const AttnBwdArgs& a, int workers, hipStream_t stream) {
+  const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, 128);
+  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = workers ? (uint32_t)workers : (uint32_t)(tiles * a.Hk);
+  attn_dq_bf16_kernel<D, TG><<<dim3(nq + plan_blocks(workers)), kThreads, 0, stream>>>(a, nq, workers);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  attn_dkv_bf16_kernel<D, TG><<<dim3(nk), kThreads, 0, stream>>>(a, nk, workers);
+  e = hipGetLastError();
+  if (e != hipSuccess || workers == 0) return e;
+  attn_dkv_join_kernel<TG, D, 128><<<dim3(nk, 4), kThreads, 0, stream>>>(a, workers);
   return hipGetLastError();
 }
-
-template <typename TG, int D>
-hipError_t launch_bf16(const AttnBwdArgs& a, int parts, hipStream_t stream) {
-  const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, 128);
-  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = (uint32_t)(tiles * a.Hk * parts);
-  attn_dq_bf16_kernel<D, TG><<<dim3(nq), kThreads, 0, stream>>>(a, nq);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  attn_dkv_bf16_kernel<D, TG><<<dim3(nk), kThreads, 0, stream>>>(a, nk, parts);
-  e = hipGetLastError();
-  if (e != hipSuccess || parts == 1) return e;
-  return launch_join<TG, D>(a, parts, stream);
-}
 template <int D>
-hipError_t launch_f32(const AttnBwdArgs& a, int parts, hipStream_t stream) {
+hipError_t launch_f32(const AttnBwdArgs& a, int workers, hipStream_t stream) {
   const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, 32);
-  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = (uint32_t)(tiles * a.Hk * parts);
-  attn_dq_f32_kernel<D><<<dim3(nq), kThreads, 0, stream>>>(a, nq);
+  const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = workers ? (uint32_t)workers : (uint32_t)(tiles * a.Hk);
+  attn_dq_f32_kernel<D><<<dim3(nq + plan_blocks(workers)), kThreads, 0, stream>>>(a, nq, workers);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attn_dkv_f32_kernel<D><<<dim3(nk), kThreads, 0, stream>>>(a, nk, parts);
+  attn_dkv_f32_kernel<D><<<dim3(nk), kThreads, 0, stream>>>(a, nk, workers);
   e = hipGetLastError();
-  if (e != hipSuccess || parts == 1) return e;
-  return launch_join<float, D>(a, parts, stream);
+  if (e != hipSuccess || workers == 0) return e;
+  attn_dkv_join_kernel<float, D, 32><<<dim3(nk, 1), kThreads, 0, stream>>>(a, workers);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-// A key tile is walked by several workgroups where there are few tiles: 1024 workgroups
-// keep the CUs evenly busy to the end, but each part's fp32 sums go through memory, and a
-// workgroup takes as long as some 4 steps before and behind its walk, so not below 8
-// steps to a part.
+// Workgroups of the second kind stay on their CU to the end: as many as there is room for.
+// With 8 tiles or more to each of them whole tiles, the dear ones first, are as even and
+// need no join; more sequences than kMaxRanked would take a workgroup long to count.
 AttnBwdPlan attn_bwd_plan(int64_t N, int64_t total_T, int64_t window, int Hq, int Hk, int d, DType io) {
-  const int64_t rows = io == DType::F32 ? 32 : 128, step = io == DType::F32 ? 32 : 64;
-  const int64_t len = N > 0 ? total_T / N : 0;
-  const int64_t tiles = total_T / rows + N, seen = window > 0 && window < len ? 2 * window : len;
-  const int64_t steps = (seen / (2 * step) + 1) * (Hq / Hk);          // of a tile, about
-  int64_t parts = (1024 + tiles * Hk - 1) / (tiles * Hk);
-  if (parts > steps / 8) parts = steps / 8;
-  if (parts < 1) parts = 1;
+  const bool f32 = io == DType::F32;
+  const int64_t rows = f32 ? 32 : 128, room = f32 ? (d == 128 ? 512 : 768) : (d == 128 ? 256 : 512);
+  const int64_t tiles = total_T / rows + N;
+  int64_t workers = 0;
+  if (N <= kMaxRanked && tiles * Hk < 8 * room) {
+    const WalkUnits u{window, (int)rows, f32 ? 32 : 64, Hq / Hk, kLead};
+    const int64_t most = Hk * (u.units(total_T) + N * (2 * u.G + u.lead)) / kLeast + 1;   // shares that there can be
+    workers = most < room ? (most + kXcds - 1) / kXcds * kXcds : room;
+  }
   AttnBwdPlan r;
-  r.parts = (int)parts;
-  r.ws_floats = 4 * total_T * Hq + (parts > 1 ? parts * total_T * Hk * 2 * d : 0);
+  r.workers = (int)workers;
+  r.ws_floats = 4 * total_T * Hq;
+  if (workers) r.ws_floats += 8 * workers + walk_floats(tiles, Hk, (int)workers) + workers * (2 * rows * 2 * d);
   return r;
 }
 
-int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, int Hk, int d,
-                        int parts, DType io) {
-  const int64_t tiles = tiles_of(N, total_T, Tseq, packed, io == DType::F32 ? 32 : 128);
-  int64_t most = tiles * Hq;
-  if (most < tiles * Hk * parts) most = tiles * Hk * parts;
-  if (parts > 1 && most < join_blocks(total_T, Hk, d)) most = join_blocks(total_T, Hk, d);
-  return most;
+int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType io) {
+  return tiles_of(N, total_T, Tseq, packed, io == DType::F32 ? 32 : 128) * Hq + plan_blocks(1024);
 }
 
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, const AttnBwdPlan& plan, hipStream_t stream) {
   if (a.io == DType::F32)
-    return a.d == 128 ? launch_f32<128>(a, plan.parts, stream) : launch_f32<64>(a, plan.parts, stream);
+    return a.d == 128 ? launch_f32<128>(a, plan.workers, stream) : launch_f32<64>(a, plan.workers, stream);
   if (a.grad == DType::F32)
-    return a.d == 128 ? launch_bf16<float, 128>(a, plan.parts, stream) : launch_bf16<float, 64>(a, plan.parts, stream);
-  return a.d == 128 ? launch_bf16<bf16, 128>(a, plan.parts, stream) : launch_bf16<bf16, 64>(a, plan.parts, stream);
+    return a.d == 128 ? launch_bf16<float, 128>(a, plan.workers, stream) : launch_bf16<float, 64>(a, plan.workers, stream);
+  return a.d == 128 ? launch_bf16<bf16, 128>(a, plan.workers, stream) : launch_bf16<bf16, 64>(a, plan.workers, stream);
 }
 
 #ifdef GDN_CHECK

@@ -185,7 +185,7 @@ __global__ __launch_bounds__(128 * KW, KW == 4 ? 2 : D == 64 ? 4 : 3) void prefi
   __shared__ float s_m[KW - 1][32], s_l[KW - 1][32];
   lds_nan_fill(s_kv, sizeof s_kv);
   float *s_k = s_kv, *s_v = s_kv + BN * LD;
-  const Tile tl = find_tile<BM>(tile_args(p), blocks);
+  const Tile tl = find_tile<BM>(tile_args(p), blockIdx.x, blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
   __shared__ __align__(16) bf16 s_k[2][STEP * D], s_v[2][STEP * D];
   lds_nan_fill(s_k, sizeof s_k);
   lds_nan_fill(s_v, sizeof s_v);
-  const Tile tl = find_tile<BM>(tile_args(p), blocks);
+  const Tile tl = find_tile<BM>(tile_args(p), blockIdx.x, blocks);
   if (!tl.valid) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);

@@ -42,9 +42,8 @@ constexpr uint32_t kXcds = 8;
 constexpr int64_t kMaxRanked = 1024;      // sequences that are ranked; more keep their order
 
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const TileArgs& p, uint32_t blocks) {
+__device__ __forceinline__ Tile find_tile(const TileArgs& p, uint32_t blk, uint32_t blocks) {
   Tile t;
-  const uint32_t blk = blockIdx.x;
   const uint32_t G = (uint32_t)p.G, Hk = (uint32_t)p.Hk, N = (uint32_t)p.N;
   const uint32_t per = blocks / kXcds;                    // full rounds over the XCDs
   const uint32_t xcd = blk % kXcds, i = blk / kXcds;

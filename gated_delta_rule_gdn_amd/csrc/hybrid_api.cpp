@@ -181,8 +181,8 @@ gdn_status gdn_attn_backward(const gdn_attn_bwd_desc* d, const int64_t* cu_seqle
   if (d->total_T == 0) return GDN_OK;
   const int64_t Tseq = cu_seqlens ? 0 : d->total_T / d->N;
   const gdn::AttnBwdPlan plan = bwd_plan(d);
-  if ((double)gdn::attn_bwd_blocks(d->N, d->total_T, Tseq, cu_seqlens != nullptr, d->H_q, d->H_k,
-                                   d->d, plan.parts, to_dtype(d->io_dtype)) * 256.0 > kMaxThreads)
+  if ((double)gdn::attn_bwd_blocks(d->N, d->total_T, Tseq, cu_seqlens != nullptr, d->H_q,
+                                   to_dtype(d->io_dtype)) * 256.0 > kMaxThreads)
     return GDN_ERR_UNSUPPORTED;
   const void* all[] = {q, k, v, o, d_o, stats, dq, dk, dv};
   for (const void* p : all)

@@ -21,17 +21,16 @@ struct AttnBwdArgs {
   float* ws;                          // attn_bwd_plan(...).ws_floats
 };
 
-// How a backward call divides its key tiles: workgroups to each of them (they
-// join through the workspace where there are several), and the workspace.
+// How a backward call divides its key tiles: equal shares of all of them to so many
+// workgroups (0: one to each tile), and the workspace.
 struct AttnBwdPlan {
-  int parts;
+  int workers;
   int64_t ws_floats;
 };
 AttnBwdPlan attn_bwd_plan(int64_t N, int64_t total_T, int64_t window, int Hq, int Hk, int d,
                           DType io);
 // The most workgroups of any launch (checked against the grid limit by the caller).
-int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, int Hk, int d,
-                        int parts, DType io);
+int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType io);
 
 struct QkNormRopeBwdArgs {
   int64_t rows, ld_q, ld_k, ld_dq, ld_dk;

@@ -21,10 +21,8 @@ int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, in
 AttnBwdPlan attn_bwd_plan(int64_t, int64_t total_T, int64_t, int Hq, int Hk, int d, DType) {
   return AttnBwdPlan{8, 4 * total_T * Hq + 8 * total_T * Hk * 2 * d};
 }
-int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, int Hk, int, int parts,
-                        DType) {
-  const int64_t t = packed ? total_T / 32 + N : N * ((Tseq + 31) / 32);
-  return t * (Hq > Hk * parts ? Hq : Hk * parts);
+int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType) {
+  return (packed ? total_T / 32 + N : N * ((Tseq + 31) / 32)) * Hq;
 }
 int64_t qk_bwd_ws_floats(int64_t rows, int Hq, int Hk, int d) { return rows > 0 ? ((int64_t)Hq + Hk) * 8 * d : 0; }
 int64_t add_norm_bwd_ws_floats(int64_t rows, int C) { return (rows < 512 ? rows : 512) * C; }
