@@ -81,7 +81,7 @@ __device__ __forceinline__ float* slot_of(const AttnBwdArgs& p, int workers, int
 // workgroups of the dq kernel, a wave to a worker.
 // ---------------------------------------------------------------------------
 constexpr int kLead = 4;                    // steps that a walk's beginning and end are worth
-constexpr int64_t kLeast = 8;               // units of a share
+constexpr int64_t kLeast = 3;               // units of a share
 constexpr int plan_blocks(int workers) { return (workers + 8 * 4 - 1) / (8 * 4) * 8; }   // whole rounds of the XCDs
 
 __device__ __forceinline__ int64_t length_of(const AttnBwdArgs& p, int64_t i) {
@@ -770,9 +770,9 @@ __device__ __forceinline__ void product_a(f32x16& acc, const bf16x8& a, const bf
   asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 #endif
 }
-__device__ __forceinline__ void settle(bf16x8& a) {
+__device__ __forceinline__ void settle(bf16x8& a, bf16x8& b) {
 #if __HIP_DEVICE_COMPILE__
-  asm volatile("s_nop 1" : "+v"(a));
+  asm volatile("s_nop 1" : "+v"(a), "+v"(b));
 #endif
 }
 // Behind it the sums can be read, or copied by the compiler: it stands at the end of each
@@ -789,6 +789,12 @@ __device__ __forceinline__ void products_done(f32x16* a, f32x16* b) {
 __device__ __forceinline__ void products_done(f32x16& a, f32x16& b) {
 #if __HIP_DEVICE_COMPILE__
   asm volatile("s_nop 11" : "+v"(a), "+v"(b));
+#endif
+}
+// Both have been read from LDS: one wait instead of two.
+__device__ __forceinline__ void both_there(const bf16x8& a, const bf16x8& b) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("" ::"v"(a), "v"(b));
 #endif
 }
 // What is behind reads x where it stands now.
@@ -822,24 +828,29 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float c_scale = p.scale * kLog2e;
   const uint32_t lq2 = (uint32_t)p.ld_q * 2, lg2 = (uint32_t)p.Hq * D * 2;
+  // a thread's part of a tile: row r0 and every RL-th behind it, whose chunks are the same
+  constexpr int CH = D / 8, RL = kThreads / CH, NL = BQ / RL;
+  static_assert(RL % 16 == 0, "chunks repeat after 16 rows");
+  const int r0 = threadIdx.x / CH;
+  const uint32_t chunk = 16 * chunk_at<D>(r0, threadIdx.x % CH);
+  const uint32_t off_q = r0 * lq2 + chunk, off_g = r0 * lg2 + chunk;
+  const uint32_t lds_t = __builtin_amdgcn_readfirstlane(lds_address(s_t)) + 1024 * wave;
+  const uint32_t lds_aux = __builtin_amdgcn_readfirstlane(lds_address(s_aux)) + BQ * 4 * wave;
 
-  // lanes 0..31 supply the terms of m and l, 32..63 those of D
+  // lanes 0..31 supply the terms, those of m and l first; what 32..63 supply counts for nothing
   const uint32_t one = 0x3f80;              // 1 in bf16
   const bool low = (threadIdx.x & 32) == 0;
   bf16x8 ones_s = __builtin_bit_cast(bf16x8, make_uint4(low ? one << 16 | one : 0, low ? one : 0, 0, 0));
-  bf16x8 ones_d = __builtin_bit_cast(bf16x8, make_uint4(low ? 0 : one << 16 | one, low ? 0 : one, 0, 0));
+  bf16x8 ones_d = __builtin_bit_cast(bf16x8, make_uint4(0, 0, low ? one << 16 | one : 0, low ? one : 0));
   const LaneReads at = lane_reads<D>(lds_address(s_t), threadIdx.x & 63);
-  const uint32_t at_aux = lds_address(s_aux) + 16 * (threadIdx.x & 31) + (low ? 0 : 8);
+  const uint32_t at_aux = lds_address(s_aux) + 16 * (threadIdx.x & 31);
 
-  auto statistics = [&](uint32_t block) {   // of a block of 32 queries, at BUF-relative byte `block`
-    const uint2 a = lds_read<uint2>(at_aux + block);
-    return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, 0, 0));
-  };
+  auto statistics = [&](uint32_t block) { return lds_read<bf16x8>(at_aux + block); };   // of 32 queries
   keep_a(ones_s);
   keep_a(ones_d);
   constexpr int NF = 2 * KB, NS = 4 * MT;   // first and second products of a block
   constexpr int AF = 4, AS = 4;             // reads ahead
-  constexpr int E1 = 10;                    // weights formed between first products; the others behind them
+  constexpr int E1 = 12;                    // weights' slots between first products; the others behind them
   constexpr uint32_t HALF = 64 * D, HALF_AUX = 512;   // the second block of a buffer
   const Walks<BK, BQ> walks(p, workers);
   for (int nth = 0; nth < walks.count; ++nth) {
@@ -852,17 +863,47 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
   if (nth > 0) wait_tiles();                // no wave reads a buffer any more
   int head = w.at / w.each, tile = w.at - head * w.each;   // of the step to load
   int now = tile;                                          // of the step at hand
+  const bf16 *q_at, *g_at;                  // that step's first rows
+  const uint4* aux_at;
+  auto head_at = [&]() {
+    const int hq = hk * G + head;
+    const int64_t row = w.a + k0 + tile * BQ;
+    q_at = static_cast<const bf16*>(p.q) + row * p.ld_q + hq * D;
+    g_at = static_cast<const bf16*>(p.d_o) + (row * p.Hq + hq) * (int64_t)D;
+    aux_at = aux_of(p, hq) + row;
+  };
+  head_at();
   auto load_step = [&](int buf) {
-    const int hq = hk * G + head, t0 = k0 + tile * BQ;
-    load_tile64<D>(static_cast<const bf16*>(p.q) + (w.a + t0) * p.ld_q + hq * D, lq2, L - t0, s_t[buf], tid);
-    load_tile64<D>(static_cast<const bf16*>(p.d_o) + ((w.a + t0) * p.Hq + hq) * (int64_t)D, lg2, L - t0,
-                   s_t[buf] + BQ * D, tid);
+    const i32x4 rq = buffer_at(q_at), rg = buffer_at(g_at), ra = buffer_at(aux_at);
+    const uint32_t to = lds_t + buf * BUF, to_aux = lds_aux + buf * (BQ * 16);
+    const int rows = L - k0 - tile * BQ;    // that there are; the last one repeats (what it gives is masked)
+    if (rows >= BQ) {
+#pragma unroll
+      for (int e = 0; e < NL; ++e) {
+        load_lds16(to + e * 4096, rq, off_q, e * RL * lq2);
+        load_lds16(to + GO + e * 4096, rg, off_g, e * RL * lg2);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < NL; ++e) {
+        const int r = r0 + e * RL < rows ? r0 + e * RL : rows - 1;
+        load_lds16(to + e * 4096, rq, r * lq2 + chunk, 0);
+        load_lds16(to + GO + e * 4096, rg, r * lg2 + chunk, 0);
+      }
+    }
     if (lane < BQ / 4) {                    // a quarter of the statistics to a wave
       const int r = BQ / 4 * wave + lane;
-      load_lds16(__builtin_amdgcn_readfirstlane(lds_address(s_aux[buf]) + BQ * 4 * wave),
-                 buffer_at(aux_of(p, hq) + w.a + t0), 16u * (uint32_t)(r < L - t0 ? r : L - t0 - 1), 0);
+      load_lds16(to_aux, ra, 16u * (uint32_t)(r < rows ? r : rows - 1), 0);
     }
-    if (++tile == w.each) { tile = 0; ++head; }
+    if (++tile == w.each) {
+      tile = 0;
+      ++head;
+      head_at();
+    } else {
+      q_at += BQ * p.ld_q;
+      g_at += BQ * (int64_t)p.Hq * D;
+      aux_at += BQ;
+    }
   };
 #pragma unroll
   for (int i = 0; i < NB - 1; ++i)
@@ -907,18 +948,24 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
     const uint32_t cols = at.cols + cur;
     bf16x8 f[NF], g[NS], pw[2], dw[2];
     auto read_second = [&](int j) { g[j] = columns_at<D>(cols, j / (2 * MT), j / 2 % MT, j % 2 ? 0 : GO); };
+    // The weights in three stages, so that none waits for the one before it: slot n begins
+    // weight n, takes weight n - 1 to the power and finishes weight n - 2.
+    float y[16], pr[16];
     auto weights = [&](int from, int to) {
 #pragma unroll
-      for (int e = from; e < to; ++e) {
-        const float pr = exp2_fast(s[e] * c_scale);
-        pw[e / 8][e % 8] = (bf16)pr;
-        dw[e / 8][e % 8] = (bf16)(pr * dp[e]);
+      for (int n = from; n < to; ++n) {
+        if (n >= 2) {
+          const int e = n - 2;
+          pw[e / 8][e % 8] = (bf16)pr[e];
+          dw[e / 8][e % 8] = (bf16)(pr[e] * dp[e]);
+        }
+        if (n < 16) y[n] = s[n] * c_scale;
+        if (n >= 1 && n < 17) pr[n - 1] = exp2_fast(y[n - 1]);
       }
     };
 #pragma unroll
     for (int i = 0; i < AF; ++i) f[i] = ahead[i];
     __builtin_amdgcn_sched_barrier(0);
-    settle(x);
     product_v0(sn, x, ones_s);
     product_v0(dpn, x, ones_d);
 #pragma unroll
@@ -930,13 +977,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
           if (n + AF < NF) f[n + AF] = read_first(next, n + AF);
           if (n >= NF - AS) read_second(n - (NF - AS));
         }
+        both_there(f[i], f[i + 1]);
       }
       if (i % 2 == 0) product_v(sn, f[i], k[i / 2]);
       else product_v(dpn, f[i], v[i / 2]);
       weights(E1 * i / NF, E1 * (i + 1) / NF);
     }
-    settle(pw[0]);
-    settle(dw[0]);
+    settle(pw[0], dw[0]);
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
       __builtin_amdgcn_sched_barrier(0);
@@ -946,18 +993,16 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
           if (n + AS < NS) read_second(n + AS);
           else if (n + AS - NS < AF) ahead[n + AS - NS] = read_first(after, n + AS - NS);
         }
+        both_there(g[j], g[j + 1]);
       }
-      if (j == NS / 2) {
-        settle(pw[1]);
-        settle(dw[1]);
-      }
+      if (j == NS / 2) settle(pw[1], dw[1]);
       if (j == NS - 1) x = statistics(after_aux);
       const int b = j / (2 * MT), c = j / 2 % MT;
       if (j % 2 == 0) product_a(dv[c], g[j], pw[b]);
       else product_a(dk[c], g[j], dw[b]);
-      if (j < NS / 2) weights(E1 + (16 - E1) * j / (NS / 2), E1 + (16 - E1) * (j + 1) / (NS / 2));
+      if (j < NS / 2) weights(E1 + (18 - E1) * j / (NS / 2), E1 + (18 - E1) * (j + 1) / (NS / 2));
     }
-    static_assert(AS >= AF && NS >= 8, "every read has its line; products behind the scores");
+    static_assert(AS >= AF && NS >= 8 && E1 >= 10, "every read has its line; products behind the scores; 8 weights before them");
     __builtin_amdgcn_sched_barrier(0);
     behind_v(sn);
     behind_v(dpn);
@@ -987,7 +1032,6 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
   }
   {
     x = statistics(0);
-    settle(x);
     product_v0(s, x, ones_s);
     product_v0(dp, x, ones_d);
 #pragma unroll
