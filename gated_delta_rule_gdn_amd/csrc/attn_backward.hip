@@ -151,10 +151,13 @@ __device__ __forceinline__ void plan_worker(const AttnBwdArgs& p, int workers, i
     int hk = (int)(r / per);
     int64_t j = u.tile_at(L, r - hk * per);
     int64_t from = base + hk * per + u.before(L, j);
-    // each tile has a place of its own in the list, and each worker one more
-    me.first = (int)(tiles * p.Hk + hk * u.tiles(L) + j + worker);
+    // each tile has a place of its own in the list, and each worker one more (ranges that
+    // overlap can have more tiles than there is room for: those are not walked)
+    const int64_t place = tiles * p.Hk + hk * u.tiles(L) + j + worker;
+    const int64_t room = tiles_of(p.N, p.total_T, p.Tseq, p.cu_seqlens != nullptr, BK) * p.Hk + workers - place;
+    me.first = room > 0 ? (int)place : 0;
     Walk* to = walks_of(p, workers) + me.first;
-    while (x < end) {
+    while (x < end && me.count < room) {
       const WalkPart w = part_of(u, L, j, from, x, end);
       if (w.s1 > w.s0) {
         const Walk t{a, (int)L, (int)(j * BK), hk, (int)(w.all / u.G), (int)w.s0, (int)w.s1,

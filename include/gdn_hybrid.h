@@ -78,7 +78,8 @@ size_t gdn_attn_backward_workspace_size(const gdn_attn_bwd_desc* desc);
  *
  * Sums in fp32; with bf16 io, p and e are rounded to bf16 for the products that
  * use them, and o is what the forward rounded.  p carries the rounding of scores
- * and of m in fp32: 2^-23 times the larger of them, relative.
+ * and of m in fp32, relative 2^-23 times the larger of them: scores (times
+ * log2 e) of 2^20 and more have no meaningful gradients.
  * Non-finite inputs: what is not finite in a token makes gradients of its own
  * sequence, in the heads concerned, unspecified; other sequences and heads, and
  * tokens further than the window and 256 more from it, are not touched by it.

@@ -232,3 +232,8 @@ def _run(tmp_path, name, sources):
 def test_validation_clean_under_asan_and_ubsan(tmp_path):
     here = os.path.join(ROOT, "tests", "abi_check")
     _run(tmp_path, "hybrid_check", [os.path.join(CSRC, "hybrid_api.cpp"), os.path.join(here, "hybrid_check.cpp")])
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_shares_of_the_backward_walks_are_equal_and_complete(tmp_path):
+    _run(tmp_path, "attn_walk_check", [os.path.join(ROOT, "tests", "abi_check", "attn_walk_check.cpp")])
