@@ -13,6 +13,7 @@
 #include "rope_device.hpp"
 
 #include "hybrid_kernels.hpp"
+#include "join_parts.hpp"
 
 namespace gdn {
 namespace {
@@ -21,7 +22,7 @@ constexpr int kThreads = 256;
 constexpr int kHeads = 2;                     // heads of a thread, sharing the angles
 // Workgroups that loop over the tokens: each leaves one partial gradient of the
 // weights, and they are joined in a fixed order.
-constexpr int64_t kBlocks = 2048;
+constexpr int64_t kBlocks = 4096;
 
 struct Split {
   int gq, gk;                                 // groups of kHeads heads of each operand
@@ -35,6 +36,21 @@ __host__ __device__ inline Split split_of(int64_t rows, int Hq, int Hk, int d) {
   const int64_t need = (rows + tokens - 1) / tokens, most = kBlocks / (s.gq + s.gk);
   s.tb = need < most ? need : (most > 1 ? most : 1);
   return s;
+}
+
+// Sum over a wave's lanes that are equal modulo LPR (4 or 8), in the vector unit.
+template <int LPR>
+__device__ __forceinline__ float over_tokens(float s) {
+  auto dpp = [](float v, auto ctrl) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+        0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  s += dpp(s, std::integral_constant<int, 0x128>{});                         // row_ror:8
+  if constexpr (LPR == 4) s += dpp(s, std::integral_constant<int, 0x124>{});  // row_ror:4
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+  s = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 template <typename T, typename G, int D, bool INTER>
@@ -122,9 +138,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(QkNormRopeBw
   // over the wave's tokens, the workgroup's waves, then (below) the workgroups
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-#pragma unroll
-    for (int off = LPR; off < 64; off *= 2) acc[e] += __shfl_xor(acc[e], off);
+  for (int e = 0; e < 16; ++e) acc[e] = over_tokens<LPR>(acc[e]);
   if (lane < LPR) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) s_w[wave][(e < 8 ? m.c0 : m.c1 - 8) + e] = acc[e];
@@ -137,31 +151,16 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(QkNormRopeBw
                                                   (s_w[2][threadIdx.x] + s_w[3][threadIdx.x]);
 }
 
-// Sum of the workgroups' partial weight gradients: one workgroup for 16 channels of an operand,
-// 64 threads to a channel, each with several loads on their way (1816 parts of 128
-// channels: 42 us with 16 threads and one load at a time, XX us so).
-constexpr int kJoin = 64;
+// Sum of the workgroups' partial weight gradients: one workgroup for 16 channels of an operand.
+constexpr int kJoinThreads = 1024;
 template <int D>
-__global__ __launch_bounds__(16 * kJoin) void qk_weight_join_kernel(QkNormRopeBwdArgs p) {
-  __shared__ float s[kJoin][17];
-  lds_nan_fill(s, sizeof s);
+__global__ __launch_bounds__(kJoinThreads) void qk_weight_join_kernel(QkNormRopeBwdArgs p) {
   const bool is_q = blockIdx.y == 0;
   float* to = is_q ? p.dq_weight : p.dk_weight;
   if (!to) return;
   const Split sp = split_of(p.rows, p.Hq, p.Hk, D);
-  const int n = (int)sp.tb * (is_q ? sp.gq : sp.gk);
-  const int col = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const float* src = p.ws + (is_q ? 0 : sp.tb * sp.gq * D) + 16 * blockIdx.x + col;
-  float v = 0.f;
-#pragma unroll 8
-  for (int i = part; i < n; i += kJoin) v += src[(int64_t)i * D];
-  s[part][col] = v;
-  __syncthreads();
-  if (part == 0) {
-#pragma unroll 8
-    for (int i = 1; i < kJoin; ++i) v += s[i][col];
-    to[16 * blockIdx.x + col] = v;
-  }
+  join_parts<kJoinThreads>(p.ws + (is_q ? 0 : sp.tb * sp.gq * D), D, (int)sp.tb * (is_q ? sp.gq : sp.gk),
+                           16 * blockIdx.x, D, to);
 }
 
 template <typename T, typename G, int D>
@@ -175,7 +174,7 @@ hipError_t launch_d(const QkNormRopeBwdArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (!a.dq_weight && !a.dk_weight) return hipSuccess;
-  qk_weight_join_kernel<D><<<dim3(D / 16, 2), 16 * kJoin, 0, stream>>>(a);
+  qk_weight_join_kernel<D><<<dim3(D / 16, 2), kJoinThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 template <typename T, typename G>

@@ -16,6 +16,7 @@
 #include "attn_device.hpp"
 
 #include "hybrid_kernels.hpp"
+#include "join_parts.hpp"
 
 namespace gdn {
 namespace {
@@ -279,22 +280,9 @@ __global__ __launch_bounds__(kThreads) void add_norm_bwd_kernel(AddNormBwdArgs p
   }
 }
 
-// 16 channels to a workgroup, 16 threads to a channel.
+// 16 channels to a workgroup.
 __global__ __launch_bounds__(kThreads) void weight_join_kernel(const float* ws, float* out, int C, int parts) {
-  __shared__ float s[16][17];
-  const int col = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
-  float v = 0.f;
-  if (col < C) {
-#pragma unroll 8
-    for (int i = part; i < parts; i += 16) v += ws[(int64_t)i * C + col];
-  }
-  s[part][threadIdx.x & 15] = v;
-  __syncthreads();
-  if (part == 0 && col < C) {
-    v = s[0][threadIdx.x];
-    for (int i = 1; i < 16; ++i) v += s[i][threadIdx.x];
-    out[col] = v;
-  }
+  join_parts<kThreads>(ws, C, parts, 16 * blockIdx.x, C, out);
 }
 
 template <typename TX, typename TR, bool CODES>
