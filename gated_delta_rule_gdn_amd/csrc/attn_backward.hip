@@ -1073,25 +1073,36 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
   }
 }
 
-// The parts of the tiles that several workers share, added in order: 32 rows of the tile
-// that a worker begins to a workgroup.
+// The parts of the tiles that several workers share, added in order: 16 rows of the tile
+// that a worker begins to a workgroup, several parts on their way at a time.
 template <typename TG, int D, int BK>
 __global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(AttnBwdArgs p, int workers) {
   constexpr int LR = 2 * D / 4;             // threads of a row of dk and dv
   const int worker = blockIdx.x;
   const Worker t = workers_of(p)[worker];
   if (t.behind <= 0) return;
-  const int c = 4 * (threadIdx.x % LR), r0 = 32 * blockIdx.y;
-  for (int r = r0 + threadIdx.x / LR; r < r0 + 32 && r < t.rows; r += kThreads / LR) {
-    float4 v = *reinterpret_cast<const float4*>(slot_of<D, BK>(p, workers, 2 * worker + 1) + r * (2 * D) + c);
+  constexpr int RB = kThreads / LR, R = 16 / RB;      // rows at a time, and of a thread
+  const int c = 4 * (threadIdx.x % LR), r0 = 16 * blockIdx.y + threadIdx.x / LR;
+  if (16 * blockIdx.y >= t.rows) return;
+  // (rows behind the tile's last read what the slots hold there, and are not written)
+  float4 v[R];
+  const float* first = slot_of<D, BK>(p, workers, 2 * worker + 1) + r0 * (2 * D) + c;
+#pragma unroll
+  for (int r = 0; r < R; ++r) v[r] = *reinterpret_cast<const float4*>(first + r * RB * (2 * D));
+  const float* src = slot_of<D, BK>(p, workers, 2 * worker + 2) + r0 * (2 * D) + c;
 #pragma unroll 4
-    for (int i = 1; i <= t.behind; ++i) {
-      const float4 x = *reinterpret_cast<const float4*>(slot_of<D, BK>(p, workers, 2 * (worker + i)) + r * (2 * D) + c);
-      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+  for (int i = 0; i < t.behind; ++i, src += 2 * (BK * 2 * D))
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float4 x = *reinterpret_cast<const float4*>(src + r * RB * (2 * D));
+      v[r].x += x.x; v[r].y += x.y; v[r].z += x.z; v[r].w += x.w;
     }
-    const int64_t row = t.row0 + r;
-    if (c < D) store4<TG>(static_cast<TG*>(p.dk) + row * p.ld_dk + t.hk * D + c, v.x, v.y, v.z, v.w);
-    else store4<TG>(static_cast<TG*>(p.dv) + row * p.ld_dv + t.hk * D + c - D, v.x, v.y, v.z, v.w);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (r0 + r * RB >= t.rows) break;
+    const int64_t row = t.row0 + r0 + r * RB;
+    if (c < D) store4<TG>(static_cast<TG*>(p.dk) + row * p.ld_dk + t.hk * D + c, v[r].x, v[r].y, v[r].z, v[r].w);
+    else store4<TG>(static_cast<TG*>(p.dv) + row * p.ld_dv + t.hk * D + c - D, v[r].x, v[r].y, v[r].z, v[r].w);
   }
 }
 
@@ -1105,7 +1116,7 @@ hipError_t launch_bf16(const AttnBwdArgs& a, int workers, hipStream_t stream) {
   attn_dkv_bf16_kernel<D, TG><<<dim3(nk), kThreads, 0, stream>>>(a, nk, workers);
   e = hipGetLastError();
   if (e != hipSuccess || workers == 0) return e;
-  attn_dkv_join_kernel<TG, D, 128><<<dim3(nk, 4), kThreads, 0, stream>>>(a, workers);
+  attn_dkv_join_kernel<TG, D, 128><<<dim3(nk, 8), kThreads, 0, stream>>>(a, workers);
   return hipGetLastError();
 }
 template <int D>
@@ -1118,7 +1129,7 @@ hipError_t launch_f32(const AttnBwdArgs& a, int workers, hipStream_t stream) {
   attn_dkv_f32_kernel<D><<<dim3(nk), kThreads, 0, stream>>>(a, nk, workers);
   e = hipGetLastError();
   if (e != hipSuccess || workers == 0) return e;
-  attn_dkv_join_kernel<float, D, 32><<<dim3(nk, 1), kThreads, 0, stream>>>(a, workers);
+  attn_dkv_join_kernel<float, D, 32><<<dim3(nk, 2), kThreads, 0, stream>>>(a, workers);
   return hipGetLastError();
 }
 
