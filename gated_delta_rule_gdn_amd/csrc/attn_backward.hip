@@ -585,9 +585,11 @@ __device__ __forceinline__ void rows_out(bf16* lds, const f32x16* acc, float f, 
   }
 }
 
-template <int D, typename TG>
+// SPLIT 2: 64 queries to a workgroup, each 32 of them to two waves that take 32 keys of a
+// tile each and add their sums at the end (see split_dq).
+template <int D, typename TG, int SPLIT>
 __global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
-  constexpr int BM = 128, BN = 64, KB = D / 16, MT = D / 32;
+  constexpr int BM = 128 / SPLIT, BN = 64, KB = D / 16, MT = D / 32;
   constexpr int KEYS = 128, STEP = 64;      // of the dk and dv kernel
   __shared__ __align__(16) bf16 s_k[2][BN * D], s_v[2][BN * D];
   lds_nan_fill(s_k, sizeof s_k);
@@ -605,7 +607,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p
   const int hk = tl.hq / G;
   const int L = __builtin_amdgcn_readfirstlane((int)tl.L);
   const int qt0 = __builtin_amdgcn_readfirstlane((int)tl.q0);
-  const int q0 = qt0 + 32 * wave, tq = q0 + i32;
+  const int q0 = qt0 + 32 * (wave / SPLIT), tq = q0 + i32, part = wave % SPLIT;
   const bf16* kb_ = static_cast<const bf16*>(p.k) + tl.a * p.ld_k + hk * D;
   const bf16* vb_ = static_cast<const bf16*>(p.v) + tl.a * p.ld_v + hk * D;
   const uint32_t lk2 = (uint32_t)p.ld_k * 2, lv2 = (uint32_t)p.ld_v * 2;
@@ -635,7 +637,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p
     dl += __shfl_xor(dl, 32);
     const float2 st = reinterpret_cast<const float2*>(p.stats)[row * p.Hq + tl.hq];
     lse = st.x + __builtin_amdgcn_logf(st.y);
-    if (h == 0 && tq < L) {
+    if (h == 0 && part == 0 && tq < L) {
       const uint2 a = three_terms(-lse / c_scale), b = three_terms(-dl);
       aux_of(p, tl.hq)[row] = make_uint4(a.x, a.y, b.x, b.y);
     }
@@ -655,8 +657,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p
     }
     if (q0 >= L) continue;
 #pragma unroll
-    for (int sub = 0; sub < BN; sub += 32) {
-      const int kw = k0 + sub;
+    for (int at = 0; at < BN; at += 32 * SPLIT) {
+      const int sub = at + 32 * part, kw = k0 + sub;
       if (kw > q0 + 31 || (window && kw + 31 <= q0 - window)) continue;   // nothing seen
       f32x16 s, dp;
 #pragma unroll
@@ -688,9 +690,30 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p
     }
   }
   wait_tiles();                             // the key tiles are free
-  if (q0 >= L) return;
-  static_assert(sizeof s_k + sizeof s_v >= 128 * D * sizeof(TG), "the rows fit");
+  static_assert(sizeof s_k + sizeof s_v >= BM * D * sizeof(TG), "the rows fit");
   bf16* mine = (wave < 2 ? s_k[0] : s_v[0]) + (wave & 1) * BN * D;
+  if constexpr (SPLIT == 2) {               // both waves of 32 queries have tiles of their own
+    static_assert(sizeof s_k >= 32 * D * sizeof(float) && sizeof s_v >= 32 * D * sizeof(float), "the sums fit");
+    float4* sums = reinterpret_cast<float4*>(wave < 2 ? s_k[0] : s_v[0]) + lane;
+#pragma unroll
+    for (int i = 0; i < 4 * MT; ++i) {
+      const f32x16& x = dq[i / 4];
+      const int r = i % 4 * 4;
+      lds_check(sums + 64 * i, 16);
+      if (part == 1) sums[64 * i] = make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
+    }
+    __syncthreads();
+    if (part == 1) return;
+#pragma unroll
+    for (int i = 0; i < 4 * MT; ++i) {
+      f32x16& x = dq[i / 4];
+      const int r = i % 4 * 4;
+      lds_check(sums + 64 * i, 16);
+      const float4 y = sums[64 * i];
+      x[r] += y.x; x[r + 1] += y.y; x[r + 2] += y.z; x[r + 3] += y.w;
+    }
+  }
+  if (q0 >= L) return;
   rows_out<D>(mine, dq, p.scale, static_cast<TG*>(p.dq) + (tl.a + q0) * p.ld_dq + tl.hq * D, p.ld_dq, L - q0, lane);
 }
 
@@ -1106,11 +1129,27 @@ __global__ __launch_bounds__(kThreads) void attn_dkv_join_kernel(AttnBwdArgs p, 
   }
 }
 
+// The dq kernel with 64 queries to a workgroup instead of 128, where a CU would otherwise
+// have room left for workgroups (us of a whole backward call, 128 / 64).  d 128: 2048 tokens,
+// 8 heads (128 workgroups of 128 queries) 106 / 80; 4096 tokens, 8 heads (256) 212 / 166;
+// 8192 tokens, 8 heads (512) 537 / 494; 4 prompts of 512, 32 heads (512) 83 / 86; 12
+// prompts, 8191 tokens, 8 heads (600) 124 / 113; 2048 tokens, 40 heads (640) 188 / 196;
+// 8192 tokens, 12 heads (768) 705 / 717.  d 64: 29 prompts, 8191 tokens, 6 heads (552)
+// 61 / 54; 4096 tokens, 20 heads (640) 203 / 193; 8192 tokens, 12 heads (768) 409 / 399,
+// 16 heads (1024) 506 / 512; 2048 tokens, 64 heads (1024) 162 / 167.
+bool split_dq(int64_t blocks, int d) { return blocks <= (d == 128 ? 512 : 768); }
+
 template <typename TG, int D>
 hipError_t launch_bf16(const AttnBwdArgs& a, int workers, hipStream_t stream) {
-  const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, 128);
+  const bool packed = a.cu_seqlens != nullptr;
+  const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, packed, 128);
   const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = workers ? (uint32_t)workers : (uint32_t)(tiles * a.Hk);
-  attn_dq_bf16_kernel<D, TG><<<dim3(nq + plan_blocks(workers)), kThreads, 0, stream>>>(a, nq, workers);
+  if (split_dq(nq, D)) {
+    const uint32_t twice = (uint32_t)(tiles_of(a.N, a.total_T, a.Tseq, packed, 64) * a.Hq);
+    attn_dq_bf16_kernel<D, TG, 2><<<dim3(twice + plan_blocks(workers)), kThreads, 0, stream>>>(a, twice, workers);
+  } else {
+    attn_dq_bf16_kernel<D, TG, 1><<<dim3(nq + plan_blocks(workers)), kThreads, 0, stream>>>(a, nq, workers);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   attn_dkv_bf16_kernel<D, TG><<<dim3(nk), kThreads, 0, stream>>>(a, nk, workers);

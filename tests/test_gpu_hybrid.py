@@ -98,6 +98,18 @@ def test_attention_many_sequences():
         check_attn(got, host, bounds, 0, None, dtype, what="many")
 
 
+@pytest.mark.parametrize("grad", [BF, F32])
+@pytest.mark.parametrize("Hq,Hk,d,window", [(32, 4, 128, 0), (32, 8, 128, 50), (48, 6, 64, 0), (50, 10, 64, 50)])
+def test_attention_of_many_heads(Hq, Hk, d, window, grad):
+    """So many query tiles that each takes 128 queries."""
+    announce(f"attn backward many heads Hq={Hq} Hk={Hk} d={d} window={window} {grad}")
+    bounds = np.concatenate([[0], np.cumsum([1 + 37 * i % 97 for i in range(20)] + [161, 0, 257])]).tolist()
+    host, on = case(bounds[-1], Hq, Hk, d, BF, Hq + d)
+    _, _, got = both(on, cu_seqlens=torch.tensor(bounds).cuda(), window=window, grad_dtype=grad)
+    torch.cuda.synchronize()
+    check_attn(got, host, bounds, window, None, BF, grad, "many heads")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_gradients_in_fp32_into_column_blocks(d):
     """bf16 inputs, gradients in fp32, all three into one buffer; other columns and rows of no sequence stay."""
