@@ -622,17 +622,28 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_bf16_kernel(AttnBwdArgs p
   bf16x8 q[KB], go[KB];
   float lse, dl = 0.f;
   {
+    uint4 o[KB];
+    uint2 low[KB];
     const int64_t row = tl.a + (tq < L ? tq : L - 1);
     const bf16* qp = static_cast<const bf16*>(p.q) + row * p.ld_q + tl.hq * D + 8 * h;
     const bf16* gp = static_cast<const bf16*>(p.d_o) + (row * p.Hq + tl.hq) * D + 8 * h;
     const bf16* op = static_cast<const bf16*>(p.o) + (row * p.Hq + tl.hq) * D + 8 * h;
+    const uint8_t* lp = reinterpret_cast<const uint8_t*>(p.stats + 2 * p.total_T * p.Hq) +
+                        (row * p.Hq + tl.hq) * D + 8 * h;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       q[kb] = *reinterpret_cast<const bf16x8*>(qp + 16 * kb);
       go[kb] = *reinterpret_cast<const bf16x8*>(gp + 16 * kb);
-      const bf16x8 o = *reinterpret_cast<const bf16x8*>(op + 16 * kb);
+      o[kb] = *reinterpret_cast<const uint4*>(op + 16 * kb);
+      low[kb] = *reinterpret_cast<const uint2*>(lp + 16 * kb);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dl = __builtin_fmaf((float)go[kb][i], (float)o[i], dl);
+    for (int kb = 0; kb < KB; ++kb) {
+      const float2 x[4] = {with_low_bytes<0>(o[kb].x, low[kb].x), with_low_bytes<2>(o[kb].y, low[kb].x),
+                           with_low_bytes<0>(o[kb].z, low[kb].y), with_low_bytes<2>(o[kb].w, low[kb].y)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dl = __builtin_fmaf((float)go[kb][2 * i + 1], x[i].y, __builtin_fmaf((float)go[kb][2 * i], x[i].x, dl));
     }
     dl += __shfl_xor(dl, 32);
     const float2 st = reinterpret_cast<const float2*>(p.stats)[row * p.Hq + tl.hq];

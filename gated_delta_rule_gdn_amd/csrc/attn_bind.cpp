@@ -427,6 +427,10 @@ PyObject* answer(PyObject* status, PyObject* const (&given)[N], const Tensor (&m
   return r;
 }
 
+int64_t stats_words(int64_t T, int64_t Hq, ScalarType io, int64_t d) {
+  return T * Hq * (io == ScalarType::BFloat16 ? 2 + d / 4 : 2);
+}
+
 // (fn, q, k, v, cu_seqlens, N, window, scale, o, stats, stream) -> (status, o, stats)
 PyObject* attn_prefill_save(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&]() -> PyObject* {
@@ -449,7 +453,7 @@ PyObject* attn_prefill_save(PyObject*, PyObject* const* a, Py_ssize_t n) {
     desc.scale = scale_of(a[7], d);
     Tensor made[2];
     void* o = out_dense(a[8], "o", dev, {T, desc.H_q, d}, io, &made[0]);
-    void* stats = out_dense(a[9], "stats", dev, {T, desc.H_q, 2}, ScalarType::Float, &made[1]);
+    void* stats = out_dense(a[9], "stats", dev, {stats_words(T, desc.H_q, io, d)}, ScalarType::Float, &made[1]);
     const auto fn = function<decltype(&gdn_attn_prefill_save)>(a[0]);
     void* stream = handle(a[10]);
     PyObject* const given[2] = {a[8], a[9]};
@@ -502,7 +506,7 @@ PyObject* attn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* v_in = heads(a[4], "v", dev, T, desc.H_k, d, io, &desc.ld_v);
     const void* o = dense(a[5], "o", dev, {T, desc.H_q, d}, io);
     const void* d_o = dense(a[6], "d_o", dev, {T, desc.H_q, d}, io);
-    const void* stats = dense(a[7], "stats", dev, {T, desc.H_q, 2}, ScalarType::Float);
+    const void* stats = dense(a[7], "stats", dev, {stats_words(T, desc.H_q, io, d)}, ScalarType::Float);
     const int64_t* cu;
     desc.N = packed(a[8], a[9], dev, &cu);
     desc.window = integer(a[10], "window");

@@ -24,6 +24,28 @@ __device__ __forceinline__ float weight_of(float x, float m) {
   return exp2_fast(x - m);
 }
 
+// The 8 bits that follow those that x keeps when it is rounded to bf16: the difference of
+// the two as fp32's bits, -2^15..2^15, and 2^15 in steps of 2^8, rounded down.  With them x
+// is known to 16 bits, in the middle of a step: bits of bf16 + 2^8 byte - 2^15 + 2^7.  (What
+// is not finite becomes NaN; a NaN stays one.)  Four in a word.
+__device__ __forceinline__ uint32_t low_bytes(float x0, float x1, float x2, float x3) {
+  auto low = [](float x) {
+    const uint32_t hi = (uint32_t)__builtin_bit_cast(uint16_t, (bf16)x) << 16;
+    const uint32_t rest = __float_as_uint(x) - hi + 0x8000;
+    return rest < 0xffff ? rest : 0xffffu;
+  };
+  const uint32_t a = __builtin_amdgcn_perm(low(x1), low(x0), 0x0c0c0501);   // bytes 1 of both
+  const uint32_t b = __builtin_amdgcn_perm(low(x3), low(x2), 0x05010c0c);
+  return a | b;
+}
+// Two bf16 and bytes E, E + 1 of low.
+template <int E>
+__device__ __forceinline__ float2 with_low_bytes(uint32_t pair, uint32_t low) {
+  const uint32_t a = __builtin_amdgcn_perm(pair, low, 0x0504000c | E << 8);
+  const uint32_t b = __builtin_amdgcn_perm(pair, low, 0x0706000c | (E + 1) << 8);
+  return make_float2(__uint_as_float(a - 0x7f80), __uint_as_float(b - 0x7f80));
+}
+
 __device__ __forceinline__ int64_t read_lane(int64_t x, int lane) {
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane);
   const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)x >> 32), lane);

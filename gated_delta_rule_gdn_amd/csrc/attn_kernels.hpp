@@ -50,6 +50,11 @@ struct KvAppendArgs {
   PagedCache cache;
 };
 
+// fp32 words that a query and head leave for the backward pass: the running maximum and
+// sum, and with bf16 rows a byte for each channel of the output (low_bytes), behind those
+// of all queries and heads.
+inline int stats_width(DType io, int d) { return io == DType::BF16 ? 2 + d / 4 : 2; }
+
 struct PrefillArgs {
   int64_t N, total_T, Tseq;           // Tseq: tokens per sequence when cu_seqlens is NULL
   const int64_t* cu_seqlens;          // device [N + 1] or NULL
@@ -59,7 +64,7 @@ struct PrefillArgs {
   float scale;
   const void *q, *k, *v;
   void* o;
-  float* stats = nullptr;             // [total_T, Hq, 2] or NULL
+  float* stats = nullptr;             // total_T Hq stats_width words, or NULL
 };
 
 struct AttnDecodeArgs {

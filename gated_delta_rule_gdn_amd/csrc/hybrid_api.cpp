@@ -154,7 +154,7 @@ gdn_status gdn_attn_prefill_save(const gdn_attn_prefill_desc* d, const int64_t* 
                       rows_span(v, d->total_T, d->ld_v, d->H_k, d->d, d->io_dtype),
                       span(cu_seqlens, d->N + 1, 8)};
   const Span outs[] = {span(o, d->total_T * d->H_q * d->d, dtype_bytes(d->io_dtype)),
-                       span(stats, d->total_T * d->H_q * 2, 4)};
+                       span(stats, d->total_T * d->H_q * gdn::stats_width(to_dtype(d->io_dtype), d->d), 4)};
   if (!apart(ins, outs)) return GDN_ERR_INVALID_ARG;
 
   gdn::PrefillArgs a;
@@ -195,7 +195,9 @@ gdn_status gdn_attn_backward(const gdn_attn_bwd_desc* d, const int64_t* cu_seqle
   const Span ins[] = {rows_span(q, T, d->ld_q, d->H_q, d->d, d->io_dtype),
                       rows_span(k, T, d->ld_k, d->H_k, d->d, d->io_dtype),
                       rows_span(v, T, d->ld_v, d->H_k, d->d, d->io_dtype), span(o, n, eb),
-                      span(d_o, n, eb), span(stats, T * d->H_q * 2, 4), span(cu_seqlens, d->N + 1, 8)};
+                      span(d_o, n, eb),
+                      span(stats, T * d->H_q * gdn::stats_width(to_dtype(d->io_dtype), d->d), 4),
+                      span(cu_seqlens, d->N + 1, 8)};
   // dq, dk and dv may be column blocks of one buffer: rows apart, not spans
   const Span sdq = rows_span(dq, T, d->ld_dq, d->H_q, d->d, d->grad_dtype);
   const Span sdk = rows_span(dk, T, d->ld_dk, d->H_k, d->d, d->grad_dtype);

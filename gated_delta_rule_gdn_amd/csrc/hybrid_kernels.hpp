@@ -16,7 +16,7 @@ struct AttnBwdArgs {
   DType io, grad;
   float scale;
   const void *q, *k, *v, *o, *d_o;
-  const float* stats;                 // [total_T, Hq, 2]
+  const float* stats;                 // total_T Hq stats_width words
   void *dq, *dk, *dv;
   float* ws;                          // attn_bwd_plan(...).ws_floats
 };

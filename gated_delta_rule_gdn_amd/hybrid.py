@@ -86,17 +86,23 @@ def _done(r, name):
 # allocated here first.
 
 
+def _stats_words(q) -> int:
+    T, H, d = q.shape
+    return T * H * (2 + d // 4 if q.dtype == torch.bfloat16 else 2)
+
+
 def gdn_attn_prefill_save(q, k, v, cu_seqlens=None, N=None, window: int = 0, scale=None, o=None,
                           stats=None, stream=None):
     """gdn_attn_prefill that also leaves the statistics gdn_attn_backward needs
     (see include/gdn_hybrid.h).  Returns (o, stats).
 
-    Arguments as gdn_attn_prefill; stats fp32 [total_T, H_q, 2] is allocated
-    when not given, as o is.
+    Arguments as gdn_attn_prefill; stats, float32 of total_T * H_q * 2 elements
+    (bfloat16 rows: total_T * H_q * (2 + d / 4)), is allocated when not given, as
+    o is.
     """
     if stream is not None:
         o = _empty(q.shape, q.dtype, q, stream) if o is None else o
-        stats = _empty((*q.shape[:2], 2), torch.float32, q, stream) if stats is None else stats
+        stats = _empty((_stats_words(q),), torch.float32, q, stream) if stats is None else stats
     return _done(_native.attn_prefill_save(_fn["gdn_attn_prefill_save"], q, k, v, cu_seqlens, N, window,
                                            scale, o, stats, _raw_stream(stream, q)), "gdn_attn_prefill_save")
 

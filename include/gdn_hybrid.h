@@ -37,9 +37,11 @@ extern "C" {
  * gdn_attn_prefill_save -- gdn_attn_prefill (same descriptor, arguments and
  * result) that also leaves, for gdn_attn_backward, each query's statistics.
  *
- *   stats [total_T, H_q, 2] fp32 (output), 16-byte aligned: m, the maximum score
- *         (times log2 e) or a number at most 8 below it, and the sum of 2^(score - m);
- *         rows that no range covers are kept
+ *   stats (output) 16-byte aligned.  [total_T, H_q, 2] fp32: m, the maximum score
+ *         (times log2 e) or a number at most 8 below it, and the sum of 2^(score - m).
+ *         With bf16 io, behind those, [total_T, H_q, d] bytes b: what o was, to 16 bits,
+ *         before it was rounded, its bits as fp32's + 2^8 b - 2^15 + 2^7.  Rows that no
+ *         range covers are kept
  */
 gdn_status gdn_attn_prefill_save(const gdn_attn_prefill_desc* desc, const int64_t* cu_seqlens,
                                  const void* q, const void* k, const void* v, void* o,
@@ -77,7 +79,7 @@ size_t gdn_attn_backward_workspace_size(const gdn_attn_bwd_desc* desc);
  *                                                     heads of the key head too)
  *
  * Sums in fp32; with bf16 io, p and e are rounded to bf16 for the products that
- * use them, and o is what the forward rounded.  p carries the rounding of scores
+ * use them, and o is the forward's to 16 bits (see stats).  p carries the rounding of scores
  * and of m in fp32, relative 2^-23 times the larger of them: scores (times
  * log2 e) of 2^20 and more have no meaningful gradients.
  * Non-finite inputs: what is not finite in a token makes gradients of its own
@@ -87,9 +89,8 @@ size_t gdn_attn_backward_workspace_size(const gdn_attn_bwd_desc* desc);
  *   cu_seqlens, q, k, v  as for gdn_attn_prefill_save
  *   o, d_o     [total_T, H_q, d] io_dtype, dense: the forward's output and the
  *              upstream gradient
- *   stats      [total_T, H_q, 2] fp32 of gdn_attn_prefill_save for the same
- *              arguments (others give meaningless gradients, never an access
- *              outside the arguments)
+ *   stats      of gdn_attn_prefill_save for the same arguments (others give
+ *              meaningless gradients, never an access outside the arguments)
  *   workspace  >= gdn_attn_backward_workspace_size(desc) bytes, 16-byte aligned
  *   dq [total_T, H_q, d], dk, dv [total_T, H_k, d] grad_dtype, row strides
  *              (outputs); may be column blocks of one buffer.  Rows before the

@@ -35,7 +35,8 @@ def attn_grads(q, k, v, d_o, window, scale, dtype, grad=None):
     Weights p: a score's d + 4 fp32 roundings relative to sum |q k| twice (forward and
     here), its and the statistics' rounding as numbers (of size 1.5 reach + log2 n + 8),
     exp2 and log2 2^-22 each, sums of n terms; bf16: rounded once more for the products.
-    D = d_o . o: o's own error (attn_bound's terms and its rounding), d products.
+    D = d_o . o: o's own error (attn_bound's terms and its rounding; bf16: known to 16 bits,
+    a step of 2^-15 at most), d products.
     e = p (d_o . v - D): those, and bf16's rounding.  Then sums of n (times the group's
     heads for dk, dv) products, and the output's rounding."""
     q, k, v, d_o = (f64(t) for t in (q, k, v, d_o))
@@ -57,7 +58,7 @@ def attn_grads(q, k, v, d_o, window, scale, dtype, grad=None):
         n = float(np.max(np.sum(seen, 1)))
         rel = 4 * ((d + 4) * EPS * 1.5 * reach + EPS * (1.5 * reach + math.log2(n) + 8) + 2.0 ** -22) + 2 * (n + 16) * EPS
         a = p @ np.abs(vh)                                     # sum p |v|
-        err_o = (rel + b) * a + HALF[dtype] * np.abs(p @ vh)
+        err_o = (rel + b) * a + (2.0 ** -15 if dtype == BF else HALF[dtype]) * np.abs(p @ vh)
         err_D = np.sum(np.abs(gh) * err_o, 1, keepdims=True) + (d + 8) * EPS * np.sum(np.abs(gh) * a, 1, keepdims=True)
         gp, ga = gh @ vh.T, np.abs(gh) @ np.abs(vh).T
         D = np.sum(p * gp, 1, keepdims=True)

@@ -47,6 +47,53 @@ def both(dv, **kw):
 # attention and its gradients
 # ----------------------------------------------------------------------------
 
+def stats_of(stats, o):
+    """[T, Hq, 2] and (bf16) the bytes [T, Hq, d] behind it."""
+    T, H, d = o.shape
+    return stats[:2 * T * H].view(T, H, 2), stats[2 * T * H:].view(torch.uint8).view(T, H, -1)
+
+
+def to_16_bits(o, stats):
+    """o before its rounding to bf16, with the bytes that stats holds of it."""
+    low = stats_of(stats, o)[1].to(torch.int32)
+    bits = o.contiguous().view(torch.int16).to(torch.int32) << 16
+    return (bits + 256 * low - 0x7f80).view(torch.float32)
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("N,L,Hq,Hk,d,window", [(1, 700, 4, 2, 128, 0), (1, 700, 4, 1, 64, 100), (3, 90, 40, 40, 128, 0),
+                                                (5, 130, 90, 45, 64, 33), (2, 1, 1, 1, 64, 0)])
+def test_statistics_and_low_bytes(N, L, Hq, Hk, d, window, far):
+    """Equal scores: weights of 1 and a sum that is their number, so outputs are means of values, in fp32 up to
+    their rounding.  `far`: an infinite value at each sequence's end sends queries that do not see it another way."""
+    announce(f"statistics N={N} L={L} Hq={Hq} d={d} window={window} far={far}")
+    host = [t.clone().contiguous() for t in attn_inputs(N * L, Hq, Hk, d, BF, L + d)]
+    host[0].zero_()
+    if far:
+        host[2][L - 1::L] = math.inf
+    q, k, v, _ = (dev(t) for t in host)
+    o, stats = gdn.gdn_attn_prefill_save(q, k, v, N=N, window=window)
+    torch.cuda.synchronize()
+    got = f64(to_16_bits(o, stats).cpu())
+    st = f64(stats_of(stats, o)[0].cpu())
+    t = np.arange(L)
+    n = np.minimum(t + 1, window or L)
+    for i in range(N):
+        rows = slice(i * L, (i + 1) * L)
+        # 2^m l is the number of keys; one or both rounded once, 2^(0 - m) exact for the m that scores of 0 leave
+        total = np.exp2(st[rows, :, 0]) * st[rows, :, 1]
+        assert np.all(np.abs(total - n[:, None]) <= 2.0 ** -20 * n[:, None])
+        vh = f64(host[2][rows]).repeat(Hq // Hk, axis=1)
+        sums = np.stack([vh[j + 1 - n[j]:j + 1].sum(0) for j in t])
+        mean, reach = sums / n[:, None, None], np.cumsum(np.abs(vh), 0) / n[:, None, None]
+        seen = t < L - 1 if far else t < L
+        # sums of n terms in fp32 and a byte's half step (a whole one at its end)
+        bound = (n[:, None, None] + 16) * EPS * reach + 2.0 ** -15 * np.abs(mean) + 1e-30
+        assert np.all(np.abs(got[rows][seen] - mean[seen]) <= bound[seen])
+        if far:
+            assert not np.any(np.isfinite(got[rows][-1]))     # spoiled, as what it sees
+
+
 LENS = [1, 0, 2, 31, 32, 33, 64, 127, 128, 129, 300, 5]
 
 
@@ -140,13 +187,16 @@ def test_attention_sequences_are_apart(dtype):
         t[360:] = bad             # behind the last one
     cu = torch.tensor([0, 100, 170, 360]).cuda()
     on = [t.cuda() for t in host]
-    o, stats = torch.full((T, 2, 64), 7.0, dtype=dtype, device="cuda"), torch.full((T, 2, 2), 7.0, device="cuda")
+    o, stats = torch.full((T, 2, 64), 7.0, dtype=dtype, device="cuda"), torch.full((T * 2 * (2 + 16 * (dtype == BF)),), 7.0, device="cuda")
     gdn.gdn_attn_prefill_save(*on[:3], cu_seqlens=cu, o=o, stats=stats)
     grads = [torch.full((T, h, 64), 7.0, dtype=dtype, device="cuda") for h in (2, 1, 1)]
     ws = torch.full((gdn.gdn_attn_backward_workspace_size(on[0], on[1], N=3),), 255, dtype=torch.uint8, device="cuda")
     gdn.gdn_attn_backward(*on[:3], o, on[3], stats, cu_seqlens=cu, dq=grads[0], dk=grads[1], dv=grads[2], workspace=ws)
     torch.cuda.synchronize()
-    assert all(bool((t[360:] == 7).all()) for t in (o, stats, *grads))
+    assert all(bool((t[360:] == 7).all()) for t in (o, stats_of(stats, o)[0], *grads))
+    if dtype == BF:
+        kept = stats_of(torch.full_like(stats, 7.0), o)[1]
+        assert torch.equal(stats_of(stats, o)[1][360:], kept[360:])
     check_attn(grads, host, [0, 100], 0, None, dtype, what="first")
     check_attn([t[170:360] for t in grads], [t[170:360] for t in host], [0, 190], 0, None, dtype, what="third")
 

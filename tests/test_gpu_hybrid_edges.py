@@ -429,11 +429,11 @@ def test_binding_refusals():
             call()
 
     back = lambda **kw: gdn.gdn_attn_backward(*[kw.pop(n, t) for n, t in (("q", q), ("k", k), ("v", v), ("o", o), ("g", g), ("s", stats))], **kw)  # noqa: E731,E501
-    refused(lambda: gdn.gdn_attn_prefill_save(q, k, v, stats=stats[:, :2].contiguous()), "stats has shape")
+    refused(lambda: gdn.gdn_attn_prefill_save(q, k, v, stats=stats[:-1]), "stats has shape")
     refused(lambda: gdn.gdn_attn_prefill_save(q, k, v, stats=stats.to(BF)), "stats must be torch.float32")
     refused(lambda: back(o=o.float()), "o must be")
     refused(lambda: back(g=g[:19]), "d_o has shape")
-    refused(lambda: back(s=stats.transpose(0, 1)), "stats has shape")
+    refused(lambda: back(s=stats.view(20, -1)), "stats has shape")
     refused(lambda: back(dq=torch.empty_like(q).transpose(1, 2).contiguous().transpose(1, 2)), "dq must have dense rows")
     refused(lambda: back(dq=torch.empty_like(q), dk=torch.empty(k.shape, device="cuda")), "dk must be")
     refused(lambda: back(grad_dtype=torch.float16), "float32 or bfloat16")

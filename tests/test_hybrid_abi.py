@@ -141,6 +141,15 @@ def test_rejects_overlaps(call, out, other):
     assert c(ptrs={out: _addr(c.ptrs.index(other))}, **kw) == gdn.GDN_ERR_INVALID_ARG
 
 
+def test_statistics_end_behind_their_bytes():
+    """9 tokens, 4 heads of 128: 288 bytes, and in bf16 4608 behind them."""
+    save, back = CALLS["save"], CALLS["backward"]
+    for io, size in ((BF, 4896), (F32, 288)):
+        assert save(ptrs={"o": _addr(5, size - 16)}, io_dtype=io) == gdn.GDN_ERR_INVALID_ARG
+        assert back(ptrs={"dq": _addr(6, size - 16)}, io_dtype=io, grad_dtype=io) == gdn.GDN_ERR_INVALID_ARG
+        assert back(ptrs={"ws": _addr(6, size - 16)}, io_dtype=io, grad_dtype=io) == gdn.GDN_ERR_INVALID_ARG
+
+
 def test_in_place_only_where_rows_are_the_same():
     c = CALLS["rope"]
     at = {"dq_raw": _addr(0)}
