@@ -19,6 +19,8 @@
 // In both, what is summed over lies on the rows of the first products (S^T = K Q^T and
 // dP^T = V dO^T for dq; S = Q K^T and dP = dO V^T for dk and dv), so p and ds are, as
 // they lie in the accumulators, the k-values of the second products.
+#include <cmath>
+
 #include "attn_shares.hpp"
 #include "attn_tiles.hpp"
 
@@ -74,7 +76,7 @@ __device__ __forceinline__ float* slot_of(const AttnBwdArgs& p, int workers, int
 
 // ---------------------------------------------------------------------------
 // Who walks what.  A workgroup of the dk and dv kernel has either one key tile (`workers`
-// 0: many tiles, the dear ones first) or an equal share of all tiles' walks, in the order
+// 0, the dear ones first; see whole_tiles) or an equal share of all tiles' walks, in the order
 // of sequence, key head and tile: then the first and the last walk of a share may be parts
 // of one, whose sums go to the workspace and are joined in order by another kernel.  Shares
 // that follow each other are on one XCD.  The shares are counted out by the first
@@ -1186,23 +1188,61 @@ hipError_t launch_f32(const AttnBwdArgs& a, int workers, hipStream_t stream) {
 }  // namespace
 
 // Workgroups of the second kind stay on their CU to the end: as many as there is room for.
-// With 8 tiles or more to each of them whole tiles, the dear ones first, are as even and
-// need no join; more sequences than kMaxRanked would take a workgroup long to count.
+struct KeyTiles {
+  int64_t rows, step, room;
+};
+static KeyTiles key_tiles(int d, DType io) {
+  return io == DType::F32 ? KeyTiles{32, 32, d == 128 ? 512 : 768} : KeyTiles{128, 64, d == 128 ? 256 : 512};
+}
+
 AttnBwdPlan attn_bwd_plan(int64_t N, int64_t total_T, int64_t window, int Hq, int Hk, int d, DType io) {
-  const bool f32 = io == DType::F32;
-  const int64_t rows = f32 ? 32 : 128, room = f32 ? (d == 128 ? 512 : 768) : (d == 128 ? 256 : 512);
-  const int64_t tiles = total_T / rows + N;
+  const KeyTiles kt = key_tiles(d, io);
+  const int64_t tiles = total_T / kt.rows + N;
   int64_t workers = 0;
-  if (N <= kMaxRanked && tiles * Hk < 8 * room) {
-    const WalkUnits u{window, (int)rows, f32 ? 32 : 64, Hq / Hk, kLead};
+  // (more sequences than kMaxRanked would take a workgroup long to count)
+  if (N <= kMaxRanked && tiles * Hk < 8 * kt.room) {
+    const WalkUnits u{window, (int)kt.rows, (int)kt.step, Hq / Hk, kLead};
     const int64_t most = Hk * (u.units(total_T) + N * (2 * u.G + u.lead)) / kLeast + 1;   // shares that there can be
-    workers = most < room ? (most + kXcds - 1) / kXcds * kXcds : room;
+    workers = most < kt.room ? (most + kXcds - 1) / kXcds * kXcds : kt.room;
   }
   AttnBwdPlan r;
   r.workers = (int)workers;
   r.ws_floats = 4 * total_T * Hq;
-  if (workers) r.ws_floats += 8 * workers + walk_floats(tiles, Hk, (int)workers) + workers * (2 * rows * 2 * d);
+  if (workers) r.ws_floats += 8 * workers + walk_floats(tiles, Hk, (int)workers) + workers * (2 * kt.rows * 2 * d);
   return r;
+}
+
+// Whether each key tile gets a workgroup of its own, the dear ones first.  Equal shares of
+// their walks are even, but cost partial sums and a join: 9 to 20 steps of a workgroup's
+// walk and a fiftieth of it (us with whole tiles / shares: 8 prompts of 64 tokens, 8 heads of
+// 2 24 / 29; 8 of 1024, 16 heads 178 / 198; 8192 tokens, 16 heads 900 / 942; 32768 tokens, 8
+// heads of 4 7010 / 7097).
+// With r tiles to each of the workgroups that there is room for, all sequences of a length,
+// whole tiles are as uneven as the next round of them makes it: tiles that see a window cost
+// alike and r is rounded up; without one costs fall evenly to 0, so two rounds, the second
+// backwards, are even, and what d = r mod 2 rounds are left over make the longest walk
+// 2 (d - d^2 / 2) / r^2 longer than the mean; up to r = 1 it is the first tile's.  (us whole / shares, r = 1: 16384 tokens, 16
+// heads of 2 5264 / 3609; r = 3: 32768 tokens, 6 heads of 3, 5765 / 5365; 4 prompts
+// of 4096, 12 heads of 6, 742 / 763; 16 prompts of 512, 12 heads, 105 / 125.)
+// Lengths that differ are not known here: from 3 tiles on (fp32, whose tiles are shorter
+// than the longest sequence by more: 2) the longest one's walks rarely decide (us whole /
+// shares; 12 prompts of 16384 tokens, r = 2.2 425 / 376, 3.3 542 / 547, 4.4 702 / 719; 16 of
+// 32768 with a window of 2048, r = 2.1 1401 / 1386, 4.3 1360 / 1410; fp32, 12 of 4096, r =
+// 2.2 221 / 238, heads of 64, r = 2.9 192 / 242), and never where all tokens in one
+// sequence would be a short walk.
+static bool whole_tiles(const AttnBwdArgs& a) {
+  const KeyTiles kt = key_tiles(a.d, a.io);
+  const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, kt.rows) * a.Hk;
+  const double r = (double)tiles / (double)kt.room;
+  const WalkUnits u{a.window, (int)kt.rows, (int)kt.step, a.Hq / a.Hk, kLead};
+  if (a.cu_seqlens && a.N > 1)
+    return r >= (a.io == DType::F32 ? 2.0 : 3.0) || u.before(a.total_T, 1) < 9;
+  const int64_t L = a.total_T / a.N;
+  const double walk = (double)(a.N * a.Hk) * (double)u.units(L) / (double)kt.room, d = std::fmod(r, 2.0);
+  const double longer = r <= 1.0 ? (double)u.before(L, 1) - walk
+                        : a.window > 0 && a.window < L / 2 ? (std::ceil(r) / r - 1.0) * walk
+                                                           : 2.0 * (d - 0.5 * d * d) / (r * r) * walk;
+  return longer < 9.0 + std::fmin(11.0, walk / 4.0) + walk / 50.0;
 }
 
 int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, int Hq, DType io) {
@@ -1210,11 +1250,12 @@ int64_t attn_bwd_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, i
 }
 
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, const AttnBwdPlan& plan, hipStream_t stream) {
+  const int workers = whole_tiles(a) ? 0 : plan.workers;
   if (a.io == DType::F32)
-    return a.d == 128 ? launch_f32<128>(a, plan.workers, stream) : launch_f32<64>(a, plan.workers, stream);
+    return a.d == 128 ? launch_f32<128>(a, workers, stream) : launch_f32<64>(a, workers, stream);
   if (a.grad == DType::F32)
-    return a.d == 128 ? launch_bf16<float, 128>(a, plan.workers, stream) : launch_bf16<float, 64>(a, plan.workers, stream);
-  return a.d == 128 ? launch_bf16<bf16, 128>(a, plan.workers, stream) : launch_bf16<bf16, 64>(a, plan.workers, stream);
+    return a.d == 128 ? launch_bf16<float, 128>(a, workers, stream) : launch_bf16<float, 64>(a, workers, stream);
+  return a.d == 128 ? launch_bf16<bf16, 128>(a, workers, stream) : launch_bf16<bf16, 64>(a, workers, stream);
 }
 
 #ifdef GDN_CHECK

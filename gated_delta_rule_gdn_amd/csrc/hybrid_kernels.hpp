@@ -21,8 +21,8 @@ struct AttnBwdArgs {
   float* ws;                          // attn_bwd_plan(...).ws_floats
 };
 
-// How a backward call divides its key tiles: equal shares of all of them to so many
-// workgroups (0: one to each tile), and the workspace.
+// To how many workgroups a backward call may deal its key tiles' walks in equal shares (0:
+// each tile has a workgroup of its own), and the workspace.
 struct AttnBwdPlan {
   int workers;
   int64_t ws_floats;

@@ -64,8 +64,8 @@ typedef struct gdn_attn_bwd_desc {
 /*
  * gdn_attn_backward_workspace_size -- bytes of device workspace gdn_attn_backward
  * needs for this descriptor (0 for an invalid one or when there is no token):
- * 16 for each token and query head, and where a key head's tokens are shared by
- * several workgroups their partial sums.
+ * 16 for each token and query head, and where several workgroups may share a key
+ * tile their partial sums.
  */
 size_t gdn_attn_backward_workspace_size(const gdn_attn_bwd_desc* desc);
 
