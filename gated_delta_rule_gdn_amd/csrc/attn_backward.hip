@@ -19,6 +19,15 @@
 // In both, what is summed over lies on the rows of the first products (S^T = K Q^T and
 // dP^T = V dO^T for dq; S = Q K^T and dP = dO V^T for dk and dv), so p and ds are, as
 // they lie in the accumulators, the k-values of the second products.
+//
+// 14 d flops to a key that a query sees, against a few bytes: bound by the matrix cores,
+// and with them by power.  Both kernels of a call, bf16, 16 heads of 128: a document of
+// 16384 tokens over 2 key heads 3500 to 3600 us, 1070 to 1100 TFLOP/s (a plain product of
+// 8192 x 8192 x 8192 reaches 1212); 8 prompts of 4096 tokens over 16 key heads 1930 to 2010
+// us, 960 to 1000; 16 documents, 32768 tokens in all, a window of 2048 over 2 key heads 1390
+// to 1470 us.  fp32, 4096 tokens, 16 heads of 128: 2200 us, 109 TFLOP/s (a product: 154).
+// Short documents are three launches and the walks of the longest one's tiles (29 of 282
+// tokens on average, 6 heads of 64 over 3: 22 + 27 + 8 us).
 #include <cmath>
 
 #include "attn_shares.hpp"
@@ -245,7 +254,8 @@ struct Walks {
 // fp32: v_mfma_f32_16x16x4_f32, 32 queries (dq) or 32 keys (dk, dv) to a workgroup,
 // tiles of 32 rows of the other in LDS.  Waves 0 and 1 take 16 rows of their own over
 // the first 16 rows of each tile, waves 2 and 3 the same over the others, and their
-// sums are added at the end.
+// sums are added at the end.  (Every fragment from LDS serves one product: 4096 tokens, 16
+// heads of 128 run at 0.71 of a plain product's rate.)
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attn_dq_f32_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
@@ -587,6 +597,10 @@ __device__ __forceinline__ void rows_out(bf16* lds, const f32x16* acc, float f, 
   }
 }
 
+// Two workgroups to a CU hide each other's waits.  D is formed from outputs of 16 bits (see
+// low_bytes): from bf16 alone a gradient's error was 3.1e-3 of its norm instead of 2.7e-3 for
+// documents of 16 tokens.  3 products: 970 TFLOP/s for 8 prompts of 4096 tokens, 16 heads of
+// 128, 1120 for a document of 16384.
 // SPLIT 2: 64 queries to a workgroup, each 32 of them to two waves that take 32 keys of a
 // tile each and add their sums at the end (see split_dq).
 template <int D, typename TG, int SPLIT>
@@ -852,7 +866,11 @@ __device__ __forceinline__ void keep_a(bf16x8& x) {
 // 192 registers.  What hides latencies instead is a pipeline by hand over blocks of 32
 // queries: the first products of the next block, with the weights of this one formed
 // between them, then this one's second products; every LDS read some products ahead of its
-// use; tiles three deep in LDS.
+// use; tiles three deep in LDS.  4 products: 870 TFLOP/s for 8 prompts of 4096 tokens, 16
+// heads of 128, 1050 for a document of 16384 tokens (two waves to a SIMD, as the compiler
+// schedules them, 640 and 690).  Of the 2.0 us that a step of 64 queries takes the products
+// alone are 1.3, at 1.7 GHz: power.  With the LDS reads, seven eighths of the weights or the
+// loads and barriers left out it takes 1.8, 1.8 and 1.7.
 template <int D, typename TG>
 __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
   constexpr int BK = 128, BQ = 64, KB = D / 16, MT = D / 32;
@@ -1221,8 +1239,8 @@ AttnBwdPlan attn_bwd_plan(int64_t N, int64_t total_T, int64_t window, int Hq, in
 // whole tiles are as uneven as the next round of them makes it: tiles that see a window cost
 // alike and r is rounded up; without one costs fall evenly to 0, so two rounds, the second
 // backwards, are even, and what d = r mod 2 rounds are left over make the longest walk
-// 2 (d - d^2 / 2) / r^2 longer than the mean; up to r = 1 it is the first tile's.  (us whole / shares, r = 1: 16384 tokens, 16
-// heads of 2 5264 / 3609; r = 3: 32768 tokens, 6 heads of 3, 5765 / 5365; 4 prompts
+// 2 (d - d^2 / 2) / r^2 longer than the mean; up to r = 1 it is the first tile's.  (us
+// whole / shares, r = 1: 16384 tokens, 16 heads of 2 5264 / 3609; r = 3: 32768 tokens, 6 heads of 3, 5765 / 5365; 4 prompts
 // of 4096, 12 heads of 6, 742 / 763; 16 prompts of 512, 12 heads, 105 / 125.)
 // Lengths that differ are not known here: from 3 tiles on (fp32, whose tiles are shorter
 // than the longest sequence by more: 2) the longest one's walks rarely decide (us whole /

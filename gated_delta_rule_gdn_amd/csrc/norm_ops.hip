@@ -8,7 +8,9 @@
 //
 // Both read their rows once, hold them in registers through the sums over a row and
 // write once, at a few flops per element: HBM-bound for many rows, launch latency
-// for few.
+// for few.  32768 rows of 2048 channels, bf16 with the residual in fp32: 143.6 us, 5.61 TB/s
+// (a copy of 1 GiB: 5.09), backward 194.0, 5.53; 8192 rows of 4096 to e4m3 44.7 us, 5.3.  One
+// row 2.5 us, 5.1 with its call.
 //
 // A row is held by W waves (1 or 4) in CH chunks of 8 channels to a lane, chunk
 // i of thread t being number t + 64 W i of the row, so that every access is
@@ -179,7 +181,8 @@ __global__ __launch_bounds__(kThreads) void add_norm_kernel(AddNormArgs p) {
 // ---------------------------------------------------------------------------
 // Backward.  Workgroups loop over rows and keep their rows' part of d_weight in
 // registers; it goes to the workspace once for each workgroup, and a second kernel
-// adds the parts in a fixed order.
+// adds the parts in a fixed order.  (256 or 768 workgroups measure 2 to 5 % worse: with two
+// to a CU loads and stores of different rows overlap; more leave more parts.)
 // ---------------------------------------------------------------------------
 constexpr int64_t kBwdBlocks = 512;
 int64_t bwd_blocks(int64_t rows, int C) {

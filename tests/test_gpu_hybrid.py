@@ -290,7 +290,7 @@ def test_norm_rope_one_operand_without_a_norm_in_place(dtype):
 # the residual stream
 # ----------------------------------------------------------------------------
 
-WIDTHS = [8, 72, 512, 520, 1024, 1032, 2048, 2056, 4096, 5000, 8192, 16384]
+WIDTHS = [8, 72, 512, 520, 1024, 1032, 1536, 1544, 2048, 2056, 4096, 5000, 8192, 16384]
 
 
 def step_of(z):
