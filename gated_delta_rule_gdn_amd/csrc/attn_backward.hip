@@ -962,9 +962,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
       aux_at += BQ;
     }
   };
-#pragma unroll
-  for (int i = 0; i < NB - 1; ++i)
-    if (w.at + i < w.stop) load_step(i);
+  load_step(0);
   bf16x8 k[KB], v[KB];
   {
     const int64_t row = w.a + (tk < L ? tk : L - 1);
@@ -1072,6 +1070,11 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
     keep_a(v[kb]);
   }
   wait_tiles();
+  // (the second tile is needed a step later: the first products wait for one only; prompts of
+  // 128 tokens, 16 heads, 438 -> 428 us with dq)
+#pragma unroll
+  for (int i = 1; i < NB - 1; ++i)
+    if (w.at + i < w.stop) load_step(i);
   int buf = 0;
   auto next_buf = [](int i) { return (i + 1) % NB; };
   // The next tile is there, with the one behind it perhaps still on its way, and the last one free.
@@ -1091,10 +1094,15 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
     x = statistics(0);
     product_v0(s, x, ones_s);
     product_v0(dp, x, ones_d);
+    bf16x8 f[NF];
 #pragma unroll
-    for (int i = 0; i < NF; ++i) {
-      if (i % 2 == 0) product_v(s, read_first(0, i), k[i / 2]);
-      else product_v(dp, read_first(0, i), v[i / 2]);
+    for (int i = 0; i < NF; ++i) f[i] = read_first(0, i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < NF; i += 2) {
+      both_there(f[i], f[i + 1]);
+      product_v(s, f[i], k[i / 2]);
+      product_v(dp, f[i + 1], v[i / 2]);
     }
     products_done(s, dp);
     x = statistics(HALF_AUX);
