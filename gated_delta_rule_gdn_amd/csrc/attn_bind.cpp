@@ -222,6 +222,15 @@ PyObject* on_device(int dev, F call) {
   return PyLong_FromLong((long)st);
 }
 
+// An exception of torch's own, as its allocations raise them.
+void raise_torch(const char* name, const char* text) {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* type = torch ? PyObject_GetAttrString(torch, name) : nullptr;
+  if (type) PyErr_SetString(type, text);    // (otherwise the import has raised)
+  Py_XDECREF(type);
+  Py_XDECREF(torch);
+}
+
 // Turns what a body throws into a Python error.
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F body) {
@@ -231,6 +240,9 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F body) {
   }
   try {
     return body();
+  } catch (const c10::OutOfMemoryError& e) {
+    raise_torch("OutOfMemoryError", e.what());
+    return nullptr;
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
     return nullptr;

@@ -1,6 +1,7 @@
 """Binding of a hybrid's training and residual operators of libgdn.so (the C ABI
 in include/gdn_hybrid.h): argument marshalling only, by the extension module
-that attn.py loads; what it refuses raises ValueError.
+that attn.py loads; what it refuses raises ValueError, and where there is no
+memory for outputs that it allocates, torch.OutOfMemoryError.
 
 Tensors of a call are on one device, which need not be the current one; work
 goes to that device's current stream, or to the one given.

@@ -462,3 +462,26 @@ def test_binding_refusals():
         with pytest.raises(gdn.GdnError) as e:
             call()
         assert e.value.status == status
+
+
+def test_no_memory_for_outputs():
+    """Outputs and workspaces that the calls allocate: torch's error, and the next call works."""
+    announce("hybrid out of memory")
+    x = torch.randn(1 << 14, 1024, device="cuda")
+    w = torch.ones(1024, device="cuda")
+    want = gdn.gdn_add_norm(x[:8], x[:8], w)[0].clone()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 20)) / total)
+    try:
+        kept = torch.empty(1 << 19, dtype=torch.uint8, device="cuda")
+        for call in (lambda: gdn.gdn_add_norm(x, x, w), lambda: gdn.gdn_add_norm_backward(x, x, w),
+                     lambda: gdn.gdn_qk_norm_rope_backward(x.view(-1, 8, 128), None, x.view(-1, 8, 128)),
+                     lambda: gdn.gdn_attn_prefill_save(*[x.view(-1, 8, 128)] * 3)):
+            with pytest.raises(torch.OutOfMemoryError):
+                call()
+        del kept
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.equal(gdn.gdn_add_norm(x[:8], x[:8], w)[0], want)
