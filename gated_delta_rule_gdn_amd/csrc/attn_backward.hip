@@ -252,22 +252,23 @@ struct Walks {
 
 // ---------------------------------------------------------------------------
 // fp32: v_mfma_f32_16x16x4_f32, 32 queries (dq) or 32 keys (dk, dv) to a workgroup,
-// tiles of 32 rows of the other in LDS.  Waves 0 and 1 take 16 rows of their own over
-// the first 16 rows of each tile, waves 2 and 3 the same over the others, and their
-// sums are added at the end.  (Every fragment from LDS serves one product: 4096 tokens, 16
+// tiles of 32 rows of the other in LDS (dq of few tiles: 64).  Waves 0 and 1 take 16 rows
+// of their own over the first 16 rows of each tile, waves 2 and 3 (4 to 7) the same over the
+// others, and their sums are added at the end.  (Every fragment from LDS serves one product: 4096 tokens, 16
 // heads of 128 run at 0.71 of a plain product's rate.)
 // ---------------------------------------------------------------------------
-template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attn_dq_f32_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
-  constexpr int BM = 32, BN = 32, LD = D + 4, KB = D / 32, MT = D / 16;
+// KW pairs of waves share a tile's keys (see split_dq_f32).
+template <int D, int KW>
+__global__ __launch_bounds__(128 * KW, 2) void attn_dq_f32_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
+  constexpr int kT = 128 * KW, BM = 32, BN = 16 * KW, LD = D + 4, KB = D / 32, MT = D / 16;
   constexpr int KEYS = 32, STEP = 32;       // of the dk and dv kernel
-  constexpr int NL = BN * D / 4 / kThreads;
+  constexpr int NL = BN * D / 4 / kT;
   __shared__ __align__(16) float s_kv[2 * BN * LD];
   lds_nan_fill(s_kv, sizeof s_kv);
   float *s_k = s_kv, *s_v = s_kv + BN * LD;
   const int G = p.Hq / p.Hk, plan = plan_blocks(workers);
   if ((int)blockIdx.x < plan) {
-    plan_worker<KEYS, STEP>(p, workers, 4 * blockIdx.x + (threadIdx.x >> 6));
+    if (threadIdx.x < 256) plan_worker<KEYS, STEP>(p, workers, 4 * blockIdx.x + (threadIdx.x >> 6));
     return;
   }
   const Tile tl = find_tile<BM>(tile_args(p, G), blockIdx.x - plan, blocks);
@@ -288,7 +289,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_f32_kernel(AttnBwdArgs p,
   auto load_tile = [&](int k0) {            // rows past the sequence are zero
 #pragma unroll
     for (int e = 0; e < NL; ++e) {
-      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+      const int row = (e * kT + tid) / (D / 4), c = 4 * ((e * kT + tid) % (D / 4));
       kr[e] = vr[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k0 + row < L) {
         kr[e] = *reinterpret_cast<const float4*>(kb_ + (int64_t)(k0 + row) * p.ld_k + c);
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_f32_kernel(AttnBwdArgs p,
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < NL; ++e) {
-      const int row = (e * kThreads + tid) / (D / 4), c = 4 * ((e * kThreads + tid) % (D / 4));
+      const int row = (e * kT + tid) / (D / 4), c = 4 * ((e * kT + tid) % (D / 4));
       lds_check(s_v + row * LD + c, 16);
       *reinterpret_cast<float4*>(s_k + row * LD + c) = kr[e];
       *reinterpret_cast<float4*>(s_v + row * LD + c) = vr[e];
@@ -361,22 +362,26 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_f32_kernel(AttnBwdArgs p,
     }
   }
   __syncthreads();
-  if (wk == 1) {
+  static_assert((KW - 1) * BM <= 2 * BN, "the sums fit");
+  if (wk > 0) {
 #pragma unroll
     for (int c = 0; c < MT; ++c) {
-      float* dst = s_kv + (16 * wq + j) * LD + 16 * c + 4 * g;
+      float* dst = s_kv + ((wk - 1) * BM + 16 * wq + j) * LD + 16 * c + 4 * g;
       lds_check(dst, 16);
       *reinterpret_cast<float4*>(dst) = make_float4(dq[c][0], dq[c][1], dq[c][2], dq[c][3]);
     }
   }
   __syncthreads();
-  if (wk == 1 || tq >= L) return;
+  if (wk > 0 || tq >= L) return;
   float* to = static_cast<float*>(p.dq) + (tl.a + tq) * p.ld_dq + tl.hq * D + 4 * g;
 #pragma unroll
   for (int c = 0; c < MT; ++c) {
-    const float4 u = *reinterpret_cast<const float4*>(s_kv + (16 * wq + j) * LD + 16 * c + 4 * g);
-    store4<float>(to + 16 * c, (dq[c][0] + u.x) * p.scale, (dq[c][1] + u.y) * p.scale,
-                  (dq[c][2] + u.z) * p.scale, (dq[c][3] + u.w) * p.scale);
+#pragma unroll
+    for (int i = 0; i < KW - 1; ++i) {
+      const float4 u = *reinterpret_cast<const float4*>(s_kv + (i * BM + 16 * wq + j) * LD + 16 * c + 4 * g);
+      dq[c][0] += u.x; dq[c][1] += u.y; dq[c][2] += u.z; dq[c][3] += u.w;
+    }
+    store4<float>(to + 16 * c, dq[c][0] * p.scale, dq[c][1] * p.scale, dq[c][2] * p.scale, dq[c][3] * p.scale);
   }
 }
 
@@ -1197,11 +1202,21 @@ hipError_t launch_bf16(const AttnBwdArgs& a, int workers, hipStream_t stream) {
   attn_dkv_join_kernel<TG, D, 128><<<dim3(nk, 8), kThreads, 0, stream>>>(a, workers);
   return hipGetLastError();
 }
+// fp32 with 8 waves to a tile of 64 keys instead of 4 to 32, where few query tiles have many
+// keys (us of a backward call, 4 / 8 waves).  d 128: 2048 tokens, 2 heads (128 workgroups)
+// 222 / 203; 8 heads (512) 393 / 353; 4096 tokens, 8 heads (1024) 1223 / 1284.  d 64: 1024
+// tokens, 4 heads 85 / 76; 12 prompts, 2048 tokens, 8 heads (608) 77.5 / 73.2; 8 of 256, 4
+// heads 33.7 / 33.5; 3 of 86, 4 heads 22.1 / 22.6; 24 of 13, 8 heads 19.8 / 21.1.
+bool split_dq_f32(int64_t blocks, int64_t keys) { return blocks <= 640 && keys >= 128; }
+
 template <int D>
 hipError_t launch_f32(const AttnBwdArgs& a, int workers, hipStream_t stream) {
   const int64_t tiles = tiles_of(a.N, a.total_T, a.Tseq, a.cu_seqlens != nullptr, 32);
   const uint32_t nq = (uint32_t)(tiles * a.Hq), nk = workers ? (uint32_t)workers : (uint32_t)(tiles * a.Hk);
-  attn_dq_f32_kernel<D><<<dim3(nq + plan_blocks(workers)), kThreads, 0, stream>>>(a, nq, workers);
+  const dim3 grid(nq + plan_blocks(workers));
+  const int64_t len = a.cu_seqlens ? a.total_T / a.N : a.Tseq;
+  if (split_dq_f32(nq, a.window > 0 && a.window < len ? a.window : len)) attn_dq_f32_kernel<D, 4><<<grid, 512, 0, stream>>>(a, nq, workers);
+  else attn_dq_f32_kernel<D, 2><<<grid, 256, 0, stream>>>(a, nq, workers);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   attn_dkv_f32_kernel<D><<<dim3(nk), kThreads, 0, stream>>>(a, nk, workers);

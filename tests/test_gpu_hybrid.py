@@ -133,6 +133,17 @@ def test_attention_one_long_sequence(T, Hq, Hk, d, window, dtype):
     check_attn(got, host, [0, T], window, None, dtype, what="long")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,Hk,d,window", [(3, 3, 128, 0), (4, 2, 64, 0), (2, 1, 128, 150), (6, 2, 64, 190)])
+def test_attention_few_tiles_of_many_keys(Hq, Hk, d, window, dtype):
+    announce(f"attn backward few tiles Hq={Hq} d={d} window={window} {dtype}")
+    bounds = [0, 300, 429, 430, 687, 687, 1010]
+    host, on = case(bounds[-1], Hq, Hk, d, dtype, window + d)
+    _, _, got = both(on, cu_seqlens=torch.tensor(bounds).cuda(), window=window)
+    torch.cuda.synchronize()
+    check_attn(got, host, bounds, window, None, dtype, what="few tiles")
+
+
 def test_attention_many_sequences():
     """More sequences than are ranked by cost, and many equal ones."""
     announce("attn backward many sequences")

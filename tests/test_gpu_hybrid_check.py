@@ -28,6 +28,8 @@ CASES = {
     "attention, one long sequence": lambda: th.test_attention_one_long_sequence(1300, 4, 1, 128, 500, BF),
     "attention, one long sequence, d 64": lambda: th.test_attention_one_long_sequence(1500, 8, 1, 64, 0, BF),
     "attention, one long sequence, fp32": lambda: th.test_attention_one_long_sequence(1300, 4, 1, 128, 500, F32),
+    "attention, few tiles, fp32": lambda: th.test_attention_few_tiles_of_many_keys(3, 3, 128, 0, F32),
+    "attention, few tiles, fp32, d 64": lambda: th.test_attention_few_tiles_of_many_keys(6, 2, 64, 190, F32),
     "attention, many heads": lambda: th.test_attention_of_many_heads(32, 8, 128, 50, F32),
     "attention, many heads, d 64": lambda: th.test_attention_of_many_heads(48, 6, 64, 0, BF),
     "attention, fp32 gradients": lambda: th.test_attention_gradients_in_fp32_into_column_blocks(128),
