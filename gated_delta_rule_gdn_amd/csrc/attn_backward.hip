@@ -385,8 +385,10 @@ __global__ __launch_bounds__(128 * KW, 2) void attn_dq_f32_kernel(AttnBwdArgs p,
   }
 }
 
+// D 64: three workgroups to a CU (168 registers; the 171 that the compiler takes of itself
+// leave room for two: 4096 tokens, 8 heads 693 -> 641 us with dq).
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attn_dkv_f32_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_dkv_f32_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
   constexpr int BK = 32, BQ = 32, LD = D + 4, KB = D / 32, MT = D / 16;
   constexpr int NL = BQ * D / 4 / kThreads;
   __shared__ __align__(16) float s_qg[2 * BQ * LD];
@@ -1269,7 +1271,7 @@ AttnBwdPlan attn_bwd_plan(int64_t N, int64_t total_T, int64_t window, int Hq, in
 // than the longest sequence by more: 2) the longest one's walks rarely decide (us whole /
 // shares; 12 prompts of 16384 tokens, r = 2.2 425 / 376, 3.3 542 / 547, 4.4 702 / 719; 16 of
 // 32768 with a window of 2048, r = 2.1 1401 / 1386, 4.3 1360 / 1410; fp32, 12 of 4096, r =
-// 2.2 221 / 238, heads of 64, r = 2.9 192 / 242), and never where all tokens in one
+// 2.2 221 / 237, heads of 64, r = 2.9 178 / 206), and never where all tokens in one
 // sequence would be a short walk.
 static bool whole_tiles(const AttnBwdArgs& a) {
   const KeyTiles kt = key_tiles(a.d, a.io);
