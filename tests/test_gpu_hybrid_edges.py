@@ -474,14 +474,18 @@ def test_no_memory_for_outputs():
     torch.cuda.empty_cache()
     total = torch.cuda.get_device_properties(0).total_memory
     torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 20)) / total)
+    kept = []
     try:
-        kept = torch.empty(1 << 19, dtype=torch.uint8, device="cuda")
+        for size in (1 << 30, 1 << 26, 1 << 23, 1 << 21):     # what the allocator holds
+            with pytest.raises(torch.OutOfMemoryError):
+                while True:
+                    kept.append(torch.empty(size, dtype=torch.uint8, device="cuda"))
         for call in (lambda: gdn.gdn_add_norm(x, x, w), lambda: gdn.gdn_add_norm_backward(x, x, w),
                      lambda: gdn.gdn_qk_norm_rope_backward(x.view(-1, 8, 128), None, x.view(-1, 8, 128)),
                      lambda: gdn.gdn_attn_prefill_save(*[x.view(-1, 8, 128)] * 3)):
             with pytest.raises(torch.OutOfMemoryError):
                 call()
-        del kept
     finally:
+        kept.clear()
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert torch.equal(gdn.gdn_add_norm(x[:8], x[:8], w)[0], want)
