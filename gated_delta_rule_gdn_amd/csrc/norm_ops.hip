@@ -79,10 +79,19 @@ __device__ __forceinline__ uint2 codes8(const float* y, float inv) {
   return make_uint2((uint32_t)a, (uint32_t)b);
 }
 
+// Rows are held times a power of two, which changes no rounding: so squares below 2^120 add
+// up to less than 2^128 over 16384 channels, and products with gradients below 2^60 too.  At
+// the other end eps covers what that costs, but for one next to nothing: there a small row
+// is summed again times kSmall as well.
+constexpr float kFactor = 0x1p-8f, kSmall = 0x1p80f;
+__device__ __forceinline__ bool sum_again(float eps, float mean) {      // (mean is the same in all lanes)
+  return eps < 0x1p-100f && __builtin_amdgcn_readfirstlane(mean < 0x1p-80f);
+}
+
 // W 1: a workgroup has 4 rows; W 4: one.
 template <typename TX, typename TR, int W, int CH, bool CODES>
 __global__ __launch_bounds__(kThreads) void add_norm_kernel(AddNormArgs p) {
-  __shared__ float s_sum[4], s_max[4];
+  __shared__ float s_sum[2][4], s_max[4];
   const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x, wave = threadIdx.x >> 6;
   const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
   if (W == 1 && row >= p.rows) return;
@@ -126,15 +135,34 @@ __global__ __launch_bounds__(kThreads) void add_norm_kernel(AddNormArgs p) {
       if (p.res_out) store8(static_cast<TR*>(p.res_out) + row * p.C + 8 * c, r[i]);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss += r[i][e] * r[i][e];
+    for (int e = 0; e < 8; ++e) {
+      const float x = r[i][e] * kFactor;
+      ss += x * x;
+    }
   }
-  ss = wave_sum_f(ss);
-  if constexpr (W == 4) {
-    if ((threadIdx.x & 63) == 0) s_sum[wave] = ss;
-    __syncthreads();
-    ss = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+  auto over_row = [&](float (&s)[4]) {
+    ss = wave_sum_f(ss);
+    if constexpr (W == 4) {
+      if ((threadIdx.x & 63) == 0) s[wave] = ss;
+      __syncthreads();
+      ss = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+    return ss / (float)p.C;
+  };
+  float mean = over_row(s_sum[0]) + p.eps * (kFactor * kFactor), f = kFactor;
+  if (sum_again(p.eps, mean)) {
+    f = kFactor * kSmall;
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = r[i][e] * f;
+        ss += x * x;
+      }
+    mean = over_row(s_sum[1]) + (p.eps * f) * f;
   }
-  const float inv = __builtin_amdgcn_rsqf(ss / (float)p.C + p.eps);
+  const float inv = __builtin_amdgcn_rsqf(mean) * f;
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
@@ -230,22 +258,41 @@ __global__ __launch_bounds__(kThreads) void add_norm_bwd_kernel(AddNormBwdArgs p
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
+        r[i][e] *= kFactor;
         ss += r[i][e] * r[i][e];
         sg += r[i][e] * (g[i][e] * w[i][e]);
       }
     }
-    ss = wave_sum_f(ss);
-    sg = wave_sum_f(sg);
-    if constexpr (W == 4) {                 // two sets in turn: one barrier to a row
-      float (*s)[2] = s_sum[turn];
-      turn ^= 1;
-      if ((threadIdx.x & 63) == 0) { s[wave][0] = ss; s[wave][1] = sg; }
-      __syncthreads();
-      ss = (s[0][0] + s[1][0]) + (s[2][0] + s[3][0]);
-      sg = (s[0][1] + s[1][1]) + (s[2][1] + s[3][1]);
+    auto over_row = [&] {
+      ss = wave_sum_f(ss);
+      sg = wave_sum_f(sg);
+      if constexpr (W == 4) {               // two sets in turn: one barrier to a sum
+        float (*s)[2] = s_sum[turn];
+        turn ^= 1;
+        if ((threadIdx.x & 63) == 0) { s[wave][0] = ss; s[wave][1] = sg; }
+        __syncthreads();
+        ss = (s[0][0] + s[1][0]) + (s[2][0] + s[3][0]);
+        sg = (s[0][1] + s[1][1]) + (s[2][1] + s[3][1]);
+      }
+    };
+    over_row();
+    float f = kFactor, squares = ss / (float)p.C + p.eps * (kFactor * kFactor);
+    if (sum_again(p.eps, squares)) {
+      f = kFactor * kSmall;
+      ss = sg = 0.f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          r[i][e] *= kSmall;
+          ss += r[i][e] * r[i][e];
+          sg += r[i][e] * (g[i][e] * w[i][e]);
+        }
+      over_row();
+      squares = ss / (float)p.C + (p.eps * f) * f;
     }
-    const float inv = __builtin_amdgcn_rsqf(ss / (float)p.C + p.eps);
-    const float mean = sg / (float)p.C * inv;          // of n w dy
+    const float root = __builtin_amdgcn_rsqf(squares), inv = root * f;
+    const float mean = sg / (float)p.C * root;         // of n w dy
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = t + 64 * W * i;
@@ -255,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void add_norm_bwd_kernel(AddNormBwdArgs p
       if (p.d_res_out && c < chunks) cd[i].unpack(u);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float n = r[i][e] * inv;
+        const float n = r[i][e] * root;
         acc[i][e] += g[i][e] * n;
         u[e] += inv * (g[i][e] * w[i][e] - n * mean);
       }

@@ -214,6 +214,7 @@ size_t gdn_add_norm_backward_workspace_size(const gdn_add_norm_bwd_desc* desc);
  *   d_weight = sum over rows of dy n
  *
  * d_r is the gradient of x and of res alike; it is written in either type.
+ * |r|, |dy| and |dy weight| < 2^60, and where eps is 0 as gdn_add_norm.
  *
  *   dy         [rows, C] io_dtype, dense
  *   r          [rows, C] res_dtype, dense
