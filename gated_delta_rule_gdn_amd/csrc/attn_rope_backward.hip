@@ -36,7 +36,7 @@ __host__ __device__ inline Split split_of(int64_t rows, int Hq, int Hk, int d) {
   s.gq = (Hq + kHeads - 1) / kHeads;
   s.gk = (Hk + kHeads - 1) / kHeads;
   const int64_t need = (rows + tokens - 1) / tokens, most = kBlocks / (s.gq + s.gk);
-  s.tb = need < most ? need : (most > 1 ? most : 1);
+  s.tb = need <= most ? need : (most > 1 ? most : 1);   // (no rows: none, at any number of heads)
   return s;
 }
 

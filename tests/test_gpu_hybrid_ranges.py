@@ -128,3 +128,12 @@ def test_gradients_that_are_not_finite_stay_in_their_rows_and_channels(C, io, rt
     rows, channels = [0, 1, 3, 5], [c for c in range(C) if c not in (5, 7)]
     assert torch.equal(dx[rows], want[0][rows]) and torch.equal(d_res[rows], want[1][rows])
     assert torch.equal(dw[channels], want[2][channels]) and not bool(torch.isfinite(dw[[5, 7]]).any())
+
+
+@pytest.mark.parametrize("heads", [2, 16384])
+def test_no_rows_of_many_heads_give_zero_weight_gradients(heads):
+    announce(f"no rows, {heads} heads")
+    h, w = torch.zeros(0, heads, 64, dtype=BF, device="cuda"), torch.ones(64, device="cuda")
+    r = gdn.gdn_qk_norm_rope_backward(h, None, h, q_weight=w, dq_weight=torch.full((64,), 7.0, device="cuda"))
+    torch.cuda.synchronize()
+    assert bool((r[2] == 0).all())

@@ -204,6 +204,17 @@ def test_workspaces_are_needed_in_full():
         assert size(ctypes.byref(c.cls(**{**c.desc, field: 3}))) == 0
 
 
+@pytest.mark.parametrize("heads", [(1, 1), (0, 1), (4, 2), (8190, 2), (8192, 1), (1, 16384), (65536, 65536)])
+def test_no_row_needs_no_workspace(heads):
+    """And so no workgroup of the gradient's kernel, which would read frequencies that a call without rows need not
+    give: also where there are more heads than it has workgroups."""
+    size = L.gdn_qk_norm_rope_backward_workspace_size
+    desc = dict(rows=0, ld_q=2 ** 22, ld_k=2 ** 22, ld_dq=2 ** 22, ld_dk=2 ** 22, H_q=heads[0], H_k=heads[1], d=64, rope_dim=64,
+                rope_mode=0, io_dtype=BF, grad_dtype=BF, rope_scale=1.0, eps=1e-6)
+    assert size(ctypes.byref(gdn.GdnQkBwdDesc(**desc))) == 0
+    assert size(ctypes.byref(gdn.GdnQkBwdDesc(**{**desc, "rows": 1}))) >= 256 * (sum(heads) // 2)
+
+
 @pytest.mark.parametrize("window", [1, 2 ** 40, 2 ** 63 - 1])
 def test_windows_of_any_size_have_a_plan(window):
     size = L.gdn_attn_backward_workspace_size
