@@ -88,7 +88,7 @@ __device__ __forceinline__ const T* in_global(const void* x) {
 // to 13 ms for the wave that it sends here, 0.11 ms without; 32768 tokens 114).  A
 // row all of whose columns are NaN is settled: where every value is NaN all waves
 // come here (16384 tokens 138 ms walking on, 2 ms so).
-template <typename T, int D>
+template <typename T, int D, bool SAVE>
 __device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl, int hk, int window,
                                            int q0, int rows) {
   const int lane = threadIdx.x & 63, L = (int)tl.L;
@@ -145,7 +145,7 @@ __device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl,
     T* op = static_cast<T*>(p.o) + ((tl.a + t) * p.Hq + tl.hq) * (int64_t)D + lane;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) op[64 * c] = (T)(o[c] / l);
-    if (p.stats) {
+    if constexpr (SAVE) {
       if (lane == 0) leave_stats(p, tl, t, m, l);
       if constexpr (std::is_same<T, bf16>::value) {
         uint8_t* low = low_at<D>(p, tl, t) + lane;
@@ -160,7 +160,7 @@ __device__ __forceinline__ void exact_rows(const PrefillArgs& p, const Tile& tl,
 // wave's maximum was).  The arguments are
 // read from the kernel's argument segment again, where `p` is its first: kept in
 // registers for this rare end they would spill others (2 % of a prompt).
-template <typename T, int D>
+template <typename T, int D, bool SAVE>
 __device__ __forceinline__ bool rows_again(const Tile& tl, int hk, int window, int q0, int rows,
                                            bool huge) {
 #if __HIP_DEVICE_COMPILE__
@@ -169,7 +169,7 @@ __device__ __forceinline__ bool rows_again(const Tile& tl, int hk, int window, i
   const PrefillArgs p = *reinterpret_cast<const PrefillArgs*>(at);
   const T* v = in_global<T>(p.v) + tl.a * p.ld_v + hk * D;
   if (!huge && !unseen_not_finite<T, D>(v, p.ld_v, (int)tl.L, window, q0, rows)) return false;
-  exact_rows<T, D>(p, tl, hk, window, q0, rows);
+  exact_rows<T, D, SAVE>(p, tl, hk, window, q0, rows);
 #endif
   return true;
 }
@@ -188,7 +188,7 @@ __device__ __forceinline__ bool rows_again(const Tile& tl, int hk, int window, i
 // key tiles double-buffered in LDS, which leaves room for two workgroups instead
 // of three: 750 us.)
 // ---------------------------------------------------------------------------
-template <int D, int KW>
+template <int D, int KW, bool SAVE>
 __global__ __launch_bounds__(128 * KW, KW == 4 ? 2 : D == 64 ? 4 : 3) void prefill_f32_kernel(PrefillArgs p, uint32_t blocks) {
   constexpr int BM = 32, BN = 16 * KW, LD = D + 4, KB = D / 32, MT = D / 16;
   constexpr int NT = 128 * KW;                        // threads
@@ -334,8 +334,8 @@ __global__ __launch_bounds__(128 * KW, KW == 4 ? 2 : D == 64 ? 4 : 3) void prefi
   for (int c = 0; c < MT; ++c)
 #pragma unroll
     for (int r = 0; r < 4; ++r) z = __builtin_fmaf(o[c][r], 0.f, z);
-  if (__any(z != z) && rows_again<float, D>(tl, hk, window, q0, 16, false)) return;
-  if (p.stats && g == 0 && tq < L) leave_stats(p, tl, tq, m, l);
+  if (__any(z != z) && rows_again<float, D, SAVE>(tl, hk, window, q0, 16, false)) return;
+  if (SAVE && g == 0 && tq < L) leave_stats(p, tl, tq, m, l);
   float* op = static_cast<float*>(p.o) + ((tl.a + tq) * p.Hq + tl.hq) * (int64_t)D + 4 * g;
 #pragma unroll
   for (int c = 0; c < MT; ++c)
@@ -366,6 +366,8 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
 
 // WIN: with the code of a window's mask (calls without a window are 1 to 2 % faster
 // without it: 8 prompts of 4096 tokens 546 / 540 us, 4 short ones 11.0 / 10.7).
+// SAVE: with the statistics (in one kernel for both, the registers that they take cost the plain
+// call 256 prompts of 128 tokens, 16 heads of 64, 54.4 us instead of 48.1; 29 of 282, 12.3 / 11.6).
 // SPLIT 2: 64 queries to a workgroup; waves 0 and 1 take the even key tiles, 2
 // and 3 the odd ones, with a maximum and sum of their own, and join at the end.
 //
@@ -374,7 +376,7 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
 // while the maximum of tile i + 1 is formed, tile i's product with V is.  K
 // runs one tile ahead of V; both are double-buffered in LDS and loaded one
 // iteration before they are read, with one barrier to an iteration.
-template <int D, int SPLIT, bool WIN>
+template <int D, int SPLIT, bool WIN, bool SAVE>
 __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void prefill_bf16_kernel(PrefillArgs p, uint32_t blocks) {
   constexpr int WQ = 4 / SPLIT;                       // waves with queries of their own
   constexpr int BM = 32 * WQ, BN = 64, KB = D / 16, MT = D / 32;
@@ -699,8 +701,8 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
 #pragma unroll
     for (int r = 0; r < 16; ++r) z[r % 4] = __builtin_fmaf(o[c][r], 0.f, z[r % 4]);
   z[0] += z[1] + (z[2] + z[3]);
-  if ((huge || __any(z[0] != z[0])) && rows_again<bf16, D>(tl, hk, window, q0, 32, huge)) return;
-  if (p.stats && h == 0 && tq < L) leave_stats(p, tl, tq, m, l);
+  if ((huge || __any(z[0] != z[0])) && rows_again<bf16, D, SAVE>(tl, hk, window, q0, 32, huge)) return;
+  if (SAVE && h == 0 && tq < L) leave_stats(p, tl, tq, m, l);
   bf16* so = &s_k[0][0] + wq * 32 * D;
 #pragma unroll
   for (int c = 0; c < MT; ++c)
@@ -718,24 +720,25 @@ __global__ __launch_bounds__(kThreads, SPLIT == 2 ? 1 : D == 64 ? 3 : 2) void pr
       *reinterpret_cast<uint4*>(op + row * (int64_t)p.Hq * D + 8 * c) =
           *reinterpret_cast<const uint4*>(so + row * D + 8 * (c ^ (row & (CH - 1))));
   }
-  if (!p.stats) return;
-  // the bytes the same way (stores of 4 bytes to a lane straight from the registers: 40 of
-  // 2500 us more for 8 prompts of 4096 tokens, 16 heads, with the backward pass)
-  uint32_t* sb = reinterpret_cast<uint32_t*>(so);
+  if constexpr (SAVE) {
+    // the bytes the same way (stores of 4 bytes to a lane straight from the registers: 40 of
+    // 2500 us more for 8 prompts of 4096 tokens, 16 heads, with the backward pass)
+    uint32_t* sb = reinterpret_cast<uint32_t*>(so);
 #pragma unroll
-  for (int c = 0; c < MT; ++c)
+    for (int c = 0; c < MT; ++c)
 #pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      uint32_t* dst = sb + i32 * (D / 4) + 2 * ((4 * c + r / 4) ^ (i32 & (CH - 1))) + h;
-      lds_check(dst, 4);
-      *dst = low_bytes(o[c][r] * inv, o[c][r + 1] * inv, o[c][r + 2] * inv, o[c][r + 3] * inv);
+      for (int r = 0; r < 16; r += 4) {
+        uint32_t* dst = sb + i32 * (D / 4) + 2 * ((4 * c + r / 4) ^ (i32 & (CH - 1))) + h;
+        lds_check(dst, 4);
+        *dst = low_bytes(o[c][r] * inv, o[c][r + 1] * inv, o[c][r + 2] * inv, o[c][r + 3] * inv);
+      }
+#pragma unroll
+    for (int e = 0; e < 32 * CH / 64; ++e) {
+      const int row = (e * 64 + lane) / CH, c = (e * 64 + lane) % CH;
+      if (q0 + row < L)
+        *reinterpret_cast<uint2*>(low_at<D>(p, tl, q0) + row * (int64_t)p.Hq * D + 8 * c) =
+            *reinterpret_cast<const uint2*>(sb + row * (D / 4) + 2 * (c ^ (row & (CH - 1))));
     }
-#pragma unroll
-  for (int e = 0; e < 32 * CH / 64; ++e) {
-    const int row = (e * 64 + lane) / CH, c = (e * 64 + lane) % CH;
-    if (q0 + row < L)
-      *reinterpret_cast<uint2*>(low_at<D>(p, tl, q0) + row * (int64_t)p.Hq * D + 8 * c) =
-          *reinterpret_cast<const uint2*>(sb + row * (D / 4) + 2 * (c ^ (row & (CH - 1))));
   }
 }
 
@@ -770,20 +773,42 @@ bool split_f32(int64_t blocks, int64_t keys) { return blocks <= 512 && keys >= 6
 
 // rows_again reads PrefillArgs where a kernel's arguments begin.
 using PrefillKernel = void (*)(PrefillArgs, uint32_t);
-static_assert(std::is_same<decltype(&prefill_bf16_kernel<128, 1, true>), PrefillKernel>::value &&
-                  std::is_same<decltype(&prefill_f32_kernel<128, 2>), PrefillKernel>::value,
+static_assert(std::is_same<decltype(&prefill_bf16_kernel<128, 1, true, false>), PrefillKernel>::value &&
+                  std::is_same<decltype(&prefill_f32_kernel<128, 2, false>), PrefillKernel>::value,
               "PrefillArgs is the first argument");
 
-template <int SPLIT>
+template <int SPLIT, bool SAVE>
 void launch_bf16(const PrefillArgs& a, int64_t blocks, hipStream_t stream) {
   const dim3 grid((unsigned)blocks);
   const uint32_t n = (uint32_t)blocks;
   if (a.d == 128) {
-    if (a.window) prefill_bf16_kernel<128, SPLIT, true><<<grid, kThreads, 0, stream>>>(a, n);
-    else prefill_bf16_kernel<128, SPLIT, false><<<grid, kThreads, 0, stream>>>(a, n);
+    if (a.window) prefill_bf16_kernel<128, SPLIT, true, SAVE><<<grid, kThreads, 0, stream>>>(a, n);
+    else prefill_bf16_kernel<128, SPLIT, false, SAVE><<<grid, kThreads, 0, stream>>>(a, n);
   } else {
-    if (a.window) prefill_bf16_kernel<64, SPLIT, true><<<grid, kThreads, 0, stream>>>(a, n);
-    else prefill_bf16_kernel<64, SPLIT, false><<<grid, kThreads, 0, stream>>>(a, n);
+    if (a.window) prefill_bf16_kernel<64, SPLIT, true, SAVE><<<grid, kThreads, 0, stream>>>(a, n);
+    else prefill_bf16_kernel<64, SPLIT, false, SAVE><<<grid, kThreads, 0, stream>>>(a, n);
+  }
+}
+template <int KW, bool SAVE>
+void launch_f32(const PrefillArgs& a, int64_t blocks, hipStream_t stream) {
+  const dim3 grid((unsigned)blocks);
+  const uint32_t n = (uint32_t)blocks;
+  if (a.d == 128) prefill_f32_kernel<128, KW, SAVE><<<grid, 128 * KW, 0, stream>>>(a, n);
+  else prefill_f32_kernel<64, KW, SAVE><<<grid, 128 * KW, 0, stream>>>(a, n);
+}
+
+template <bool SAVE>
+void launch(const PrefillArgs& a, hipStream_t stream) {
+  const bool packed = a.cu_seqlens != nullptr;
+  const int64_t blocks = prefill_blocks(a.N, a.total_T, a.Tseq, packed, a.Hq, a.io);
+  const int64_t keys = mean_keys(a);
+  if (a.io == DType::F32) {
+    if (split_f32(blocks, keys)) launch_f32<4, SAVE>(a, blocks, stream);
+    else launch_f32<2, SAVE>(a, blocks, stream);
+  } else if (split_bf16(blocks, keys, a.d)) {
+    launch_bf16<2, SAVE>(a, blocks_of(a.N, a.total_T, a.Tseq, packed, a.Hq, 64), stream);
+  } else {
+    launch_bf16<1, SAVE>(a, blocks, stream);
   }
 }
 
@@ -794,24 +819,8 @@ int64_t prefill_blocks(int64_t N, int64_t total_T, int64_t Tseq, bool packed, in
 }
 
 hipError_t launch_attn_prefill(const PrefillArgs& a, hipStream_t stream) {
-  const bool packed = a.cu_seqlens != nullptr;
-  const int64_t blocks = prefill_blocks(a.N, a.total_T, a.Tseq, packed, a.Hq, a.io);
-  const int64_t keys = mean_keys(a);
-  const dim3 grid((unsigned)blocks);
-  if (a.io == DType::F32) {
-    if (split_f32(blocks, keys)) {
-      if (a.d == 128) prefill_f32_kernel<128, 4><<<grid, 512, 0, stream>>>(a, (uint32_t)blocks);
-      else prefill_f32_kernel<64, 4><<<grid, 512, 0, stream>>>(a, (uint32_t)blocks);
-    } else {
-      if (a.d == 128) prefill_f32_kernel<128, 2><<<grid, 256, 0, stream>>>(a, (uint32_t)blocks);
-      else prefill_f32_kernel<64, 2><<<grid, 256, 0, stream>>>(a, (uint32_t)blocks);
-    }
-  } else if (split_bf16(blocks, keys, a.d)) {
-    const int64_t twice = blocks_of(a.N, a.total_T, a.Tseq, packed, a.Hq, 64);
-    launch_bf16<2>(a, twice, stream);
-  } else {
-    launch_bf16<1>(a, blocks, stream);
-  }
+  if (a.stats) launch<true>(a, stream);
+  else launch<false>(a, stream);
   return hipGetLastError();
 }
 
