@@ -394,6 +394,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_dkv_f32_kernel
   __shared__ __align__(16) float s_qg[2 * BQ * LD];
   __shared__ __align__(16) float4 s_aux[BQ];
   lds_nan_fill(s_qg, sizeof s_qg);
+  lds_nan_fill(s_aux, sizeof s_aux);
   float *s_q = s_qg, *s_g = s_qg + BQ * LD;
   const int G = p.Hq / p.Hk;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -448,7 +449,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_dkv_f32_kernel
         *reinterpret_cast<float4*>(s_q + row * LD + c) = qr[e];
         *reinterpret_cast<float4*>(s_g + row * LD + c) = gr[e];
       }
-      if (tid < BQ) s_aux[tid] = ar;
+      if (tid < BQ) {
+        lds_check(s_aux + tid, 16);
+        s_aux[tid] = ar;
+      }
       __syncthreads();
       if (step + 1 < w.stop) load_tile();
       const int t0 = k0 + now * BQ + 16 * wq;         // this wave's queries
@@ -466,6 +470,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attn_dkv_f32_kernel
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = 16 * wq + 4 * g + r, t = t0 + 4 * g + r;
+        lds_check(s_aux + row, 16);
         const float4 st = s_aux[row];
         const bool seen = tk <= t && t < L && (!window || tk > t - window);
         const float pr = seen ? weight_of(s[r] * c_scale, st.x) * st.y : 0.f;
@@ -888,6 +893,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
   __shared__ __align__(1024) bf16 s_t[NB][2 * BQ * D];
   __shared__ __align__(1024) uint4 s_aux[NB][BQ];
   lds_nan_fill(s_t, sizeof s_t);
+  lds_nan_fill(s_aux, sizeof s_aux);
   const int G = p.Hq / p.Hk;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float c_scale = p.scale * kLog2e;

@@ -143,7 +143,11 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(QkNormRopeBw
   for (int e = 0; e < 16; ++e) acc[e] = over_tokens<LPR>(acc[e]);
   if (lane < LPR) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) s_w[wave][(e < 8 ? m.c0 : m.c1 - 8) + e] = acc[e];
+    for (int e = 0; e < 16; ++e) {
+      float* dst = &s_w[wave][(e < 8 ? m.c0 : m.c1 - 8) + e];
+      lds_check(dst, 4);
+      *dst = acc[e];
+    }
   }
   __syncthreads();
   // the parts of an operand follow each other: q's, then k's

@@ -16,6 +16,8 @@ __device__ __forceinline__ void join_parts(const float* __restrict__ src, int64_
   constexpr int P = THREADS / 4;
   static_assert(THREADS >= 256 && P % 16 == 0, "256 threads for the second sum");
   __shared__ __align__(16) float s[P][20], s2[16][17];
+  lds_nan_fill(s, sizeof s);
+  lds_nan_fill(s2, sizeof s2);
   const int c = col + 4 * (threadIdx.x & 3), part = threadIdx.x >> 2;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < cols) {
@@ -25,13 +27,18 @@ __device__ __forceinline__ void join_parts(const float* __restrict__ src, int64_
       v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
     }
   }
+  lds_check(&s[part][4 * (threadIdx.x & 3)], 16);
   *reinterpret_cast<float4*>(&s[part][4 * (threadIdx.x & 3)]) = v;
   __syncthreads();
   const int k = threadIdx.x & 15, g = threadIdx.x >> 4;
   if (g < 16) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < P / 16; ++i) t += s[16 * i + g][k];
+    for (int i = 0; i < P / 16; ++i) {
+      lds_check(&s[16 * i + g][k], 4);
+      t += s[16 * i + g][k];
+    }
+    lds_check(&s2[g][k], 4);
     s2[g][k] = t;
   }
   __syncthreads();

@@ -92,6 +92,8 @@ __device__ __forceinline__ bool sum_again(float eps, float mean) {      // (mean
 template <typename TX, typename TR, int W, int CH, bool CODES>
 __global__ __launch_bounds__(kThreads) void add_norm_kernel(AddNormArgs p) {
   __shared__ float s_sum[2][4], s_max[4];
+  lds_nan_fill(s_sum, sizeof s_sum);
+  lds_nan_fill(s_max, sizeof s_max);
   const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x, wave = threadIdx.x >> 6;
   const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
   if (W == 1 && row >= p.rows) return;
@@ -143,6 +145,7 @@ __global__ __launch_bounds__(kThreads) void add_norm_kernel(AddNormArgs p) {
   auto over_row = [&](float (&s)[4]) {
     ss = wave_sum_f(ss);
     if constexpr (W == 4) {
+      lds_check(s + wave, 4);
       if ((threadIdx.x & 63) == 0) s[wave] = ss;
       __syncthreads();
       ss = (s[0] + s[1]) + (s[2] + s[3]);
@@ -187,6 +190,7 @@ __global__ __launch_bounds__(kThreads) void add_norm_kernel(AddNormArgs p) {
     if (!p.group) {
       top = wave_max(top);
       if constexpr (W == 4) {
+        lds_check(s_max + wave, 4);
         if ((threadIdx.x & 63) == 0) s_max[wave] = top;
         __syncthreads();
         top = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
@@ -222,6 +226,8 @@ template <typename TX, typename TR, int W, int CH>
 __global__ __launch_bounds__(kThreads) void add_norm_bwd_kernel(AddNormBwdArgs p, int blocks) {
   __shared__ float s_sum[2][4][2];
   __shared__ __align__(16) float s_w[W == 1 ? 4 * CH * 512 : 4];
+  lds_nan_fill(s_sum, sizeof s_sum);
+  lds_nan_fill(s_w, sizeof s_w);
   const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x, wave = threadIdx.x >> 6;
   const int chunks = p.C / 8;
   float acc[CH][8], w[CH][8];
@@ -269,6 +275,7 @@ __global__ __launch_bounds__(kThreads) void add_norm_bwd_kernel(AddNormBwdArgs p
       if constexpr (W == 4) {               // two sets in turn: one barrier to a sum
         float (*s)[2] = s_sum[turn];
         turn ^= 1;
+        lds_check(s + wave, 8);
         if ((threadIdx.x & 63) == 0) { s[wave][0] = ss; s[wave][1] = sg; }
         __syncthreads();
         ss = (s[0][0] + s[1][0]) + (s[2][0] + s[3][0]);
@@ -318,12 +325,16 @@ __global__ __launch_bounds__(kThreads) void add_norm_bwd_kernel(AddNormBwdArgs p
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; e += 4)
-        *reinterpret_cast<float4*>(s_w + (wave * CH + i) * 512 + 8 * t + e) =
-            make_float4(acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]);
+      for (int e = 0; e < 8; e += 4) {
+        float* dst = s_w + (wave * CH + i) * 512 + 8 * t + e;
+        lds_check(dst, 16);
+        *reinterpret_cast<float4*>(dst) = make_float4(acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]);
+      }
     __syncthreads();
-    for (int c = threadIdx.x; c < p.C; c += kThreads)
+    for (int c = threadIdx.x; c < p.C; c += kThreads) {
+      lds_check(s_w + 3 * CH * 512 + c, 4);
       to[c] = (s_w[c] + s_w[CH * 512 + c]) + (s_w[2 * CH * 512 + c] + s_w[3 * CH * 512 + c]);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {

@@ -235,6 +235,17 @@ def test_binding_rejects_host_tensors_and_what_does_not_fit():
         gdn.gdn_qk_norm_rope_backward(None, None)
 
 
+@pytest.mark.parametrize("source", ["norm_ops.hip", "join_parts.hpp", "attn_rope_backward.hip", "attn_backward.hip"])
+def test_debug_kernels_begin_with_nan_in_all_their_lds(source):
+    """Every shared array is filled in the debug library, where reads of what was not written show as NaN."""
+    text = open(os.path.join(CSRC, source)).read()
+    arrays = [n for d in re.findall(r"__shared__\s+([^;]+);", text) for n in re.findall(r"(\w+)\[", d.split("=")[0])]
+    arrays = [n for n in arrays if n.startswith("s")]
+    filled = re.findall(r"lds_nan_fill\((\w+), sizeof \1\);", text)
+    assert arrays and sorted(arrays) == sorted(filled)
+    assert len(re.findall(r"\blds_check\(", text)) >= len(set(arrays))
+
+
 def _run(tmp_path, name, sources):
     exe = str(tmp_path / name)
     cmd = ["g++", "-std=c++17", "-O1", "-g", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
