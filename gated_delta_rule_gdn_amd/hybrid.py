@@ -8,11 +8,13 @@ goes to that device's current stream, or to the one given.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
+from torch._C import _cuda_getCurrentRawStream
 
-from .attn import GdnAttnPrefillDesc, _empty, _native, _raw_stream
+from .attn import GdnAttnPrefillDesc, _native
 from .gdn import _DT, GDN_OK, GdnError, lib
 
 HYBRID_ABI_VERSION = 1
@@ -83,13 +85,25 @@ def _done(r, name):
     return r[1:]
 
 
-# The extension module allocates what is not given for the device's current stream; on another stream it is
-# allocated here first.
+# The extension module checks the tensors and allocates what is not given, for the current stream of their
+# device: a call on another stream is the same call with that one as the current stream.
 
 
-def _stats_words(q) -> int:
-    T, H, d = q.shape
-    return T * H * (2 + d // 4 if q.dtype == torch.bfloat16 else 2)
+def _current(t) -> int:
+    """The current stream's handle on the device of t (what is no device tensor is refused by the call)."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    return _cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+
+
+def _on(stream, t):
+    """With it the stream, or the one of this handle on the device of t, is the current one there."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return contextlib.nullcontext()       # (refused by the call)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    elif stream.device != t.device:
+        raise ValueError("stream is on another device than the tensors")
+    return torch.cuda.stream(stream)
 
 
 def gdn_attn_prefill_save(q, k, v, cu_seqlens=None, N=None, window: int = 0, scale=None, o=None,
@@ -102,10 +116,10 @@ def gdn_attn_prefill_save(q, k, v, cu_seqlens=None, N=None, window: int = 0, sca
     o is.
     """
     if stream is not None:
-        o = _empty(q.shape, q.dtype, q, stream) if o is None else o
-        stats = _empty((_stats_words(q),), torch.float32, q, stream) if stats is None else stats
+        with _on(stream, q):
+            return gdn_attn_prefill_save(q, k, v, cu_seqlens, N, window, scale, o, stats)
     return _done(_native.attn_prefill_save(_fn["gdn_attn_prefill_save"], q, k, v, cu_seqlens, N, window,
-                                           scale, o, stats, _raw_stream(stream, q)), "gdn_attn_prefill_save")
+                                           scale, o, stats, _current(q)), "gdn_attn_prefill_save")
 
 
 def gdn_attn_backward_workspace_size(q, k, N: int = 1, window: int = 0) -> int:
@@ -130,19 +144,16 @@ def gdn_attn_backward(q, k, v, o, d_o, stats, cu_seqlens=None, N=None, window: i
     type, that of q or float32).  `workspace` is a device uint8 tensor of at
     least gdn_attn_backward_workspace_size(...) bytes, allocated when not given.
     """
-    if grad_dtype is None:
-        grad_dtype = next((t.dtype for t in (dq, dk, dv) if t is not None), q.dtype)
-    if grad_dtype not in _DT:
-        raise ValueError("gradients must be float32 or bfloat16")
     if stream is not None:
-        dq, dk, dv = (_empty(x.shape, grad_dtype, q, stream) if t is None else t
-                      for t, x in ((dq, q), (dk, k), (dv, v)))
-        if workspace is None:
-            need = gdn_attn_backward_workspace_size(q, k, len(cu_seqlens) - 1 if cu_seqlens is not None else N or 1, window)
-            workspace = _empty((need,), torch.uint8, q, stream)
+        with _on(stream, q):
+            return gdn_attn_backward(q, k, v, o, d_o, stats, cu_seqlens, N, window, scale, dq, dk, dv, grad_dtype, workspace)
+    if grad_dtype is None:
+        grad_dtype = getattr(next((t for t in (dq, dk, dv) if t is not None), q), "dtype", None)
+    if grad_dtype is not None and grad_dtype not in _DT:      # (without one, what is no tensor is refused by the call)
+        raise ValueError("gradients must be float32 or bfloat16")
     return _done(_native.attn_backward(_fn["gdn_attn_backward"], _fn["gdn_attn_backward_workspace_size"],
                                        q, k, v, o, d_o, stats, cu_seqlens, N, window, scale, dq, dk, dv,
-                                       grad_dtype == torch.float32, workspace, _raw_stream(stream, q)),
+                                       grad_dtype == torch.float32, workspace, _current(q)),
                  "gdn_attn_backward")
 
 
@@ -175,16 +186,13 @@ def gdn_qk_norm_rope_backward(dq, dk, q_raw=None, k_raw=None, positions=None, in
     if one is None:
         raise ValueError("dq or dk must be given")
     if stream is not None:
-        dq_raw, dk_raw = (_empty(x.shape, x.dtype, x, stream) if t is None and x is not None else t
-                          for t, x in ((dq_raw, dq), (dk_raw, dk)))
-        dq_weight, dk_weight = (_empty(w.shape, torch.float32, one, stream) if t is None and w is not None else t
-                                for t, w in ((dq_weight, q_weight), (dk_weight, k_weight)))
-        if workspace is None:
-            workspace = _empty((gdn_qk_norm_rope_backward_workspace_size(dq, dk),), torch.uint8, one, stream)
+        with _on(stream, one):
+            return gdn_qk_norm_rope_backward(dq, dk, q_raw, k_raw, positions, inv_freq, q_weight, k_weight, interleaved,
+                                             rope_scale, eps, dq_raw, dk_raw, dq_weight, dk_weight, workspace)
     return _done(_native.qk_norm_rope_backward(
         _fn["gdn_qk_norm_rope_backward"], _fn["gdn_qk_norm_rope_backward_workspace_size"], dq, dk, q_raw, k_raw,
         positions, inv_freq, q_weight, k_weight, interleaved, rope_scale, eps, dq_raw, dk_raw, dq_weight,
-        dk_weight, workspace, _raw_stream(stream, one)), "gdn_qk_norm_rope_backward")
+        dk_weight, workspace, _current(one)), "gdn_qk_norm_rope_backward")
 
 
 def gdn_add_norm(x, res=None, weight=None, eps: float = 1e-6, group=None, res_out=None, y=None,
@@ -200,14 +208,10 @@ def gdn_add_norm(x, res=None, weight=None, eps: float = 1e-6, group=None, res_ou
     y may be a dense x.
     """
     if stream is not None:
-        if y is None:
-            y = _empty(x.shape, x.dtype if group is None else torch.float8_e4m3fn, x, stream)
-        if y_scale is None and group is not None:
-            y_scale = _empty((x.shape[0], x.shape[1] // group if group else 1), torch.float32, x, stream)
-        if res_out is None and res is not None:
-            res_out = _empty(res.shape, res.dtype, x, stream)
+        with _on(stream, x):
+            return gdn_add_norm(x, res, weight, eps, group, res_out, y, y_scale)
     return _done(_native.add_norm(_fn["gdn_add_norm"], x, res, weight, eps, group, res_out, y, y_scale,
-                                  _raw_stream(stream, x)), "gdn_add_norm")
+                                  _current(x)), "gdn_add_norm")
 
 
 def gdn_add_norm_backward_workspace_size(dy) -> int:
@@ -231,14 +235,8 @@ def gdn_add_norm_backward(dy, r, weight=None, d_res_out=None, eps: float = 1e-6,
     is allocated (d_weight only with a weight); dx may be dy, d_res may be d_res_out.
     """
     if stream is not None:
-        if d_res is None:
-            d_res = _empty(r.shape, r.dtype, dy, stream)
-        if d_weight is None and weight is not None:
-            d_weight = _empty(weight.shape, torch.float32, dy, stream)
-        if dx is None and dy.dtype != r.dtype:
-            dx = _empty(dy.shape, dy.dtype, dy, stream)
-        if workspace is None:
-            workspace = _empty((gdn_add_norm_backward_workspace_size(dy),), torch.uint8, dy, stream)
+        with _on(stream, dy):
+            return gdn_add_norm_backward(dy, r, weight, d_res_out, eps, dx, d_res, d_weight, workspace)
     return _done(_native.add_norm_backward(
         _fn["gdn_add_norm_backward"], _fn["gdn_add_norm_backward_workspace_size"], dy, r, weight, d_res_out, eps,
-        dx, d_res, d_weight, workspace, _raw_stream(stream, dy)), "gdn_add_norm_backward")
+        dx, d_res, d_weight, workspace, _current(dy)), "gdn_add_norm_backward")
