@@ -79,7 +79,8 @@ typedef struct gdn_qk_desc {
  * position up to +-2^53 and frequency up to 2^24, so far ones lose nothing;
  * frequencies scaled for long contexts come in through inv_freq and rope_scale.
  * The rest is fp32, rounded once at the end: x^2 is formed in it, so |x| < 2^60,
- * and where eps is 0 the mean of a row's squares must be a normal number.
+ * and eps plus the mean of a row's squares must be a normal number (2^-126 or
+ * more: a row of zeros needs such an eps).
  *
  *   q_raw     [rows, H_q, d] io_dtype, row stride ld_q (NULL when H_q == 0)
  *   k_raw     [rows, H_k, d] io_dtype, row stride ld_k (NULL when H_k == 0)
