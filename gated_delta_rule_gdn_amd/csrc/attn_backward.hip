@@ -20,14 +20,17 @@
 // dP^T = V dO^T for dq; S = Q K^T and dP = dO V^T for dk and dv), so p and ds are, as
 // they lie in the accumulators, the k-values of the second products.
 //
-// 14 d flops to a key that a query sees, against a few bytes: bound by the matrix cores,
-// and with them by power.  Both kernels of a call, bf16, 16 heads of 128: a document of
-// 16384 tokens over 2 key heads 3500 to 3600 us, 1070 to 1100 TFLOP/s (a plain product of
-// 8192 x 8192 x 8192 reaches 1212); 8 prompts of 4096 tokens over 16 key heads 1930 to 2010
-// us, 960 to 1000; 16 documents, 32768 tokens in all, a window of 2048 over 2 key heads 1390
-// to 1470 us.  fp32, 4096 tokens, 16 heads of 128: 2200 us, 109 TFLOP/s (a product: 154).
-// Short documents are three launches and the walks of the longest one's tiles (29 of 282
-// tokens on average, 6 heads of 64 over 3: 22 + 27 + 8 us).
+// 14 d flops to a key that a query sees, against a few bytes: bound by the matrix cores, at
+// the clock that power leaves them (1.7 to 1.9 GHz), and by the waits between products, in
+// which they are idle 41 to 51 % of the time.  Calls in a row, bf16, 16 heads of 128: a
+// document of 16384 tokens over 2 key heads 3570 to 3660 us, 1050 to 1080 TFLOP/s (a plain
+// product of 8192 x 8192 x 8192 reaches 1212); 8 prompts of 4096 tokens over 16 key heads
+// 1970 to 1990 us, 970; 16 documents, 32768 tokens in all, a window of 2048 over 2 key heads
+// 1210 to 1360 us by their lengths, 870 to 890.  Gradients in fp32 from bf16 rows: 2030 us
+// for the 8 prompts, the document as before.  fp32, 4096 tokens, 16 heads of 128: 2200 us,
+// 109 TFLOP/s (a product: 154).  Short documents are three launches and the walks of the
+// longest one's tiles (29 of 282 tokens on average, 6 heads of 64 over 3: 52 to 55 us, traced
+// 22 + 26 + 8).
 #include <cmath>
 
 #include "attn_shares.hpp"
@@ -612,7 +615,7 @@ __device__ __forceinline__ void rows_out(bf16* lds, const f32x16* acc, float f, 
 // Two workgroups to a CU hide each other's waits.  D is formed from outputs of 16 bits (see
 // low_bytes): from bf16 alone a gradient's error was 3.1e-3 of its norm instead of 2.7e-3 for
 // documents of 16 tokens.  3 products: 970 TFLOP/s for 8 prompts of 4096 tokens, 16 heads of
-// 128, 1120 for a document of 16384.
+// 128, 1080 to 1100 for a document of 16384.
 // SPLIT 2: 64 queries to a workgroup, each 32 of them to two waves that take 32 keys of a
 // tile each and add their sums at the end (see split_dq).
 template <int D, typename TG, int SPLIT>
@@ -878,11 +881,13 @@ __device__ __forceinline__ void keep_a(bf16x8& x) {
 // 192 registers.  What hides latencies instead is a pipeline by hand over blocks of 32
 // queries: the first products of the next block, with the weights of this one formed
 // between them, then this one's second products; every LDS read some products ahead of its
-// use; tiles three deep in LDS.  4 products: 870 TFLOP/s for 8 prompts of 4096 tokens, 16
-// heads of 128, 1050 for a document of 16384 tokens (two waves to a SIMD, as the compiler
-// schedules them, 640 and 690).  Of the 2.0 us that a step of 64 queries takes the products
-// alone are 1.3, at 1.7 GHz: power.  With the LDS reads, seven eighths of the weights or the
-// loads and barriers left out it takes 1.8, 1.8 and 1.7.
+// use; tiles in four buffers in LDS: the one in use, the next, whose first rows are read ahead
+// of it, and two on their way (the last of them into the buffer that the tile before this one
+// has left).  4 products: 850 to 890 TFLOP/s for 8 prompts of 4096 tokens, 16 heads of 128,
+// 1030 to 1060 for a document of 16384 tokens (two waves to a SIMD, as the compiler schedules
+// them, 640 and 690).  Of the 2.0 us that a step of 64 queries takes the products alone are
+// 1.3, at the 1.7 GHz that power leaves them.  With the LDS reads, seven eighths of the weights
+// or the loads and barriers left out it takes 1.8, 1.8 and 1.7.
 template <int D, typename TG>
 __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kernel(AttnBwdArgs p, uint32_t blocks, int workers) {
   constexpr int BK = 128, BQ = 64, KB = D / 16, MT = D / 32;
@@ -1132,8 +1137,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 2 : 1) void attn_dkv_bf16_kerne
     products_done<MT>(dk, dv);
     buf = nb;
   }
-  // Rows leave through LDS, so that a store covers whole rows.  The last two buffers but
-  // one are read by no wave any more: a quarter of them to a wave.
+  // Rows leave through LDS, so that a store covers whole rows.  Waves that are still at the last
+  // tile read its buffer (buf - 1) and, ahead of a tile that is none, the next (buf); the other two
+  // have been read before the last barrier: a quarter of them to a wave.
   bf16* mine = s_t[(buf + 1 + (wave >> 1)) % NB] + (wave & 1) * BQ * D;
   const int rows = L - u0 < 32 ? L - u0 : 32;
   if (w.slot < 0) {

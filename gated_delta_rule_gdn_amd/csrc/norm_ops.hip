@@ -8,9 +8,11 @@
 //
 // Both read their rows once, hold them in registers through the sums over a row and
 // write once, at a few flops per element: HBM-bound for many rows, launch latency
-// for few.  32768 rows of 2048 channels, bf16 with the residual in fp32: 143.6 us, 5.61 TB/s
-// (a copy of 1 GiB: 5.09), backward 194.0, 5.53; 8192 rows of 4096 to e4m3 44.7 us, 5.3.  One
-// row 2.5 us, 5.1 with its call.
+// for few.  32768 rows of 2048 channels, bf16 with the residual in fp32: 142.9 us, 5.64 TB/s
+// (a copy of 1 GiB: 5.09), backward 193.1, 5.56; 8192 rows of 4096 to e4m3 44.7 us, 5.3.  One
+// row 1.8 us, 5.1 to 5.9 with its call.  Backward of 4096 rows of 16384 channels: bf16 115 us,
+// 4.7 TB/s, with the residual in fp32 189, 5.7, all in fp32 277, 3.9: a thread's 64 channels take
+// all 512 registers there, and in fp32 82 more.
 //
 // A row is held by W waves (1 or 4) in CH chunks of 8 channels to a lane, chunk
 // i of thread t being number t + 64 W i of the row, so that every access is
@@ -24,9 +26,10 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-// Waves of a row (us, 1 / 4, 16384 rows, bf16 with the residual in fp32: 1536 channels 49.8 /
-// 50.8 and backward 58 / 62; 2048 channels 75.7 / 72.8, 79.8 / 76.0; 2560 95.1 / 92.1, 109 /
-// 95; 4096 147 / 145, 176 / 155).
+// Waves of a row (us, 1 / 4, 16384 rows, bf16 with the residual in fp32: 1024 channels 33.6 /
+// 34.9 and backward 37.2 / 49.2; 1536 50.7 / 51.4, 55.4 / 58.0; 2048 75.6 / 72.9, 79.9 / 76.1;
+// 2560 94.4 / 92.0, 103 / 97; 4096 149 / 146, 189 / 156.  With the residual in bf16: 32768 rows of
+// 2048 93.0 / 92.9, 77 / 94; 16384 of 4096 100 / 94, 98 / 76).
 int waves_of(int C) { return C <= 1536 ? 1 : 4; }
 
 __device__ __forceinline__ float wave_sum_f(float s) {
@@ -213,8 +216,12 @@ __global__ __launch_bounds__(kThreads) void add_norm_kernel(AddNormArgs p) {
 // ---------------------------------------------------------------------------
 // Backward.  Workgroups loop over rows and keep their rows' part of d_weight in
 // registers; it goes to the workspace once for each workgroup, and a second kernel
-// adds the parts in a fixed order.  (256 or 768 workgroups measure 2 to 5 % worse: with two
-// to a CU loads and stores of different rows overlap; more leave more parts.)
+// adds the parts in a fixed order.  With two workgroups to a CU loads and stores of different
+// rows overlap; more leave more parts (us, 256 / 512 / 768 workgroups, bf16 with the residual in
+// fp32: 16384 rows of 1536 channels 55.1 / 55.5 / 63.5, of 2048 103 / 76 / 83, of 2560 118 / 97 /
+// 103, of 4096 150 / 156 / 157).  From 4097 channels on with the residual in fp32, and from 8193 on
+// in any type, registers leave room for one to a CU (8192 rows of 8192 149 / 152 / 158, 4096 of
+// 16384 180 / 189 / 200, all in fp32 253 / 278 / 280).
 // ---------------------------------------------------------------------------
 constexpr int64_t kBwdBlocks = 512;
 int64_t bwd_blocks(int64_t rows, int C) {
