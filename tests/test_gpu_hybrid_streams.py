@@ -93,3 +93,35 @@ def test_default_stream_given_as_a_handle():
         got = gdn.gdn_add_norm(x, x, w, stream=0)
     torch.cuda.default_stream().synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+
+
+def test_every_argument_goes_with_a_stream_where_it_goes_without():
+    """None left at its default, and outputs and workspaces given."""
+    announce("hybrid, all arguments with a stream")
+    (_, (q, k, v, g)), s = th.case(40, 4, 2, 64, BF, 3), torch.cuda.Stream()
+    cu, pos, freq = torch.tensor([0, 15, 40]).cuda(), torch.arange(7, 47).cuda(), inv_freq(32).cuda()
+    w = [1 + 0.1 * torch.randn(64, device="cuda") for _ in range(2)]
+    x, res, wide = torch.randn(40, 128, device="cuda").to(BF), torch.randn(40, 128, device="cuda"), torch.rand(128, device="cuda")
+    empty = lambda t, dtype=None: torch.empty(t.shape, dtype=dtype or t.dtype, device="cuda")  # noqa: E731
+    bytes_ = lambda n: torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")  # noqa: E731
+    F = torch.float32
+
+    def run(**kw):
+        o, stats = gdn.gdn_attn_prefill_save(q, k, v, cu, 2, 9, 0.2, empty(q), torch.empty(40 * 4 * 18, device="cuda"), **kw)
+        grads = gdn.gdn_attn_backward(q, k, v, o, g, stats, cu, 2, 9, 0.2, empty(q, F), empty(k, F), empty(v, F), F,
+                                      bytes_(gdn.gdn_attn_backward_workspace_size(q, k, 2, 9)), **kw)
+        rope = gdn.gdn_qk_norm_rope_backward(grads[0], grads[1], q, k, pos, freq, w[0], w[1], True, 1.5, 1e-3, empty(q, F),
+                                             empty(k, F), empty(w[0]), empty(w[1]),
+                                             bytes_(gdn.gdn_qk_norm_rope_backward_workspace_size(grads[0], grads[1])), **kw)
+        codes = gdn.gdn_add_norm(x, res, wide, 1e-3, 64, empty(res), empty(x, torch.float8_e4m3fn),
+                                 torch.empty(40, 2, device="cuda"), **kw)
+        back = gdn.gdn_add_norm_backward(x, codes[2], wide, res, 1e-3, empty(x), empty(res), empty(wide),
+                                         bytes_(gdn.gdn_add_norm_backward_workspace_size(x)), **kw)
+        return [o, stats, *grads, *rope, *codes, *back]
+
+    want = run()
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        got = run(stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)) for a, b in zip(got, want))
